@@ -69,7 +69,8 @@ typedef enum spec_status {
     SPEC_ERR_TIMEOUT = 6       /* reserved: a bounded device wait gave up */
 } spec_status;
 
-typedef enum spec_dtype { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype;
+/* SPEC_F16 is a type of the paged cache (spec_cache.h) alone: the sampler takes fp32 and bf16. */
+typedef enum spec_dtype { SPEC_F32 = 0, SPEC_BF16 = 1, SPEC_F16 = 2 } spec_dtype;
 
 /* Largest vocabulary a call accepts. */
 #define SPEC_REJECT_MAX_VOCAB 1048576

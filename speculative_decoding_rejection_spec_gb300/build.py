@@ -14,7 +14,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SOURCES = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-HEADERS = [os.path.join(ROOT, "include", "spec_reject.h")] + sorted(glob.glob(os.path.join(CSRC, "*.cuh")))
+HEADERS = sorted(glob.glob(os.path.join(ROOT, "include", "*.h"))) + sorted(glob.glob(os.path.join(CSRC, "*.cuh")))
 LIBRARY = os.path.join(HERE, "libspecreject.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]
