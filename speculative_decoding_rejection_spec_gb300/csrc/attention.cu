@@ -1,8 +1,30 @@
 // attention.cu -- attention of a step's new tokens over the paged cache (sm_103a).
 //
-// A warp per (new token, query head) walks the visible positions with a running maximum and sum.
+// For request r, kv head h and a block of up to 256 query rows (row m = new token m / G, query head
+// h * G + m % G), over tiles of 128 keys:
+//   S = Q K^T (tcgen05, operands in shared memory), P = exp2(S * scale * log2(e) - M) with the
+//   running maximum M of each row, O = O + P V (P read from tensor memory), l = l + sum P.
+//
+// One block per SM, warps by role:
+//   warps 0-3, 4-7  two softmax groups, a thread per row: S from tensor memory to registers, mask,
+//                   maximum, exponentials, P back over S.  M only moves when a row's maximum has
+//                   grown by more than 2^8 since (P stays below 2^8, exact in its sum's fp32), so
+//                   the accumulator in tensor memory is rarely rescaled.
+//   warp 8          loads tiles of K and V, page by page, through TMA into a ring of slots
+//   warp 9          issues the matrix products (one lane)
+// A block of more than 128 rows ("wide") gives each group 128 of them and both use every tile: the
+// products of one group run while the other computes its exponentials.  A block of at most 128 rows
+// ("narrow": decoding and most verify steps) gives both groups the same rows and every other tile,
+// merged at the end; the tiles are padded to 128 rows, which costs nothing while memory bounds the
+// call (128 keys of K and V at head_dim 128 are 64 KB, 1.45 us of one SM's share of HBM bandwidth;
+// their two products take 0.55 us).
+//
+// The work of a call is the list of all (request, head, row block, key tile), cut into equal
+// contiguous shares, one per block, whatever the lengths.  A (request, head, row block) that is cut
+// leaves partial sums (O, M, l), which a second kernel joins.
 #include <algorithm>
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -11,24 +33,36 @@
 namespace specrej {
 namespace {
 
+constexpr int kTile = 128;          // keys per tile, and rows per softmax group
+constexpr int kBlockRows = 256;     // query rows of a (request, head, row block)
+constexpr int kSoftmaxWarps = 8, kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kAttnThreads = 320;
+constexpr int kMaxGrid = 160;       // blocks a call may use (SMs of the device, 152 on GB300)
+constexpr int kMinTiles = 2;        // least tiles of a block's share
+constexpr float kLazy = 8.0f;       // log2 of the growth that moves a row's maximum
+constexpr int kTmemColumns = 512;   // two groups: 128 of S (P over it), up to 128 of O
+
+struct Partial {  // of the row block that starts in a block's share and goes on behind it
+    int32_t r, h, b, rows;  // rows 0: none
+    int32_t last;           // the last block that works on it
+    int32_t pad[3];
+};
+
 struct AttentionParams {
     const char *q;
     char *out;
     float *lse;
     int64_t q_token, q_head, out_token, out_head;  // elements
-    int32_t heads, group, B;
+    int32_t heads, group, B, box;
     int64_t N;
     const int32_t *cu, *parent;
-    float scale;
-    int64_t layer_offset;
+    float scale_log2;
+    // workspace
+    Partial *partial;   // [grid]
+    float2 *part_ml;    // [grid * 2 * max_rows] M, l
+    float *part_o;      // [grid * 2 * max_rows * DP]
+    int32_t max_rows;
 };
-
-template <int DT> __device__ __forceinline__ float2 to_float2(uint32_t x)
-{
-    if (DT == SPEC_BF16)
-        return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
-    return __half22float2(*reinterpret_cast<const __half2 *>(&x));
-}
 
 template <int DT> __device__ __forceinline__ uint32_t from_float2(float a, float b)
 {
@@ -40,91 +74,972 @@ template <int DT> __device__ __forceinline__ uint32_t from_float2(float a, float
     return *reinterpret_cast<const uint32_t *>(&y);
 }
 
-template <int DT> __global__ void __launch_bounds__(256) attention_kernel(CacheView c, AttentionParams p)
+// ---------------------------------------------------------------------------------------
+// tcgen05, TMA and barriers
+// ---------------------------------------------------------------------------------------
+
+__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 32 columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, float *x)
 {
-    const int lane = threadIdx.x & 31;
+    uint32_t *r = reinterpret_cast<uint32_t *>(x);
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+                   "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+                   "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+                   "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const float *x)
+{
+    const uint32_t *r = reinterpret_cast<const uint32_t *>(x);
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+                 "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+                 "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+                 "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+                 "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+                 "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+                 : "memory");
+}
+
+// Shared-memory matrix descriptor, 128-byte swizzle.  Rows of 128 bytes in groups of 8 (1024 bytes
+// apart: the stride byte offset); `leading` is the distance between 64-element chunks of an operand
+// whose contiguous dimension is not the summed one (V), and unused (1) for Q and K.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t leading)
+{
+    return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(leading >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+// Instruction descriptor: fp32 accumulator, 16-bit A and B of one type, M = 128 rows, N columns;
+// b_mn: B's contiguous dimension is N.
+template <int DT> __device__ __forceinline__ constexpr uint32_t mma_desc(int n, bool b_mn)
+{
+    return 1u << 4 | (DT == SPEC_BF16 ? 1u : 0u) << 7 | (DT == SPEC_BF16 ? 1u : 0u) << 10 | (b_mn ? 1u : 0u) << 16 |
+           (uint32_t)(n >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+                 : "memory");
+}
+
+// Arrives on the barrier when every product this thread has issued is done.
+__device__ __forceinline__ void mma_commit(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+__device__ __forceinline__ void fence_proxy_async_shared()
+{
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, int x, int token, int head, int page,
+                                        uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+                 "l"(map), "r"(x), "r"(token), "r"(head), "r"(page), "r"(smem_addr(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ uint64_t global_ns()
+{
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+
+// What a block keeps behind the operand tiles.
+template <int SLOTS> struct alignas(16) AttnShared {
+    // per group: (M, l) of its rows at the end of a narrow row block, or a tree's parents at its start
+    union {
+        float2 ml[kTile];
+        int32_t parent[kMaxTree];
+        int64_t sums[kAttnThreads / 32];
+    } group[2];
+    uint64_t full[SLOTS], empty[SLOTS];  // a slot's tile has landed / has been used
+    uint64_t s_full[2], p_full[2];       // a group's S is there (or its last O) / its P is there
+    uint64_t q_full, q_free, done;
+    int64_t base;                        // work before request r
+    int32_t r;                           // first request of this block's share
+    uint32_t tmem;
+    volatile int32_t gave_up;
+};
+
+// Waits for a barrier's phase.  A wait of two seconds (or another one's) gives up: the roles then
+// run through their loops without waiting, issue nothing more and leave together.
+__device__ __forceinline__ void attn_wait(uint64_t *bar, uint32_t parity, volatile int32_t *gave_up, int32_t *error)
+{
+    if (mbar_try_wait(bar, parity))
+        return;
+    const uint64_t start = global_ns();
+    for (uint32_t i = 0; i < kWaitLimit; ++i) {
+        if (mbar_try_wait(bar, parity) || *gave_up)
+            return;
+        if (i % 64 == 63 && global_ns() - start > 2000000000ull)
+            break;
+    }
+    *gave_up = 1;
+    atomicOr(error, SPEC_DEVERR_TIMEOUT);
+}
+
+// ---------------------------------------------------------------------------------------
+// The list of work
+// ---------------------------------------------------------------------------------------
+
+struct Request {
+    int n, len, rows, tiles;  // new tokens, committed tokens, query rows, tiles of all its row blocks (one head)
+};
+
+// Tiles of row block b: the keys up to the last row's own.
+__device__ __forceinline__ int block_keys(const Request &q, int group, int b)
+{
+    const int end = min((b + 1) * kBlockRows, q.rows);
+    return q.len + (end - 1) / group + 1;
+}
+
+__device__ __forceinline__ int block_tiles(const Request &q, int group, int b)
+{
+    return (block_keys(q, group, b) + kTile - 1) / kTile;
+}
+
+// The request's sizes; tiles = 0 when there is nothing to do, or an error, which is recorded on demand.
+__device__ __forceinline__ Request request_of(const CacheView &c, const AttentionParams &p, int r, bool report)
+{
+    Request q;
+    q.n = p.cu[r + 1] - p.cu[r];
+    q.len = c.lens[r];
+    q.rows = q.n * p.group;
+    q.tiles = 0;
+    if (q.n <= 0)
+        return q;
+    if (q.len < 0 || (int64_t)q.len + q.n > (int64_t)c.max_pages * c.page_size || (p.parent && q.n > kMaxTree)) {
+        if (report)
+            cache_error(c.error, p.parent && q.n > kMaxTree ? SPEC_DEVERR_TREE : SPEC_DEVERR_LENGTH, r);
+        return q;
+    }
+    for (int b = 0; b * kBlockRows < q.rows; ++b)
+        q.tiles += block_tiles(q, p.group, b);
+    return q;
+}
+
+// Tiles of a block's share: [begin(x), begin(x + 1)).
+struct Shares {
+    int64_t total;
+    int blocks;
+    __device__ __forceinline__ int64_t begin(int x) const { return total * x / blocks; }
+    // the block whose share holds tile t
+    __device__ __forceinline__ int owner(int64_t t) const { return (int)(((t + 1) * blocks - 1) / total); }
+};
+
+// Walks a block's share, one (request, head, row block) at a time.  Every role walks for itself; the
+// calls are made by whole warps.
+struct Walk {
+    Request q;
+    int r, h, b;
+    int tiles;        // of this row block
+    int t0, t1;       // those in the share
+    int64_t pos, end; // place in the list
+
+    __device__ __forceinline__ void start(const CacheView &c, const AttentionParams &p, const Shares &s, int first,
+                                          int64_t base)
+    {
+        pos = s.begin(blockIdx.x);
+        end = s.begin(blockIdx.x + 1);
+        r = first;
+        q = request_of(c, p, r, false);
+        int64_t at = pos - base;
+        h = (int)(at / q.tiles);
+        at %= q.tiles;
+        for (b = 0; at >= block_tiles(q, p.group, b); ++b)
+            at -= block_tiles(q, p.group, b);
+        here(p, (int)at);
+    }
+    __device__ __forceinline__ void here(const AttentionParams &p, int from)
+    {
+        tiles = block_tiles(q, p.group, b);
+        t0 = from;
+        t1 = (int)min((int64_t)tiles, from + (end - pos));
+    }
+    // to the next row block; false at the share's end
+    __device__ __forceinline__ bool next(const CacheView &c, const AttentionParams &p)
+    {
+        pos += t1 - t0;
+        if (pos >= end)
+            return false;
+        if (++b * kBlockRows >= q.rows) {
+            b = 0;
+            if (++h == c.heads) {
+                h = 0;
+                const int lane = threadIdx.x & 31;
+                for (++r;; r += 32) {
+                    const bool some = r + lane < p.B && request_of(c, p, r + lane, false).tiles > 0;
+                    const unsigned any = __ballot_sync(kFull, some);
+                    if (any) {
+                        r += __ffs(any) - 1;
+                        break;
+                    }
+                    if (r >= p.B)
+                        return false;  // cannot be: the share ends before
+                }
+                q = request_of(c, p, r, false);
+            }
+        }
+        here(p, 0);
+        return true;
+    }
+    __device__ __forceinline__ int rows() const { return min(kBlockRows, q.rows - b * kBlockRows); }
+    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
+};
+
+// ---------------------------------------------------------------------------------------
+// The kernel
+// ---------------------------------------------------------------------------------------
+
+template <int DP> struct AttnSizes {
+    static constexpr int kSlotBytes = kTile * DP * 2;     // a tile of K or V; a group's Q
+    static constexpr int kSlots = (224 * 1024 - 2 * kSlotBytes) / kSlotBytes;  // 5 of 32 KB, 12 of 16 KB
+    static constexpr int kChunk = kTile * 128;            // 64 elements of every row of a tile
+    using Shared = AttnShared<kSlots>;
+    static constexpr int kBytes = (2 + kSlots) * kSlotBytes + (int)sizeof(Shared);
+};
+static_assert(AttnSizes<128>::kBytes <= 227 * 1024 && AttnSizes<64>::kBytes <= 227 * 1024, "shared memory of one SM");
+
+// Which of the 32 columns from `column` on row i sees: of the chain, or by the tree's bits.
+__device__ __forceinline__ uint32_t low_bits(int k) { return k <= 0 ? 0u : k >= 32 ? ~0u : (1u << k) - 1; }
+
+__device__ __forceinline__ uint32_t tree_columns(const uint32_t *bits, int len, int column)
+{
+    const int o = column - len;  // node of the first column
+    uint32_t lo = 0, hi = 0;
+#pragma unroll
+    for (int j = 0; j < kMaxTree / 32; ++j) {
+        lo = o >= 0 && o / 32 == j ? bits[j] : lo;
+        hi = o >= 0 && o / 32 + 1 == j ? bits[j] : hi;
+    }
+    if (o >= 0)
+        return __funnelshift_r(lo, hi, o & 31);
+    return low_bits(-o) | (o > -32 ? bits[0] << -o : 0u);
+}
+
+template <int DT, int DP>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, CacheView c,
+                     AttentionParams p)
+{
+    using Z = AttnSizes<DP>;
+    constexpr int SLOTS = Z::kSlots;
+    extern __shared__ __align__(1024) char smem[];
+    char *const qtile = smem, *const ring = smem + 2 * Z::kSlotBytes;
+    auto &S = *reinterpret_cast<typename Z::Shared *>(smem + (2 + SLOTS) * Z::kSlotBytes);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    // The whole list's length, and this block's place in it.
     bool bad = false;
-    for (int r = threadIdx.x; r <= p.B; r += blockDim.x) {
+    for (int r = tid; r <= p.B; r += kAttnThreads) {
         const int32_t x = p.cu[r];
         bad |= (r == 0 ? x != 0 : p.cu[r - 1] > x) || x > p.N;
     }
-    if (__syncthreads_or(bad)) {
-        if (blockIdx.x == 0 && threadIdx.x == 0)
+    bad = __syncthreads_or(bad);
+    Shares shares{0, 1};
+    if (bad) {
+        if (blockIdx.x == 0 && tid == 0)
             cache_error(c.error, SPEC_DEVERR_LAYOUT, -1);
-        return;
-    }
-    const int64_t w = (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
-    const int64_t t = w / p.heads;
-    const int h = (int)(w % p.heads);
-    if (t >= p.cu[p.B])
-        return;
-    const int r = warp_find_request(p.cu, p.B, t, lane);
-    const int first = p.cu[r], n = p.cu[r + 1] - first, i = (int)(t - first);
-    const int len = c.lens[r];
-    if (len < 0 || (int64_t)len + n > (int64_t)c.max_pages * c.page_size || (p.parent && n > kMaxTree)) {
-        if (lane == 0)
-            cache_error(c.error, p.parent && n > kMaxTree ? SPEC_DEVERR_TREE : SPEC_DEVERR_LENGTH, r);
-        return;
-    }
-    uint32_t seen[kMaxTree / 32] = {};
-    if (p.parent)
-        for (int at = i; at >= 0;) {
+    } else {
+        for (int pass = 0; pass < 2; ++pass) {
+            int64_t before = 0;
+            for (int r0 = 0; r0 < p.B; r0 += kAttnThreads) {
+                const int r = r0 + tid;
+                int64_t mine = 0;
+                if (r < p.B)
+                    mine = (int64_t)request_of(c, p, r, pass == 0 && blockIdx.x == 0).tiles * c.heads;
+                int64_t incl = mine;
 #pragma unroll
-            for (int j = 0; j < kMaxTree / 32; ++j)
-                seen[j] |= at / 32 == j ? 1u << at % 32 : 0;
-            const int up = p.parent[first + at];
-            if (at == 0 ? up != -1 : up < 0 || up >= at) {
-                if (lane == 0)
-                    cache_error(c.error, SPEC_DEVERR_TREE, r);
-                break;
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int64_t y = __shfl_up_sync(kFull, incl, d);
+                    incl += lane >= d ? y : 0;
+                }
+                __syncthreads();
+                if (lane == 31)
+                    S.group[0].sums[warp] = incl;
+                __syncthreads();
+                int64_t all = 0, lower = 0;
+#pragma unroll
+                for (int i = 0; i < kAttnThreads / 32; ++i) {
+                    lower += i < warp ? S.group[0].sums[i] : 0;
+                    all += S.group[0].sums[i];
+                }
+                if (pass == 1) {
+                    const int64_t at = before + lower + incl - mine, want = shares.begin(blockIdx.x);
+                    if (mine > 0 && at <= want && want < at + mine) {
+                        S.r = r;
+                        S.base = at;
+                    }
+                }
+                before += all;
             }
-            at = up;
+            shares.total = before;
+            shares.blocks = (int)max((int64_t)1, min((int64_t)gridDim.x, (before + kMinTiles - 1) / kMinTiles));
+            if (blockIdx.x >= shares.blocks || before == 0)
+                break;
         }
-    const int e = lane * 4;
-    const bool on = e < c.dim;
-    float q[4] = {}, acc[4] = {}, m = -INFINITY, l = 0;
-    if (on) {
-        const uint2 x = *reinterpret_cast<const uint2 *>(p.q + 2 * (t * p.q_token + h * p.q_head + e));
-        const float2 a = to_float2<DT>(x.x), b = to_float2<DT>(x.y);
-        q[0] = a.x, q[1] = a.y, q[2] = b.x, q[3] = b.y;
     }
-    const int64_t base = p.layer_offset + h / p.group * c.head_stride + e;
-    for (int pos = 0; pos <= len + i; ++pos) {
-        if (p.parent && pos >= len) {
-            const int j = pos - len;
-            uint32_t word = 0;
-#pragma unroll
-            for (int x = 0; x < kMaxTree / 32; ++x)
-                word = j / 32 == x ? seen[x] : word;
-            if (!(word >> (j % 32) & 1))
-                continue;
+    if (tid == 0)
+        p.partial[blockIdx.x].rows = 0;
+    if (shares.total == 0 || blockIdx.x >= shares.blocks)
+        return;
+
+    if (tid == 0) {
+        for (int i = 0; i < SLOTS; ++i) {
+            mbar_init(&S.full[i], 1);
+            mbar_init(&S.empty[i], 1);
         }
-        const int page = c.table[r * c.table_stride + pos / c.page_size];
-        const bool there = page >= 0 && page < c.num_pages;
-        if (!there && lane == 0)
-            cache_error(c.error, SPEC_DEVERR_PAGE, r);
-        const int64_t at = 2 * (base + page * c.page_stride + pos % c.page_size * c.token_stride);
-        float kx[4] = {}, vx[4] = {};
-        if (on && there) {
-            const uint2 x = *reinterpret_cast<const uint2 *>(c.k + at), y = *reinterpret_cast<const uint2 *>(c.v + at);
-            const float2 a = to_float2<DT>(x.x), b = to_float2<DT>(x.y), d = to_float2<DT>(y.x), f = to_float2<DT>(y.y);
-            kx[0] = a.x, kx[1] = a.y, kx[2] = b.x, kx[3] = b.y;
-            vx[0] = d.x, vx[1] = d.y, vx[2] = f.x, vx[3] = f.y;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&S.s_full[i], 1);
+            mbar_init(&S.p_full[i], 4);
         }
-        const float s = warp_sum(q[0] * kx[0] + q[1] * kx[1] + q[2] * kx[2] + q[3] * kx[3]) * p.scale;
-        const float mx = fmaxf(m, s), f = expf(m - mx), g = expf(s - mx);
-        l = l * f + g;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            acc[j] = acc[j] * f + g * vx[j];
-        m = mx;
+        mbar_init(&S.q_full, kSoftmaxWarps);
+        mbar_init(&S.q_free, 1);
+        mbar_init(&S.done, 1);
+        S.gave_up = 0;
+        mbar_fence_init();
     }
-    if (on) {
-        const uint2 x = make_uint2(from_float2<DT>(acc[0] / l, acc[1] / l), from_float2<DT>(acc[2] / l, acc[3] / l));
-        *reinterpret_cast<uint2 *>(p.out + 2 * (t * p.out_token + h * p.out_head + e)) = x;
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&S.tmem)),
+                     "r"(kTmemColumns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = S.tmem;
+    auto wait = [&](uint64_t *bar, uint32_t parity) { attn_wait(bar, parity, &S.gave_up, c.error); };
+
+    Walk w;
+    w.start(c, p, shares, S.r, S.base);
+
+    if (warp == kLoadWarp) {
+        // Slot order: K of tile 0, then K of tile t + 1 and V of tile t, as the products use them.
+        const int pieces = kTile / p.box;
+        uint32_t slot = 0, turn = 0;  // turn: parity of the slots' next use
+        bool first_turn = true;
+        do {
+            const int keys = block_keys(w.q, p.group, w.b);
+            const int32_t *row = c.table + w.r * c.table_stride;
+            // the pages of tile t, a piece per lane
+            auto lookup = [&](int t, int &page, int &token) {
+                const int at = t * kTile + lane * p.box;
+                page = -1;
+                token = 0;
+                if (t < w.t1 && lane < pieces && at < keys) {
+                    page = row[at / c.page_size];
+                    token = at % c.page_size;
+                    if (page < 0 || page >= c.num_pages) {
+                        cache_error(c.error, SPEC_DEVERR_PAGE, w.r);
+                        page = c.num_pages;  // outside the tensor: reads as zeros
+                    }
+                }
+            };
+            auto load = [&](const CUtensorMap *map, int page, int token) {
+                if (!first_turn)
+                    wait(&S.empty[slot], turn ^ 1);
+                if (!S.gave_up) {
+                    const unsigned there = __ballot_sync(kFull, page >= 0);
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(&S.full[slot], __popc(there) * p.box * 128 * (DP / 64));
+                    __syncwarp();
+                    if (page >= 0) {
+                        const uint32_t dst = smem_addr(ring + slot * Z::kSlotBytes) + lane * p.box * 128;
+#pragma unroll
+                        for (int i = 0; i < DP / 64; ++i)
+                            tma_box(dst + i * Z::kChunk, map, i * 64, token, w.h, page, &S.full[slot]);
+                    }
+                }
+                __syncwarp();
+                if (++slot == SLOTS) {
+                    slot = 0;
+                    turn ^= 1;
+                    first_turn = false;
+                }
+            };
+            int page, token, next_page, next_token;
+            lookup(w.t0, page, token);
+            load(&kmap, page, token);
+            for (int t = w.t0; t < w.t1; ++t) {
+                lookup(t + 1, next_page, next_token);
+                if (t + 1 < w.t1)
+                    load(&kmap, next_page, next_token);
+                load(&vmap, page, token);
+                page = next_page;
+                token = next_token;
+            }
+        } while (w.next(c, p));
+    } else if (warp == kMmaWarp) {
+        uint32_t slot = 0, turn = 0, q_turn = 0, p_turn[2] = {0, 0};
+        auto take = [&]() {  // the next slot, landed
+            wait(&S.full[slot], turn);
+            const uint32_t s = slot;
+            if (++slot == SLOTS) {
+                slot = 0;
+                turn ^= 1;
+            }
+            return s;
+        };
+        auto scores = [&](int g, uint32_t kslot, int qslot) {
+            const uint32_t a = smem_addr(qtile + qslot * Z::kSlotBytes), b = smem_addr(ring + kslot * Z::kSlotBytes);
+#pragma unroll
+            for (int i = 0; i < DP / 16; ++i) {
+                const uint32_t o = i / 4 * Z::kChunk + i % 4 * 32;
+                mma_ss(tmem + g * 256, smem_desc(a + o, 16), smem_desc(b + o, 16), mma_desc<DT>(kTile, false), i > 0);
+            }
+        };
+        auto outputs = [&](int g, uint32_t vslot, bool add) {
+            const uint32_t b = smem_addr(ring + vslot * Z::kSlotBytes);
+#pragma unroll
+            for (int i = 0; i < kTile / 16; ++i)
+                mma_ts(tmem + g * 256 + kTile, tmem + g * 256 + i * 8, smem_desc(b + i * 2048, Z::kChunk),
+                       mma_desc<DT>(DP, true), add || i > 0);
+        };
+        auto p_ready = [&](int g) {
+            wait(&S.p_full[g], p_turn[g]);
+            p_turn[g] ^= 1;
+            tmem_fence_after();
+        };
+        // Rows of V behind the last key: whatever the page (or the slot before) holds there, a weight
+        // of zero must meet a finite value.
+        auto clear_tail = [&](uint32_t vslot, int t, int keys) {
+            const int from = keys - t * kTile;
+            if (from >= kTile)
+                return;
+            char *base = ring + vslot * Z::kSlotBytes;
+            for (int i = from * 8 + lane; i < kTile * 8; i += 32)
+#pragma unroll
+                for (int j = 0; j < DP / 64; ++j)
+                    *reinterpret_cast<uint4 *>(base + j * Z::kChunk + i * 16) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_shared();
+            __syncwarp();
+        };
+        do {
+            const int keys = block_keys(w.q, p.group, w.b), nt = w.t1 - w.t0;
+            const bool wide = w.rows() > kTile;
+            wait(&S.q_full, q_turn);
+            q_turn ^= 1;
+            tmem_fence_after();
+            for (int t = 0; t <= nt; ++t) {
+                uint32_t kslot = 0, vslot = 0;
+                if (t < nt)
+                    kslot = take();
+                if (!wide && t < nt) {
+                    if (lane == 0 && !S.gave_up) {
+                        scores(t & 1, kslot, 0);
+                        mma_commit(&S.s_full[t & 1]);
+                        mma_commit(&S.empty[kslot]);
+                    }
+                    __syncwarp();
+                }
+                if (t > 0) {
+                    vslot = take();
+                    clear_tail(vslot, w.t0 + t - 1, keys);
+                }
+                if (!wide && t > 0) {
+                    const int u = t - 1, g = u & 1;
+                    p_ready(g);
+                    if (lane == 0 && !S.gave_up) {
+                        outputs(g, vslot, u >= 2);
+                        mma_commit(&S.empty[vslot]);
+                        if (u + 2 >= nt)
+                            mma_commit(&S.s_full[g]);
+                    }
+                    __syncwarp();
+                }
+                if (wide) {
+                    for (int g = 0; g < 2; ++g) {
+                        if (t > 0)
+                            p_ready(g);
+                        if (lane == 0 && !S.gave_up) {
+                            if (t > 0)
+                                outputs(g, vslot, t > 1);
+                            if (t < nt)
+                                scores(g, kslot, g);
+                            mma_commit(&S.s_full[g]);
+                        }
+                        __syncwarp();
+                    }
+                    if (lane == 0 && !S.gave_up) {
+                        if (t > 0)
+                            mma_commit(&S.empty[vslot]);
+                        if (t < nt)
+                            mma_commit(&S.empty[kslot]);
+                    }
+                    __syncwarp();
+                }
+                if (t == nt - 1 && lane == 0 && !S.gave_up)
+                    mma_commit(&S.q_free);
+                __syncwarp();
+            }
+        } while (w.next(c, p));
+        // every product is done before the block gives its memory back
+        if (lane == 0) {
+            mma_commit(&S.done);
+            for (uint32_t i = 0; i < kWaitLimit && !mbar_try_wait(&S.done, 0); ++i) {
+            }
+        }
+        __syncwarp();
+    } else {
+        const int g = warp >> 2, row = tid & (kTile - 1), sub = warp & 3;
+        const uint32_t lanes = (uint32_t)sub * 32 << 16;
+        const uint32_t s_addr = tmem + g * 256 + lanes;
+        uint32_t s_turn = 0, free_turn = 0;
+        bool first = true;
+        do {
+            const int rows = w.rows(), nt = w.t1 - w.t0;
+            const bool wide = rows > kTile;
+            const int m0 = wide ? g * kTile : 0;             // the group's first row in the block
+            const int mine = min(kTile, rows - m0);          // its rows
+            const bool warp_on = sub * 32 < mine, on = row < mine;
+            const int m = w.b * kBlockRows + m0 + row;       // row of the request
+            const int token = m / p.group, head = w.h * p.group + m % p.group;
+            const int64_t first_token = p.cu[w.r];
+            // Q, once the products of the row block before have read it
+            if (!first) {
+                wait(&S.q_free, free_turn);
+                free_turn ^= 1;
+            }
+            first = false;
+            if (wide || g == 0) {
+                char *dst = qtile + (wide ? g : 0) * Z::kSlotBytes;
+                constexpr int kVecs = DP / 8;
+                for (int i = row; i < mine * kVecs; i += kTile) {
+                    const int x = i / kVecs, vec = i % kVecs;
+                    const int mx = w.b * kBlockRows + m0 + x;
+                    uint4 val = make_uint4(0, 0, 0, 0);
+                    if (vec * 8 < c.dim)
+                        val = ld_stream(p.q + 2 * ((first_token + mx / p.group) * p.q_token +
+                                                   (w.h * p.group + mx % p.group) * p.q_head + vec * 8));
+                    *reinterpret_cast<uint4 *>(dst + vec / 8 * Z::kChunk + x * 128 + ((vec % 8) ^ (x % 8)) * 16) = val;
+                }
+                fence_proxy_async_shared();
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&S.q_full);
+
+            uint32_t bits[kMaxTree / 32] = {};
+            if (p.parent) {
+                int32_t *par = S.group[g].parent;
+                if (row < w.q.n)
+                    par[row] = p.parent[first_token + row];
+                asm volatile("bar.sync %0, 128;" ::"r"(2 + g) : "memory");
+                if (on)
+                    for (int at = token; at >= 0;) {
+#pragma unroll
+                        for (int j = 0; j < kMaxTree / 32; ++j)
+                            bits[j] |= at / 32 == j ? 1u << (at & 31) : 0u;
+                        const int up = par[at];
+                        if (at == 0 ? up != -1 : up < 0 || up >= at) {
+                            cache_error(c.error, SPEC_DEVERR_TREE, w.r);
+                            break;
+                        }
+                        at = up;
+                    }
+                asm volatile("bar.sync %0, 128;" ::"r"(2 + g) : "memory");
+            }
+            // keys that every row of this warp sees
+            const int all_see = p.parent ? w.q.len
+                                         : w.q.len + (w.b * kBlockRows + m0 + sub * 32) / p.group + 1;
+            float M = -INFINITY, l = 0;
+            bool any = false;  // the accumulator holds something
+            for (int t = wide ? 0 : g; t < nt; t += wide ? 1 : 2) {
+                wait(&S.s_full[g], s_turn);
+                s_turn ^= 1;
+                if (warp_on) {
+                    tmem_fence_after();
+                    float x[kTile];
+#pragma unroll
+                    for (int j = 0; j < kTile / 32; ++j)
+                        tmem_ld32(s_addr + j * 32, x + j * 32);
+                    tmem_wait_ld();
+                    const int column = (w.t0 + t) * kTile;
+                    if (column + kTile > all_see) {
+#pragma unroll
+                        for (int j = 0; j < kTile / 32; ++j) {
+                            const uint32_t see = p.parent ? tree_columns(bits, w.q.len, column + j * 32)
+                                                          : low_bits(w.q.len + token + 1 - column - j * 32);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                x[j * 32 + e] = see >> e & 1 ? x[j * 32 + e] : -INFINITY;
+                        }
+                    }
+                    float top[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                    for (int e = 4; e < kTile; ++e)
+                        top[e & 3] = fmaxf(top[e & 3], x[e]);
+                    const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
+                    const bool grown = mx > M + kLazy;  // also from -inf
+                    const float f = grown ? ex2(M - mx) : 1.0f;
+                    if (grown) {
+                        M = mx;
+                        l *= f;
+                    }
+                    if (any && __any_sync(kFull, grown)) {
+#pragma unroll 1
+                        for (int j = 0; j < DP / 32; ++j) {
+                            float o[32];
+                            tmem_ld32(s_addr + kTile + j * 32, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] *= f;
+                            tmem_st32(s_addr + kTile + j * 32, o);
+                        }
+                        tmem_wait_st();
+                    }
+                    any = true;
+                    const float base = M == -INFINITY ? 0.0f : M;
+                    float sum[4] = {0, 0, 0, 0};
+#pragma unroll
+                    for (int e = 0; e < kTile; e += 2) {
+                        const float a = ex2(fmaf(x[e], p.scale_log2, -base));
+                        const float b = ex2(fmaf(x[e + 1], p.scale_log2, -base));
+                        sum[e / 2 & 3] += a + b;
+                        x[e / 2] = __uint_as_float(from_float2<DT>(a, b));
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tmem_st32(s_addr, x);
+                    tmem_st32(s_addr + 32, x + 32);
+                    tmem_wait_st();
+                    tmem_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&S.p_full[g]);
+            }
+            const int turns = wide ? nt : (nt - g + 1) / 2;  // this group's tiles
+            if (turns > 0) {
+                wait(&S.s_full[g], s_turn);  // its last product
+                s_turn ^= 1;
+            }
+            tmem_fence_after();
+            const bool whole = w.whole();
+            // partial sums: of a row block from before this share (0), or going on behind it (1)
+            const int64_t place = ((int64_t)blockIdx.x * 2 + (w.t0 == 0)) * p.max_rows + m0 + row;
+            char *out = p.out + 2 * ((first_token + token) * p.out_token + head * p.out_head);
+            auto store = [&](const float *o, int col, float by) {  // 32 columns
+                if (!on)
+                    return;
+                if (whole) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        if (col + e < c.dim)
+                            *reinterpret_cast<uint4 *>(out + 2 * (col + e)) =
+                                make_uint4(from_float2<DT>(o[e] * by, o[e + 1] * by),
+                                           from_float2<DT>(o[e + 2] * by, o[e + 3] * by),
+                                           from_float2<DT>(o[e + 4] * by, o[e + 5] * by),
+                                           from_float2<DT>(o[e + 6] * by, o[e + 7] * by));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<float4 *>(p.part_o + place * DP + col + e) =
+                            make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                }
+            };
+            auto store_ml = [&]() {
+                if (!on)
+                    return;
+                if (!whole)
+                    p.part_ml[place] = make_float2(M, l);
+                else if (p.lse)
+                    p.lse[(first_token + token) * p.heads + head] = (M + log2f(l)) * 0.69314718055994531f;
+            };
+            if (wide) {
+                if (warp_on) {
+#pragma unroll 1
+                    for (int j = 0; j < DP / 32; ++j) {
+                        float o[32];
+                        tmem_ld32(s_addr + kTile + j * 32, o);
+                        tmem_wait_ld();
+                        store(o, j * 32, 1.0f / l);
+                    }
+                    store_ml();
+                }
+            } else {
+                S.group[g].ml[row] = make_float2(M, l);
+                tmem_fence_before();
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                tmem_fence_after();
+                if (warp_on) {
+                    const float2 other = S.group[g ^ 1].ml[row];
+                    const float top = fmaxf(M, other.x);
+                    const float fm = M == -INFINITY ? 0.0f : ex2(M - top);
+                    const float fo = other.x == -INFINITY ? 0.0f : ex2(other.x - top);
+                    M = top;
+                    l = l * fm + other.y * fo;
+                    const float f0 = g == 0 ? fm : fo, f1 = g == 0 ? fo : fm;
+                    const uint32_t o_addr = tmem + lanes + kTile + g * (DP / 2);  // half of the columns
+#pragma unroll 1
+                    for (int j = 0; j < DP / 64; ++j) {
+                        float o[32];
+                        tmem_ld32(o_addr + j * 32, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            o[e] *= f0;
+                        if (nt > 1) {
+                            float o1[32];
+                            tmem_ld32(o_addr + 256 + j * 32, o1);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = fmaf(o1[e], f1, o[e]);
+                        }
+                        store(o, g * (DP / 2) + j * 32, 1.0f / l);
+                    }
+                    if (g == 0)
+                        store_ml();
+                }
+                tmem_fence_before();
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                tmem_fence_after();
+            }
+            if (!whole && w.t0 == 0 && tid == 0) {
+                Partial &x = p.partial[blockIdx.x];
+                x.r = w.r;
+                x.h = w.h;
+                x.b = w.b;
+                x.last = shares.owner(w.pos + w.tiles - 1);
+                x.rows = rows;
+            }
+        } while (w.next(c, p));
+        tmem_fence_before();
+    }
+    __syncthreads();
+    if (warp == kLoadWarp && S.gave_up) {
+        // copies that nobody waited for; a slot that none was started into waits in vain, for a while
+        for (int i = 0; i < SLOTS; ++i)
+            for (uint32_t n = 0; n < 4096 && !(mbar_try_wait(&S.full[i], 0) && mbar_try_wait(&S.full[i], 1)); ++n) {
+            }
+    }
+    __syncthreads();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp == kMmaWarp) {
+        tmem_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemColumns));
+    }
+}
+
+// Joins the partial sums of the row blocks that were cut: blocks (share, 8 rows), a warp per row.
+template <int DT, int DP>
+__global__ void __launch_bounds__(256) join_kernel(CacheView c, AttentionParams p)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Partial x = p.partial[blockIdx.x];
+    const int lane = threadIdx.x & 31, row = blockIdx.y * 8 + (threadIdx.x >> 5);
+    if (row >= x.rows)
+        return;
+    const int parts = x.last - (int)blockIdx.x + 1;
+    // the first part is the tail of its block's share, the others lie at the head of theirs
+    auto place = [&](int i) { return ((int64_t)(blockIdx.x + i) * 2 + (i == 0)) * p.max_rows + row; };
+    constexpr int kMost = (kMaxGrid + 31) / 32;
+    float2 ml[kMost];
+    float top = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < kMost; ++j) {
+        const int i = j * 32 + lane;
+        ml[j] = i < parts ? p.part_ml[place(i)] : make_float2(-INFINITY, 0);
+        top = fmaxf(top, ml[j].x);
+    }
+    top = warp_max(top);
+    float l = 0;
+#pragma unroll
+    for (int j = 0; j < kMost; ++j) {
+        ml[j].x = ml[j].x == -INFINITY ? 0.0f : ex2(ml[j].x - top);
+        l += ml[j].x * ml[j].y;
+    }
+    l = warp_sum(l);
+    constexpr int E = DP / 32;  // elements per lane
+    float acc[E] = {};
+#pragma unroll
+    for (int j = 0; j < kMost; ++j) {
+        const int some = min(32, parts - j * 32);
+#pragma unroll 4
+        for (int i = 0; i < some; ++i) {
+            const float f = __shfl_sync(kFull, ml[j].x, i);
+            const float *o = p.part_o + place(j * 32 + i) * DP + lane * E;
+            float v[E];
+            if (E == 4) {
+                const float4 y = *reinterpret_cast<const float4 *>(o);
+                v[0] = y.x, v[1] = y.y, v[E > 2 ? 2 : 0] = y.z, v[E > 3 ? 3 : 0] = y.w;
+            } else {
+                const float2 y = *reinterpret_cast<const float2 *>(o);
+                v[0] = y.x, v[1] = y.y;
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                acc[e] = f == 0.0f ? acc[e] : fmaf(f, v[e], acc[e]);
+        }
+    }
+    const int m = x.b * kBlockRows + row;
+    const int64_t t = (int64_t)p.cu[x.r] + m / p.group;
+    const int head = x.h * p.group + m % p.group;
+    const float by = 1.0f / l;
+    if (lane * E < c.dim) {
+        char *out = p.out + 2 * (t * p.out_token + head * p.out_head + lane * E);
+        if (E == 4)
+            *reinterpret_cast<uint2 *>(out) = make_uint2(from_float2<DT>(acc[0] * by, acc[1] * by),
+                                                         from_float2<DT>(acc[E > 2 ? 2 : 0] * by, acc[E > 3 ? 3 : 0] * by));
+        else
+            *reinterpret_cast<uint32_t *>(out) = from_float2<DT>(acc[0] * by, acc[1] * by);
     }
     if (lane == 0 && p.lse)
-        p.lse[t * p.heads + h] = m + logf(l);
+        p.lse[t * p.heads + head] = (top + log2f(l)) * 0.69314718055994531f;
+}
+
+// ---------------------------------------------------------------------------------------
+// Host
+// ---------------------------------------------------------------------------------------
+
+struct AttentionPlan {
+    int dp, max_rows;
+    size_t partial, ml, o, total;
+};
+
+AttentionPlan attention_plan(const CacheView &c, int32_t num_q_heads, int64_t N)
+{
+    AttentionPlan a;
+    a.dp = c.dim <= 64 ? 64 : 128;
+    a.max_rows = (int)std::max<int64_t>(1, std::min<int64_t>(kBlockRows, N * (num_q_heads / c.heads)));
+    size_t o = 0;
+    a.partial = o;
+    o = align256(o + sizeof(Partial) * kMaxGrid);
+    a.ml = o;
+    o = align256(o + sizeof(float2) * 2 * kMaxGrid * a.max_rows);
+    a.o = o;
+    o = align256(o + sizeof(float) * 2 * kMaxGrid * a.max_rows * a.dp);
+    a.total = o + 256;  // slack for aligning the caller's pointer
+    return a;
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled()
+{
+    static const EncodeTiled f = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return f;
+}
+
+// The pages of one layer as a tensor (head_dim, token, head, page); boxes of 64 elements by `box`
+// tokens, written to shared memory with the 128-byte swizzle that the products read.
+bool encode_pages(CUtensorMap *map, const CacheView &c, int dtype, char *base, int box)
+{
+    const EncodeTiled f = encode_tiled();
+    if (!f)
+        return false;
+    const int64_t least = 2 * (int64_t)c.dim;  // any valid stride does for a dimension of size 1
+    const cuuint64_t dims[4] = {(cuuint64_t)c.dim, (cuuint64_t)c.page_size, (cuuint64_t)c.heads,
+                                (cuuint64_t)c.num_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)(c.page_size > 1 ? 2 * c.token_stride : least),
+                                   (cuuint64_t)(c.heads > 1 ? 2 * c.head_stride : least),
+                                   (cuuint64_t)(c.num_pages > 1 ? 2 * c.page_stride : least)};
+    const cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1}, steps[4] = {1, 1, 1, 1};
+    return f(map, dtype == SPEC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, base,
+             dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kMaxDevices = 64;
+
+// SMs of the current device; sets the kernels' shared memory on its first call there.
+template <int DT, int DP> cudaError_t prepare_kernel()
+{
+    return cudaFuncSetAttribute(attention_kernel<DT, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                AttnSizes<DP>::kBytes);
+}
+
+cudaError_t current_sms(int *sms)
+{
+    static int cached[kMaxDevices];  // written with the same value by every thread that finds it 0
+    int dev;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e)
+        return e;
+    if (dev < 0 || dev >= kMaxDevices)
+        return cudaErrorInvalidDevice;
+    int n = __atomic_load_n(&cached[dev], __ATOMIC_ACQUIRE);
+    if (n == 0) {
+        e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        if (!e)
+            e = prepare_kernel<SPEC_BF16, 64>();
+        if (!e)
+            e = prepare_kernel<SPEC_BF16, 128>();
+        if (!e)
+            e = prepare_kernel<SPEC_F16, 64>();
+        if (!e)
+            e = prepare_kernel<SPEC_F16, 128>();
+        if (e)
+            return e;
+        __atomic_store_n(&cached[dev], n, __ATOMIC_RELEASE);
+    }
+    *sms = n;
+    return cudaSuccess;
+}
+
+template <int DT, int DP>
+cudaError_t launch_attention(const CUtensorMap &kmap, const CUtensorMap &vmap, const CacheView &c,
+                             const AttentionParams &p, int grid, cudaStream_t st)
+{
+    attention_kernel<DT, DP><<<grid, kAttnThreads, AttnSizes<DP>::kBytes, st>>>(kmap, vmap, c, p);
+    cudaError_t e = cudaGetLastError();
+    if (e)
+        return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid, (p.max_rows + 7) / 8);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, join_kernel<DT, DP>, c, p);
 }
 
 spec_status check_attention(const spec_cache *cache, CacheView *c, int32_t num_q_heads, int32_t B, int64_t N)
@@ -152,7 +1067,7 @@ size_t spec_attention_workspace_size(const spec_cache *cache, int32_t num_q_head
     CacheView c;
     if (check_attention(cache, &c, num_q_heads, B, N) != SPEC_OK)
         return 0;
-    return 256;
+    return attention_plan(c, num_q_heads, N).total;
 }
 
 spec_status spec_attention(const spec_cache *cache, int32_t layer, const void *q, int64_t q_token_stride,
@@ -173,7 +1088,8 @@ spec_status spec_attention(const spec_cache *cache, int32_t layer, const void *q
         return SPEC_ERR_INVALID_ARG;
     if (workspace_bytes < spec_attention_workspace_size(cache, num_q_heads, B, N))
         return SPEC_ERR_WORKSPACE;
-    if (cudaPeekAtLastError() != cudaSuccess)
+    int sms;
+    if (cudaPeekAtLastError() != cudaSuccess || current_sms(&sms) != cudaSuccess)
         return SPEC_ERR_CUDA;
     if (B == 0 || N == 0)
         return SPEC_OK;
@@ -191,15 +1107,30 @@ spec_status spec_attention(const spec_cache *cache, int32_t layer, const void *q
     p.N = N;
     p.cu = cu_new;
     p.parent = parent;
-    p.scale = scale;
-    p.layer_offset = layer * c.layer_stride;
-    const unsigned blocks = (unsigned)((N * num_q_heads + 7) / 8);
+    p.scale_log2 = scale * kLog2e;
+    const AttentionPlan plan = attention_plan(c, num_q_heads, N);
+    char *ws = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~uintptr_t(255));
+    p.partial = reinterpret_cast<Partial *>(ws + plan.partial);
+    p.part_ml = reinterpret_cast<float2 *>(ws + plan.ml);
+    p.part_o = reinterpret_cast<float *>(ws + plan.o);
+    p.max_rows = plan.max_rows;
+    p.box = 8;
+    while (p.box < kTile && c.page_size % (2 * p.box) == 0)
+        p.box *= 2;
+    CUtensorMap kmap, vmap;
+    if (!encode_pages(&kmap, c, cache->dtype, c.k + 2 * layer * c.layer_stride, p.box) ||
+        !encode_pages(&vmap, c, cache->dtype, c.v + 2 * layer * c.layer_stride, p.box))
+        return SPEC_ERR_UNSUPPORTED;
+    const int grid = std::min(sms, kMaxGrid);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
     if (cache->dtype == SPEC_BF16)
-        attention_kernel<SPEC_BF16><<<blocks, 256, 0, st>>>(c, p);
+        e = plan.dp == 64 ? launch_attention<SPEC_BF16, 64>(kmap, vmap, c, p, grid, st)
+                          : launch_attention<SPEC_BF16, 128>(kmap, vmap, c, p, grid, st);
     else
-        attention_kernel<SPEC_F16><<<blocks, 256, 0, st>>>(c, p);
-    return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+        e = plan.dp == 64 ? launch_attention<SPEC_F16, 64>(kmap, vmap, c, p, grid, st)
+                          : launch_attention<SPEC_F16, 128>(kmap, vmap, c, p, grid, st);
+    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
 }  // extern "C"
