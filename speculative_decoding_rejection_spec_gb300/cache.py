@@ -19,7 +19,10 @@ request r.  Chains of k_r drafts are k_r + 1 new tokens: ``cu_new = cu_num_draft
 from __future__ import annotations
 
 import ctypes
+from contextlib import nullcontext
 from dataclasses import dataclass, field
+
+import torch
 
 from .binding import SpecRejectError, load as _load_library
 
@@ -84,7 +87,7 @@ class PagedCache:
     k, v [layers, pages, page_size, kv_heads, head_dim] (bfloat16 or float16, the same strides, unit
     stride inside; views of one tensor are fine); page_table [requests, max_pages], lens and held
     [requests], ref_counts and free_pages [pages], num_free [1]: int32, as spec_cache.h describes
-    them.  ``make_cache`` makes an empty one.
+    them.  ``make_cache`` makes an empty one.  The tensors stay those given: write into them.
     """
     k: object
     v: object
@@ -99,13 +102,14 @@ class PagedCache:
     struct: SpecCache = field(default=None, repr=False)
 
     def __post_init__(self):
-        import torch
         k, v, dev = self.k, self.v, self.k.device
         if k.dtype not in (torch.bfloat16, torch.float16) or v.dtype != k.dtype:
             raise TypeError("keys and values must both be bfloat16 or both float16")
         if k.dim() != 5 or k.shape != v.shape or k.stride(4) != 1 or v.stride(4) != 1:
             raise ValueError("keys and values must be [layers, pages, page_size, kv_heads, head_dim] alike, with "
                              "unit stride along head_dim")
+        if v.device != dev:
+            raise ValueError("keys and values must be on one device")
         if any(k.stride(i) != v.stride(i) for i in range(4) if k.shape[i] > 1):
             raise ValueError("keys and values must have the same strides")
         L, NP, P, H, D = (int(x) for x in k.shape)
@@ -133,51 +137,41 @@ class PagedCache:
             num_requests=R, max_pages=MP, lens=self.lens.data_ptr(), held=self.held.data_ptr(),
             ref_counts=self.ref_counts.data_ptr(), free_pages=self.free_pages.data_ptr(),
             num_free=self.num_free.data_ptr(), error=self.error.data_ptr(), scratch=self.scratch.data_ptr())
-
-    @property
-    def device(self):
-        return self.k.device
+        # what every call needs, looked up once: the tensors of a cache do not change
+        self.ref, self.device, self.dtype, self.heads, self.dim = ctypes.byref(self.struct), dev, k.dtype, H, D
 
 
 def _code(t) -> int:
-    import torch
     return BF16 if t.dtype == torch.bfloat16 else F16
 
 
 def _int32(t, shape, name, device, contiguous=True):
-    import torch
-    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or (contiguous and not t.is_contiguous()):
+    if t.dtype is not torch.int32 or t.shape != shape or (contiguous and not t.is_contiguous()):
         raise TypeError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-class _On:
-    """Makes the cache's device current and names the stream a call runs on."""
+_SAME_DEVICE = nullcontext()
 
-    def __init__(self, c, stream):
-        import torch
-        self.guard = torch.cuda.device(c.device)
-        self.stream, self.device = stream, c.device
 
-    def __enter__(self):
-        import torch
-        self.guard.__enter__()
-        s = torch.cuda.current_stream(self.device) if self.stream is None else self.stream
-        return ctypes.c_void_p(s.cuda_stream)
+def _on(c):
+    """A context in which the cache's device is current."""
+    return _SAME_DEVICE if torch.cuda.current_device() == c.device.index else torch.cuda.device(c.device)
 
-    def __exit__(self, *exc):
-        return self.guard.__exit__(*exc)
+
+def _stream(c, stream) -> int:
+    # the raw handle of the device's current stream, without a Stream object around it
+    return torch._C._cuda_getCurrentRawStream(c.device.index) if stream is None else stream.cuda_stream
 
 
 def make_cache(num_layers: int, num_pages: int, page_size: int, num_kv_heads: int, head_dim: int, num_requests: int,
                max_pages: int, dtype=None, device="cuda", stream=None) -> PagedCache:
     """An empty cache: every page free.  Keys and values are zero."""
-    import torch
     dev = torch.device(device)
     if dev.type == "cuda" and dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
@@ -186,56 +180,58 @@ def make_cache(num_layers: int, num_pages: int, page_size: int, num_kv_heads: in
                      dtype=torch.bfloat16 if dtype is None else dtype, device=dev)
     c = PagedCache(kv[0], kv[1], page_table=ints(num_requests, max_pages), lens=ints(num_requests),
                    held=ints(num_requests), ref_counts=ints(num_pages), free_pages=ints(num_pages), num_free=ints(1))
-    with _On(c, stream) as s:
-        _check(load().spec_cache_init(ctypes.byref(c.struct), s), "spec_cache_init")
+    with _on(c):
+        _check(load().spec_cache_init(c.ref, _stream(c, stream)), "spec_cache_init")
     return c
 
 
 def last_error(c: PagedCache, stream=None):
     """(status, error_bits, first_bad_request) since the last call, and clears them (synchronises)."""
     bits, first = ctypes.c_int32(0), ctypes.c_int32(0)
-    with _On(c, stream) as s:
-        st = load().spec_cache_error(ctypes.byref(c.struct), s, ctypes.byref(bits), ctypes.byref(first))
+    with _on(c):
+        st = load().spec_cache_error(c.ref, _stream(c, stream), ctypes.byref(bits), ctypes.byref(first))
     if st not in (0, 5, 6):
         raise SpecRejectError(st, "spec_cache_error")
     return int(st), int(bits.value), int(first.value)
 
 
 def _cu(c, cu_new) -> int:
-    if cu_new.dim() != 1 or cu_new.shape[0] < 1:
+    shape = cu_new.shape
+    if len(shape) != 1 or shape[0] < 1:
         raise TypeError("cu_new must be a 1-D int32 tensor of B + 1 entries")
-    _int32(cu_new, cu_new.shape, "cu_new", c.device)
-    return int(cu_new.shape[0]) - 1
+    _int32(cu_new, shape, "cu_new", c.device)
+    return shape[0] - 1
 
 
 def _rows(c, t, heads, name):
     """Checks a [N, heads, head_dim] tensor; returns its token and head strides."""
-    if t.dtype != c.k.dtype or t.dim() != 3 or (heads is not None and t.shape[1] != heads) or \
-            t.shape[2] != c.k.shape[4] or (t.numel() and t.stride(2) != 1):
-        raise TypeError(f"{name} must be a {c.k.dtype} tensor [N, heads, {c.k.shape[4]}] with unit stride inside")
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not c.dtype or len(shape) != 3 or (heads is not None and shape[1] != heads) or \
+            shape[2] != c.dim or (stride[2] != 1 and t.numel()):
+        raise TypeError(f"{name} must be a {c.dtype} tensor [N, heads, {c.dim}] with unit stride inside")
     if t.device != c.device:
         raise ValueError(f"{name} must be on {c.device}")
-    return [int(t.stride(i)) if t.shape[i] > 1 else 0 for i in (0, 1)]
+    return stride[0], stride[1]
 
 
 def reserve(c: PagedCache, cu_new, stream=None):
     """Pages for the new tokens of every request (spec_cache_reserve)."""
     B = _cu(c, cu_new)
-    with _On(c, stream) as s:
-        _check(load().spec_cache_reserve(ctypes.byref(c.struct), _ptr(cu_new), B, s), "spec_cache_reserve")
+    with _on(c):
+        _check(load().spec_cache_reserve(c.ref, cu_new.data_ptr(), B, _stream(c, stream)), "spec_cache_reserve")
 
 
 def append(c: PagedCache, layer: int, k_new, v_new, cu_new, stream=None):
     """Writes the new tokens' keys and values [N, kv_heads, head_dim] of one layer (spec_cache_append)."""
     B = _cu(c, cu_new)
-    H = int(c.k.shape[3])
-    kt, kh = _rows(c, k_new, H, "k_new")
-    vt, vh = _rows(c, v_new, H, "v_new")
-    if k_new.shape[0] != v_new.shape[0]:
+    kt, kh = _rows(c, k_new, c.heads, "k_new")
+    vt, vh = _rows(c, v_new, c.heads, "v_new")
+    N = k_new.shape[0]
+    if v_new.shape[0] != N:
         raise ValueError("k_new and v_new must have the same rows")
-    with _On(c, stream) as s:
-        _check(load().spec_cache_append(ctypes.byref(c.struct), int(layer), _ptr(k_new), kt, kh, _ptr(v_new), vt, vh,
-                                        _ptr(cu_new), B, int(k_new.shape[0]), s), "spec_cache_append")
+    with _on(c):
+        _check(load().spec_cache_append(c.ref, layer, k_new.data_ptr(), kt, kh, v_new.data_ptr(), vt, vh,
+                                        cu_new.data_ptr(), B, N, _stream(c, stream)), "spec_cache_append")
 
 
 def commit(c: PagedCache, cu_new, num_accepted, parent=None, last_node=None, out_lens=None, stream=None):
@@ -252,9 +248,9 @@ def commit(c: PagedCache, cu_new, num_accepted, parent=None, last_node=None, out
         _int32(last_node, (B,), "last_node", c.device)
     if out_lens is not None:
         _int32(out_lens, (B,) if out_lens is not c.lens else c.lens.shape, "out_lens", c.device)
-    with _On(c, stream) as s:
-        _check(load().spec_cache_commit(ctypes.byref(c.struct), _ptr(cu_new), B, N, _ptr(num_accepted), _ptr(parent),
-                                        _ptr(last_node), _ptr(out_lens), s), "spec_cache_commit")
+    with _on(c):
+        _check(load().spec_cache_commit(c.ref, cu_new.data_ptr(), B, N, num_accepted.data_ptr(), _ptr(parent),
+                                        _ptr(last_node), _ptr(out_lens), _stream(c, stream)), "spec_cache_commit")
 
 
 def fork(c: PagedCache, src, dst, stream=None):
@@ -262,8 +258,9 @@ def fork(c: PagedCache, src, dst, stream=None):
     F = int(src.shape[0])
     _int32(src, (F,), "src", c.device)
     _int32(dst, (F,), "dst", c.device)
-    with _On(c, stream) as s:
-        _check(load().spec_cache_fork(ctypes.byref(c.struct), _ptr(src), _ptr(dst), F, s), "spec_cache_fork")
+    with _on(c):
+        _check(load().spec_cache_fork(c.ref, src.data_ptr(), dst.data_ptr(), F, _stream(c, stream)),
+               "spec_cache_fork")
 
 
 def release(c: PagedCache, keep_lens=None, stream=None):
@@ -273,13 +270,12 @@ def release(c: PagedCache, keep_lens=None, stream=None):
     if keep_lens is not None:
         B = int(keep_lens.shape[0])
         _int32(keep_lens, (B,), "keep_lens", c.device)
-    with _On(c, stream) as s:
-        _check(load().spec_cache_release(ctypes.byref(c.struct), _ptr(keep_lens), B, s), "spec_cache_release")
+    with _on(c):
+        _check(load().spec_cache_release(c.ref, _ptr(keep_lens), B, _stream(c, stream)), "spec_cache_release")
 
 
 def attention_workspace_size(c: PagedCache, num_q_heads: int, B: int, N: int) -> int:
-    with _On(c, None):
-        n = load().spec_attention_workspace_size(ctypes.byref(c.struct), int(num_q_heads), int(B), int(N))
+    n = load().spec_attention_workspace_size(c.ref, int(num_q_heads), int(B), int(N))
     if n == 0:
         raise ValueError("invalid or unsupported sizes for spec_attention_workspace_size")
     return int(n)
@@ -295,31 +291,30 @@ def attention(c: PagedCache, layer: int, q, cu_new, parent=None, scale=None, out
     row's softmax sum; ``workspace`` (uint8) may be given to reuse it: calls that can run at the
     same time need one each.  Rows behind ``cu_new[B]`` are left as they were in ``out``.
     """
-    import torch
     B = _cu(c, cu_new)
     qt, qh = _rows(c, q, None, "q")
-    N, H = int(q.shape[0]), int(q.shape[1])
+    N, H, _ = q.shape
     if parent is not None:
         _int32(parent, (N,), "parent", c.device)
     if out is None:
-        out = torch.empty((N, H, int(q.shape[2])), dtype=q.dtype, device=q.device)
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     elif out.shape != q.shape:
         raise ValueError("out must have the shape of q")
     ot, oh = _rows(c, out, H, "out")
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (N, H) or not lse.is_contiguous() or
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (N, H) or not lse.is_contiguous() or
                             lse.device != c.device):
         raise TypeError(f"lse must be a contiguous float32 tensor of shape {(N, H)} on {c.device}")
-    size = load().spec_attention_workspace_size
-    with _On(c, stream) as s:
+    lib = load()
+    with _on(c):
         if workspace is None:
-            n = int(size(ctypes.byref(c.struct), H, B, N))
-            workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=c.device)
+            n = lib.spec_attention_workspace_size(c.ref, H, B, N)
+            workspace = torch.empty(n, dtype=torch.uint8, device=c.device)
             if stream is not None:
                 workspace.record_stream(stream)
-        elif workspace.dtype != torch.uint8 or workspace.device != c.device or not workspace.is_contiguous():
+        elif workspace.dtype is not torch.uint8 or workspace.device != c.device or not workspace.is_contiguous():
             raise TypeError(f"workspace must be a contiguous uint8 tensor on {c.device}")
-        _check(load().spec_attention(
-            ctypes.byref(c.struct), int(layer), _ptr(q), qt, qh, H, _ptr(cu_new), B, N, _ptr(parent),
-            float(c.k.shape[4] ** -0.5 if scale is None else scale), _ptr(out), ot, oh, _ptr(lse), _ptr(workspace),
-            int(workspace.numel()), s), "spec_attention")
+        _check(lib.spec_attention(
+            c.ref, layer, q.data_ptr(), qt, qh, H, cu_new.data_ptr(), B, N, _ptr(parent),
+            c.dim ** -0.5 if scale is None else scale, out.data_ptr(), ot, oh, _ptr(lse), workspace.data_ptr(),
+            workspace.numel(), _stream(c, stream)), "spec_attention")
     return out

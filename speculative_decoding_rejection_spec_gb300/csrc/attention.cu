@@ -11,7 +11,8 @@
 //                   grown by more than 2^8 since (P stays below 2^8, exact in its sum's fp32), so
 //                   the accumulator in tensor memory is rarely rescaled.
 //   warp 8          loads tiles of K and V, page by page, through TMA into a ring of slots
-//   warp 9          issues the matrix products (one lane)
+//   warp 9          issues the matrix products (one thread)
+//   warps 10, 11    walk the list of work ahead of the others, announce it in a ring and load Q
 // A block of more than 128 rows ("wide") gives each group 128 of them and both use every tile: the
 // products of one group run while the other computes its exponentials.  A block of at most 128 rows
 // ("narrow": decoding and most verify steps) gives both groups the same rows and every other tile,
@@ -35,8 +36,9 @@ namespace {
 
 constexpr int kTile = 128;          // keys per tile, and rows per softmax group
 constexpr int kBlockRows = 256;     // query rows of a (request, head, row block)
-constexpr int kSoftmaxWarps = 8, kLoadWarp = 8, kMmaWarp = 9;
-constexpr int kAttnThreads = 320;
+constexpr int kSoftmaxWarps = 8, kLoadWarp = 8, kMmaWarp = 9, kQueryWarp = 10;
+constexpr int kAttnThreads = 384;
+constexpr int kItems = 4;           // row blocks announced ahead
 constexpr int kMaxGrid = 160;       // blocks a call may use (SMs of the device, 152 on GB300)
 constexpr int kMinTiles = 2;        // least tiles of a block's share
 constexpr float kLazy = 8.0f;       // log2 of the growth that moves a row's maximum
@@ -170,12 +172,26 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, in
                  : "memory");
 }
 
-__device__ __forceinline__ uint64_t global_ns()
+// One lane of the (converged) warp: behind this predicate the compiler knows that a single lane is
+// active and takes the operands of products and copies from uniform registers.
+__device__ __forceinline__ bool elect_one()
 {
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p != 0;
 }
+
+// A row block of this block's share, as the roles need it.  nt = 0 ends the share.
+struct alignas(16) Item {
+    int32_t r, h, b;       // request, kv head, row block
+    int32_t rows, nt;      // query rows; tiles in the share
+    int32_t t0, tiles;     // the first of those, and tiles of the row block
+    int32_t keys;          // keys up to the last row's own
+    int32_t len, n, first; // of the request: committed tokens, new tokens, its first row
+    int32_t q_use;         // Q slots used before (a narrow row block takes one, a wide one both)
+    uint32_t slots;        // K / V slots used before
+    int32_t last;          // the last block that works on the row block
+};
 
 // What a block keeps behind the operand tiles.
 template <int SLOTS> struct alignas(16) AttnShared {
@@ -185,30 +201,31 @@ template <int SLOTS> struct alignas(16) AttnShared {
         int32_t parent[kMaxTree];
         int64_t sums[kAttnThreads / 32];
     } group[2];
+    Item item[kItems];
     uint64_t full[SLOTS], empty[SLOTS];  // a slot's tile has landed / has been used
-    uint64_t s_full[2], p_full[2];       // a group's S is there (or its last O) / its P is there
-    uint64_t q_full, q_free, done;
+    uint64_t s_full[2], p_full[2], o_full[2];  // a group's S is there / its P / the last of its O
+    uint64_t q_full[2], q_empty[2];      // a slot's Q is there / has been used
+    uint64_t item_full[kItems], item_empty[kItems];
+    uint64_t merge, done;
     int64_t base;                        // work before request r
     int32_t r;                           // first request of this block's share
     uint32_t tmem;
     volatile int32_t gave_up;
 };
 
-// Waits for a barrier's phase.  A wait of two seconds (or another one's) gives up: the roles then
-// run through their loops without waiting, issue nothing more and leave together.
-__device__ __forceinline__ void attn_wait(uint64_t *bar, uint32_t parity, volatile int32_t *gave_up, int32_t *error)
+// Waits for a barrier's phase, a bounded number of polls.  When one wait gives up, all do: no row block
+// is begun and no copy started any more, what has begun runs through without waiting (its indices are
+// those of an announced row block), and the roles leave together.
+__device__ __forceinline__ bool attn_wait(uint64_t *bar, uint32_t parity, volatile int32_t *gave_up, int32_t *error)
 {
-    if (mbar_try_wait(bar, parity))
-        return;
-    const uint64_t start = global_ns();
-    for (uint32_t i = 0; i < kWaitLimit; ++i) {
-        if (mbar_try_wait(bar, parity) || *gave_up)
-            return;
-        if (i % 64 == 63 && global_ns() - start > 2000000000ull)
-            break;
-    }
+    for (uint32_t i = 0; i < kWaitLimit; ++i)
+        if (mbar_try_wait(bar, parity))
+            return true;
+        else if (*gave_up)
+            return false;
     *gave_up = 1;
     atomicOr(error, SPEC_DEVERR_TIMEOUT);
+    return false;
 }
 
 // ---------------------------------------------------------------------------------------
@@ -260,8 +277,7 @@ struct Shares {
     __device__ __forceinline__ int owner(int64_t t) const { return (int)(((t + 1) * blocks - 1) / total); }
 };
 
-// Walks a block's share, one (request, head, row block) at a time.  Every role walks for itself; the
-// calls are made by whole warps.
+// Walks a block's share, one (request, head, row block) at a time; a whole warp.
 struct Walk {
     Request q;
     int r, h, b;
@@ -350,6 +366,37 @@ __device__ __forceinline__ uint32_t tree_columns(const uint32_t *bits, int len, 
     return low_bits(-o) | (o > -32 ? bits[0] << -o : 0u);
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Two fp32 values in one instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b)
+{
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t x, float &a, float &b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 template <int DT, int DP>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, CacheView c,
@@ -425,9 +472,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&S.s_full[i], 1);
             mbar_init(&S.p_full[i], 4);
+            mbar_init(&S.o_full[i], 1);
+            mbar_init(&S.q_full[i], 2);
+            mbar_init(&S.q_empty[i], 1);
         }
-        mbar_init(&S.q_full, kSoftmaxWarps);
-        mbar_init(&S.q_free, 1);
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&S.item_full[i], 1);
+            mbar_init(&S.item_empty[i], kSoftmaxWarps + 3);  // loads, products, the second query warp
+        }
+        mbar_init(&S.merge, kSoftmaxWarps);
         mbar_init(&S.done, 1);
         S.gave_up = 0;
         mbar_fence_init();
@@ -442,46 +495,67 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = S.tmem;
-    auto wait = [&](uint64_t *bar, uint32_t parity) { attn_wait(bar, parity, &S.gave_up, c.error); };
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return attn_wait(bar, parity, &S.gave_up, c.error); };
 
-    Walk w;
-    w.start(c, p, shares, S.r, S.base);
+    // Waits for the row block announced as number k (in S.item[k % kItems]); the caller gives the entry
+    // back with done_with() when it has read it.
+    auto announced = [&](uint32_t k) { return wait(&S.item_full[k % kItems], k / kItems & 1); };
+    auto done_with = [&](uint32_t k) {
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&S.item_empty[k % kItems]);
+    };
 
     if (warp == kLoadWarp) {
         // Slot order: K of tile 0, then K of tile t + 1 and V of tile t, as the products use them.
         const int pieces = kTile / p.box;
         uint32_t slot = 0, turn = 0;  // turn: parity of the slots' next use
         bool first_turn = true;
-        do {
-            const int keys = block_keys(w.q, p.group, w.b);
-            const int32_t *row = c.table + w.r * c.table_stride;
-            // the pages of tile t, a piece per lane
-            auto lookup = [&](int t, int &page, int &token) {
-                const int at = t * kTile + lane * p.box;
-                page = -1;
-                token = 0;
-                if (t < w.t1 && lane < pieces && at < keys) {
-                    page = row[at / c.page_size];
-                    token = at % c.page_size;
-                    if (page < 0 || page >= c.num_pages) {
-                        cache_error(c.error, SPEC_DEVERR_PAGE, w.r);
-                        page = c.num_pages;  // outside the tensor: reads as zeros
-                    }
+        struct Pages {
+            int page, token;  // of the lane's piece; token < 0: behind the last key
+        };
+        for (uint32_t k = 0;; ++k) {
+            if (!announced(k))
+                break;
+            const Item &item = S.item[k % kItems];
+            const int r = item.r, h = item.h, keys = item.keys, t0 = item.t0, nt = item.nt;
+            done_with(k);
+            if (nt == 0)
+                break;
+            const int32_t *row = c.table + r * c.table_stride;
+            // The pages of a tile, a piece per lane.  Looked up two tiles ahead: `page` is not looked
+            // at before the tile is loaded.
+            auto lookup = [&](int t) {
+                Pages x{-1, -1};
+                const int at = (t0 + t) * kTile + lane * p.box;
+                if (t < nt && lane < pieces && at < keys) {
+                    const int column = at / c.page_size;
+                    x.page = row[column];
+                    x.token = at - column * c.page_size;
                 }
+                return x;
             };
-            auto load = [&](const CUtensorMap *map, int page, int token) {
+            auto load = [&](const CUtensorMap *map, const Pages &x) {
+                const int count = __popc(__ballot_sync(kFull, x.token >= 0));
+                int page = x.page;
+                if (x.token >= 0 && (page < 0 || page >= c.num_pages)) {
+                    cache_error(c.error, SPEC_DEVERR_PAGE, r);
+                    page = c.num_pages;  // outside the tensor: reads as zeros
+                }
                 if (!first_turn)
                     wait(&S.empty[slot], turn ^ 1);
+                __syncwarp();
                 if (!S.gave_up) {
-                    const unsigned there = __ballot_sync(kFull, page >= 0);
-                    if (lane == 0)
-                        mbar_arrive_expect_tx(&S.full[slot], __popc(there) * p.box * 128 * (DP / 64));
-                    __syncwarp();
-                    if (page >= 0) {
-                        const uint32_t dst = smem_addr(ring + slot * Z::kSlotBytes) + lane * p.box * 128;
+                    const uint32_t dst = smem_addr(ring) + slot * Z::kSlotBytes;
+                    if (elect_one())
+                        mbar_arrive_expect_tx(&S.full[slot], count * p.box * 128 * (DP / 64));
+                    for (int i = 0; i < count; ++i) {
+                        const int pg = __shfl_sync(kFull, page, i), tk = __shfl_sync(kFull, x.token, i);
+                        if (elect_one()) {
 #pragma unroll
-                        for (int i = 0; i < DP / 64; ++i)
-                            tma_box(dst + i * Z::kChunk, map, i * 64, token, w.h, page, &S.full[slot]);
+                            for (int j = 0; j < DP / 64; ++j)
+                                tma_box(dst + i * p.box * 128 + j * Z::kChunk, map, j * 64, tk, h, pg, &S.full[slot]);
+                        }
                     }
                 }
                 __syncwarp();
@@ -491,174 +565,227 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     first_turn = false;
                 }
             };
-            int page, token, next_page, next_token;
-            lookup(w.t0, page, token);
-            load(&kmap, page, token);
-            for (int t = w.t0; t < w.t1; ++t) {
-                lookup(t + 1, next_page, next_token);
-                if (t + 1 < w.t1)
-                    load(&kmap, next_page, next_token);
-                load(&vmap, page, token);
-                page = next_page;
-                token = next_token;
+            Pages now = lookup(0), next = lookup(1);
+            load(&kmap, now);
+            for (int t = 0; t < nt; ++t) {
+                const Pages later = lookup(t + 2);
+                if (t + 1 < nt)
+                    load(&kmap, next);
+                load(&vmap, now);
+                now = next;
+                next = later;
             }
-        } while (w.next(c, p));
+        }
     } else if (warp == kMmaWarp) {
-        uint32_t slot = 0, turn = 0, q_turn = 0, p_turn[2] = {0, 0};
-        auto take = [&]() {  // the next slot, landed
-            wait(&S.full[slot], turn);
-            const uint32_t s = slot;
-            if (++slot == SLOTS) {
-                slot = 0;
-                turn ^= 1;
-            }
-            return s;
-        };
-        auto scores = [&](int g, uint32_t kslot, int qslot) {
-            const uint32_t a = smem_addr(qtile + qslot * Z::kSlotBytes), b = smem_addr(ring + kslot * Z::kSlotBytes);
-#pragma unroll
-            for (int i = 0; i < DP / 16; ++i) {
-                const uint32_t o = i / 4 * Z::kChunk + i % 4 * 32;
-                mma_ss(tmem + g * 256, smem_desc(a + o, 16), smem_desc(b + o, 16), mma_desc<DT>(kTile, false), i > 0);
-            }
-        };
-        auto outputs = [&](int g, uint32_t vslot, bool add) {
-            const uint32_t b = smem_addr(ring + vslot * Z::kSlotBytes);
-#pragma unroll
-            for (int i = 0; i < kTile / 16; ++i)
-                mma_ts(tmem + g * 256 + kTile, tmem + g * 256 + i * 8, smem_desc(b + i * 2048, Z::kChunk),
-                       mma_desc<DT>(DP, true), add || i > 0);
-        };
-        auto p_ready = [&](int g) {
-            wait(&S.p_full[g], p_turn[g]);
-            p_turn[g] ^= 1;
-            tmem_fence_after();
-        };
-        // Rows of V behind the last key: whatever the page (or the slot before) holds there, a weight
-        // of zero must meet a finite value.
-        auto clear_tail = [&](uint32_t vslot, int t, int keys) {
-            const int from = keys - t * kTile;
-            if (from >= kTile)
-                return;
-            char *base = ring + vslot * Z::kSlotBytes;
-            for (int i = from * 8 + lane; i < kTile * 8; i += 32)
-#pragma unroll
-                for (int j = 0; j < DP / 64; ++j)
-                    *reinterpret_cast<uint4 *>(base + j * Z::kChunk + i * 16) = make_uint4(0, 0, 0, 0);
-            fence_proxy_async_shared();
-            __syncwarp();
-        };
-        do {
-            const int keys = block_keys(w.q, p.group, w.b), nt = w.t1 - w.t0;
-            const bool wide = w.rows() > kTile;
-            wait(&S.q_full, q_turn);
-            q_turn ^= 1;
-            tmem_fence_after();
-            for (int t = 0; t <= nt; ++t) {
-                uint32_t kslot = 0, vslot = 0;
-                if (t < nt)
-                    kslot = take();
-                if (!wide && t < nt) {
-                    if (lane == 0 && !S.gave_up) {
-                        scores(t & 1, kslot, 0);
-                        mma_commit(&S.s_full[t & 1]);
-                        mma_commit(&S.empty[kslot]);
-                    }
-                    __syncwarp();
+        if (elect_one()) {
+            const uint64_t q_desc = smem_desc(smem_addr(qtile), 16), k_desc = smem_desc(smem_addr(ring), 16),
+                           v_desc = smem_desc(smem_addr(ring), Z::kChunk);
+            uint32_t slot = 0, turn = 0, p_turn = 0;  // p_turn: a bit per group
+            auto take = [&]() {                       // the next slot, landed
+                wait(&S.full[slot], turn);
+                const uint32_t s = slot;
+                if (++slot == SLOTS) {
+                    slot = 0;
+                    turn ^= 1;
                 }
-                if (t > 0) {
-                    vslot = take();
-                    clear_tail(vslot, w.t0 + t - 1, keys);
+                return s;
+            };
+            auto scores = [&](int g, uint32_t kslot, int qslot) {
+                const uint64_t a = q_desc + qslot * (Z::kSlotBytes >> 4), b = k_desc + kslot * (Z::kSlotBytes >> 4);
+#pragma unroll
+                for (int i = 0; i < DP / 16; ++i) {
+                    const uint32_t o = (i / 4 * Z::kChunk + i % 4 * 32) >> 4;
+                    mma_ss(tmem + g * 256, a + o, b + o, mma_desc<DT>(kTile, false), i > 0);
                 }
-                if (!wide && t > 0) {
-                    const int u = t - 1, g = u & 1;
-                    p_ready(g);
-                    if (lane == 0 && !S.gave_up) {
-                        outputs(g, vslot, u >= 2);
-                        mma_commit(&S.empty[vslot]);
-                        if (u + 2 >= nt)
-                            mma_commit(&S.s_full[g]);
-                    }
-                    __syncwarp();
-                }
-                if (wide) {
-                    for (int g = 0; g < 2; ++g) {
-                        if (t > 0)
-                            p_ready(g);
-                        if (lane == 0 && !S.gave_up) {
-                            if (t > 0)
-                                outputs(g, vslot, t > 1);
-                            if (t < nt)
-                                scores(g, kslot, g);
-                            mma_commit(&S.s_full[g]);
+            };
+            auto outputs = [&](int g, uint32_t vslot, bool add) {
+                const uint64_t b = v_desc + vslot * (Z::kSlotBytes >> 4);
+#pragma unroll
+                for (int i = 0; i < kTile / 16; ++i)
+                    mma_ts(tmem + g * 256 + kTile, tmem + g * 256 + i * 8, b + (i * 2048 >> 4),
+                           mma_desc<DT>(DP, true), i > 0 || add);
+            };
+            auto p_ready = [&](int g) {
+                wait(&S.p_full[g], p_turn >> g & 1);
+                p_turn ^= 1u << g;
+                tmem_fence_after();
+            };
+            for (uint32_t k = 0;; ++k) {
+                if (!announced(k))
+                    break;
+                const Item &item = S.item[k % kItems];
+                const int nt = item.nt, q_use = item.q_use;
+                const bool wide = item.rows > kTile;
+                mbar_arrive(&S.item_empty[k % kItems]);
+                if (nt == 0)
+                    break;
+                for (int g = 0; g <= (int)wide; ++g)
+                    wait(&S.q_full[(q_use + g) & 1], (q_use + g) >> 1 & 1);
+                if (!wide) {
+                    for (int t = 0; t <= nt; ++t) {
+                        if (t < nt) {
+                            const uint32_t kslot = take();
+                            scores(t & 1, kslot, q_use & 1);
+                            mma_commit(&S.s_full[t & 1]);
+                            mma_commit(&S.empty[kslot]);
+                            if (t == nt - 1)
+                                mma_commit(&S.q_empty[q_use & 1]);
                         }
-                        __syncwarp();
+                        if (t > 0) {
+                            const int u = t - 1, g = u & 1;
+                            const uint32_t vslot = take();
+                            p_ready(g);
+                            outputs(g, vslot, u >= 2);
+                            mma_commit(&S.empty[vslot]);
+                            if (u + 2 >= nt)
+                                mma_commit(&S.o_full[g]);
+                        }
                     }
-                    if (lane == 0 && !S.gave_up) {
+                } else {
+                    for (int t = 0; t <= nt; ++t) {
+                        const uint32_t kslot = t < nt ? take() : 0, vslot = t > 0 ? take() : 0;
+                        for (int g = 0; g < 2; ++g) {
+                            if (t > 0) {
+                                p_ready(g);
+                                outputs(g, vslot, t > 1);
+                            }
+                            if (t < nt)
+                                scores(g, kslot, (q_use + g) & 1);
+                            mma_commit(t < nt ? &S.s_full[g] : &S.o_full[g]);
+                        }
                         if (t > 0)
                             mma_commit(&S.empty[vslot]);
                         if (t < nt)
                             mma_commit(&S.empty[kslot]);
+                        if (t == nt - 1) {
+                            mma_commit(&S.q_empty[0]);
+                            mma_commit(&S.q_empty[1]);
+                        }
                     }
-                    __syncwarp();
                 }
-                if (t == nt - 1 && lane == 0 && !S.gave_up)
-                    mma_commit(&S.q_free);
-                __syncwarp();
             }
-        } while (w.next(c, p));
-        // every product is done before the block gives its memory back
-        if (lane == 0) {
+            // every product is done before the block gives its memory back
             mma_commit(&S.done);
             for (uint32_t i = 0; i < kWaitLimit && !mbar_try_wait(&S.done, 0); ++i) {
             }
         }
         __syncwarp();
+    } else if (warp >= kQueryWarp) {
+        Walk w;
+        if (warp == kQueryWarp)
+            w.start(c, p, shares, S.r, S.base);
+        int q_use = 0;
+        uint32_t slots = 0;
+        bool more = true;
+        for (uint32_t k = 0;; ++k) {
+            Item *mine = &S.item[k % kItems];
+            if (warp == kQueryWarp) {
+                if (k >= kItems && !wait(&S.item_empty[k % kItems], (k / kItems & 1) ^ 1))
+                    break;
+                if (lane == 0) {
+                    Item x{};
+                    if (more) {
+                        x.r = w.r;
+                        x.h = w.h;
+                        x.b = w.b;
+                        x.rows = w.rows();
+                        x.nt = w.t1 - w.t0;
+                        x.t0 = w.t0;
+                        x.tiles = w.tiles;
+                        x.keys = block_keys(w.q, p.group, w.b);
+                        x.len = w.q.len;
+                        x.n = w.q.n;
+                        x.first = p.cu[w.r];
+                        x.q_use = q_use;
+                        x.slots = slots;
+                        x.last = shares.owner(w.pos - w.t0 + w.tiles - 1);
+                    }
+                    *mine = x;
+                    mbar_arrive(&S.item_full[k % kItems]);
+                }
+                __syncwarp();
+            } else if (!announced(k)) {
+                break;
+            }
+            const Item item = *mine;
+            if (warp != kQueryWarp)
+                done_with(k);
+            if (item.nt == 0)
+                break;
+            const int count = item.rows > kTile ? 2 : 1;
+            q_use = item.q_use + count;
+            slots = item.slots + 2 * item.nt;
+            constexpr int kVecs = DP / 8, U = 8;
+            for (int g = 0; g < count; ++g) {
+                const int use = item.q_use + g;
+                if (use >= 2)
+                    wait(&S.q_empty[use & 1], (use >> 1 & 1) ^ 1);
+                char *dst = qtile + (use & 1) * Z::kSlotBytes;
+                const int m0 = item.b * kBlockRows + g * kTile, rows = min(kTile, item.rows - g * kTile);
+                for (int i0 = (warp - kQueryWarp) * 32 + lane; i0 < rows * kVecs; i0 += 64 * U) {
+                    uint4 val[U];
+#pragma unroll
+                    for (int j = 0; j < U; ++j) {
+                        const int i = i0 + j * 64, x = i / kVecs, vec = i % kVecs, m = m0 + x;
+                        val[j] = make_uint4(0, 0, 0, 0);
+                        if (i < rows * kVecs && vec * 8 < c.dim)
+                            val[j] = ld_stream(p.q + 2 * ((int64_t)(item.first + m / p.group) * p.q_token +
+                                                          (item.h * p.group + m % p.group) * p.q_head + vec * 8));
+                    }
+#pragma unroll
+                    for (int j = 0; j < U; ++j) {
+                        const int i = i0 + j * 64, x = i / kVecs, vec = i % kVecs;
+                        if (i < rows * kVecs)
+                            *reinterpret_cast<uint4 *>(dst + vec / 8 * Z::kChunk + x * 128 +
+                                                       ((vec % 8) ^ (x % 8)) * 16) = val[j];
+                    }
+                }
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&S.q_full[use & 1]);
+            }
+            if (warp == kQueryWarp)
+                more = w.next(c, p);
+        }
     } else {
         const int g = warp >> 2, row = tid & (kTile - 1), sub = warp & 3;
         const uint32_t lanes = (uint32_t)sub * 32 << 16;
         const uint32_t s_addr = tmem + g * 256 + lanes;
-        uint32_t s_turn = 0, free_turn = 0;
-        bool first = true;
-        do {
-            const int rows = w.rows(), nt = w.t1 - w.t0;
-            const bool wide = rows > kTile;
-            const int m0 = wide ? g * kTile : 0;             // the group's first row in the block
-            const int mine = min(kTile, rows - m0);          // its rows
-            const bool warp_on = sub * 32 < mine, on = row < mine;
-            const int m = w.b * kBlockRows + m0 + row;       // row of the request
-            const int token = m / p.group, head = w.h * p.group + m % p.group;
-            const int64_t first_token = p.cu[w.r];
-            // Q, once the products of the row block before have read it
-            if (!first) {
-                wait(&S.q_free, free_turn);
-                free_turn ^= 1;
-            }
-            first = false;
-            if (wide || g == 0) {
-                char *dst = qtile + (wide ? g : 0) * Z::kSlotBytes;
-                constexpr int kVecs = DP / 8;
-                for (int i = row; i < mine * kVecs; i += kTile) {
-                    const int x = i / kVecs, vec = i % kVecs;
-                    const int mx = w.b * kBlockRows + m0 + x;
-                    uint4 val = make_uint4(0, 0, 0, 0);
-                    if (vec * 8 < c.dim)
-                        val = ld_stream(p.q + 2 * ((first_token + mx / p.group) * p.q_token +
-                                                   (w.h * p.group + mx % p.group) * p.q_head + vec * 8));
-                    *reinterpret_cast<uint4 *>(dst + vec / 8 * Z::kChunk + x * 128 + ((vec % 8) ^ (x % 8)) * 16) = val;
-                }
-                fence_proxy_async_shared();
-            }
+        uint32_t s_turn = 0, o_turn = 0, merge_turn = 0;
+        // all eight softmax warps
+        auto meet = [&]() {
+            tmem_fence_before();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(&S.q_full);
+                mbar_arrive(&S.merge);
+            wait(&S.merge, merge_turn);
+            merge_turn ^= 1;
+            tmem_fence_after();
+        };
+        for (uint32_t k = 0;; ++k) {
+            if (!announced(k))
+                break;
+            const Item item = S.item[k % kItems];
+            done_with(k);
+            const int nt = item.nt;
+            if (nt == 0)
+                break;
+            const bool wide = item.rows > kTile;
+            const int m0 = wide ? g * kTile : 0;             // the group's first row in the block
+            const int mine = min(kTile, item.rows - m0);     // its rows
+            const bool warp_on = sub * 32 < mine, on = row < mine;
+            const int m = item.b * kBlockRows + m0 + row;    // row of the request
+            const int token = m / p.group, head = item.h * p.group + m % p.group;
+
+            const int turns = wide ? nt : (nt - g + 1) / 2;  // this group's tiles
 
             uint32_t bits[kMaxTree / 32] = {};
-            if (p.parent) {
-                int32_t *par = S.group[g].parent;
-                if (row < w.q.n)
-                    par[row] = p.parent[first_token + row];
-                asm volatile("bar.sync %0, 128;" ::"r"(2 + g) : "memory");
+            if (p.parent && turns > 0) {
+                int32_t *par = S.group[g].parent;  // every warp of the group writes the same there
+                for (int i = lane; i < item.n; i += 32)
+                    par[i] = p.parent[item.first + i];
+                __syncwarp();
                 if (on)
                     for (int at = token; at >= 0;) {
 #pragma unroll
@@ -666,44 +793,57 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             bits[j] |= at / 32 == j ? 1u << (at & 31) : 0u;
                         const int up = par[at];
                         if (at == 0 ? up != -1 : up < 0 || up >= at) {
-                            cache_error(c.error, SPEC_DEVERR_TREE, w.r);
+                            cache_error(c.error, SPEC_DEVERR_TREE, item.r);
                             break;
                         }
                         at = up;
                     }
-                asm volatile("bar.sync %0, 128;" ::"r"(2 + g) : "memory");
+                __syncwarp();
             }
             // keys that every row of this warp sees
-            const int all_see = p.parent ? w.q.len
-                                         : w.q.len + (w.b * kBlockRows + m0 + sub * 32) / p.group + 1;
+            const int all_see = p.parent ? item.len
+                                         : item.len + (item.b * kBlockRows + m0 + sub * 32) / p.group + 1;
             float M = -INFINITY, l = 0;
             bool any = false;  // the accumulator holds something
             for (int t = wide ? 0 : g; t < nt; t += wide ? 1 : 2) {
                 wait(&S.s_full[g], s_turn);
                 s_turn ^= 1;
+                const int column = (item.t0 + t) * kTile;
                 if (warp_on) {
                     tmem_fence_after();
-                    float x[kTile];
+                    // 64 columns at a time, read once for the maximum and once for the exponentials:
+                    // a short loop that stays in the instruction cache, and no spills
+                    const bool cut = column + kTile > all_see;
+                    auto columns = [&](int j, float *x) {
+                        tmem_ld32(s_addr + j * 64, x);
+                        tmem_ld32(s_addr + j * 64 + 32, x + 32);
+                        tmem_wait_ld();
+                        if (cut) {
 #pragma unroll
-                    for (int j = 0; j < kTile / 32; ++j)
-                        tmem_ld32(s_addr + j * 32, x + j * 32);
-                    tmem_wait_ld();
-                    const int column = (w.t0 + t) * kTile;
-                    if (column + kTile > all_see) {
+                            for (int i = 0; i < 2; ++i) {
+                                const int col = column + j * 64 + i * 32;
+                                const uint32_t see = p.parent ? tree_columns(bits, item.len, col)
+                                                              : low_bits(item.len + token + 1 - col);
 #pragma unroll
-                        for (int j = 0; j < kTile / 32; ++j) {
-                            const uint32_t see = p.parent ? tree_columns(bits, w.q.len, column + j * 32)
-                                                          : low_bits(w.q.len + token + 1 - column - j * 32);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                x[j * 32 + e] = see >> e & 1 ? x[j * 32 + e] : -INFINITY;
+                                for (int e = 0; e < 32; ++e)
+                                    x[i * 32 + e] = see >> e & 1 ? x[i * 32 + e] : -INFINITY;
+                            }
                         }
-                    }
-                    float top[4] = {x[0], x[1], x[2], x[3]};
+                    };
+                    float mx = -INFINITY;
+#pragma unroll 1
+                    for (int j = 0; j < kTile / 64; ++j) {
+                        float x[64];
+                        columns(j, x);
+                        float top[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int e = 4; e < kTile; ++e)
-                        top[e & 3] = fmaxf(top[e & 3], x[e]);
-                    const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
+                        for (int e = 0; e < 64; e += 8)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                top[i] = max3(top[i], x[e + 2 * i], x[e + 2 * i + 1]);
+                        mx = max3(fmaxf(top[0], top[1]), top[2], top[3]);
+                    }
+                    mx *= p.scale_log2;
                     const bool grown = mx > M + kLazy;  // also from -inf
                     const float f = grown ? ex2(M - mx) : 1.0f;
                     if (grown) {
@@ -724,35 +864,56 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         tmem_wait_st();
                     }
                     any = true;
-                    const float base = M == -INFINITY ? 0.0f : M;
-                    float sum[4] = {0, 0, 0, 0};
+                    const float base = M == -INFINITY ? 0.0f : -M;
+                    const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2), base2 = pack2(base, base);
+                    uint64_t sum[4] = {};
+#pragma unroll 1
+                    for (int j = 0; j < kTile / 64; ++j) {
+                        float x[64];
+                        columns(j, x);
 #pragma unroll
-                    for (int e = 0; e < kTile; e += 2) {
-                        const float a = ex2(fmaf(x[e], p.scale_log2, -base));
-                        const float b = ex2(fmaf(x[e + 1], p.scale_log2, -base));
-                        sum[e / 2 & 3] += a + b;
-                        x[e / 2] = __uint_as_float(from_float2<DT>(a, b));
+                        for (int e = 0; e < 64; e += 2) {
+                            float a, b;
+                            unpack2(fma2(pack2(x[e], x[e + 1]), scale2, base2), a, b);
+                            a = ex2(a);
+                            b = ex2(b);
+                            sum[e / 2 & 3] = add2(sum[e / 2 & 3], pack2(a, b));
+                            x[e / 2] = __uint_as_float(from_float2<DT>(a, b));
+                        }
+                        tmem_st32(s_addr + j * 32, x);
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                    tmem_st32(s_addr, x);
-                    tmem_st32(s_addr + 32, x + 32);
+                    float a, b;
+                    unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
+                    l += a + b;
                     tmem_wait_st();
                     tmem_fence_before();
+                }
+                // Rows of V behind the last key: whatever the page (or the slot before) holds there, a
+                // weight of zero must meet a finite value.
+                const int behind = item.keys - column;
+                if (behind < kTile && (!wide || g == 0)) {
+                    const uint32_t use = item.slots + 2 * nt - 1;  // the share's last slot
+                    wait(&S.full[use % SLOTS], use / SLOTS & 1);
+                    char *base = ring + use % SLOTS * Z::kSlotBytes;
+                    for (int i = behind * 8 + row; i < kTile * 8; i += kTile)
+#pragma unroll
+                        for (int j = 0; j < DP / 64; ++j)
+                            *reinterpret_cast<uint4 *>(base + j * Z::kChunk + i * 16) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_shared();
                 }
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(&S.p_full[g]);
             }
-            const int turns = wide ? nt : (nt - g + 1) / 2;  // this group's tiles
             if (turns > 0) {
-                wait(&S.s_full[g], s_turn);  // its last product
-                s_turn ^= 1;
+                wait(&S.o_full[g], o_turn);  // its last product
+                o_turn ^= 1;
             }
             tmem_fence_after();
-            const bool whole = w.whole();
+            const bool whole = item.t0 == 0 && nt == item.tiles;
             // partial sums: of a row block from before this share (0), or going on behind it (1)
-            const int64_t place = ((int64_t)blockIdx.x * 2 + (w.t0 == 0)) * p.max_rows + m0 + row;
-            char *out = p.out + 2 * ((first_token + token) * p.out_token + head * p.out_head);
+            const int64_t place = ((int64_t)blockIdx.x * 2 + (item.t0 == 0)) * p.max_rows + m0 + row;
+            char *out = p.out + 2 * ((int64_t)(item.first + token) * p.out_token + head * p.out_head);
             auto store = [&](const float *o, int col, float by) {  // 32 columns
                 if (!on)
                     return;
@@ -778,7 +939,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (!whole)
                     p.part_ml[place] = make_float2(M, l);
                 else if (p.lse)
-                    p.lse[(first_token + token) * p.heads + head] = (M + log2f(l)) * 0.69314718055994531f;
+                    p.lse[(int64_t)(item.first + token) * p.heads + head] = (M + log2f(l)) * 0.69314718055994531f;
             };
             if (wide) {
                 if (warp_on) {
@@ -793,9 +954,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 }
             } else {
                 S.group[g].ml[row] = make_float2(M, l);
-                tmem_fence_before();
-                asm volatile("bar.sync 1, 256;" ::: "memory");
-                tmem_fence_after();
+                meet();
                 if (warp_on) {
                     const float2 other = S.group[g ^ 1].ml[row];
                     const float top = fmaxf(M, other.x);
@@ -826,19 +985,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     if (g == 0)
                         store_ml();
                 }
-                tmem_fence_before();
-                asm volatile("bar.sync 1, 256;" ::: "memory");
-                tmem_fence_after();
+                meet();
             }
-            if (!whole && w.t0 == 0 && tid == 0) {
+            if (!whole && item.t0 == 0 && tid == 0) {
                 Partial &x = p.partial[blockIdx.x];
-                x.r = w.r;
-                x.h = w.h;
-                x.b = w.b;
-                x.last = shares.owner(w.pos + w.tiles - 1);
-                x.rows = rows;
+                x.r = item.r;
+                x.h = item.h;
+                x.b = item.b;
+                x.last = item.last;
+                x.rows = item.rows;
             }
-        } while (w.next(c, p));
+        }
         tmem_fence_before();
     }
     __syncthreads();
