@@ -10,9 +10,12 @@
 //                   maximum, exponentials, P back over S.  M only moves when a row's maximum has
 //                   grown by more than 2^8 since (P stays below 2^8, exact in its sum's fp32), so
 //                   the accumulator in tensor memory is rarely rescaled.
-//   warp 8          loads tiles of K and V, page by page, through TMA into a ring of slots
-//   warp 9          issues the matrix products (one thread)
-//   warps 10, 11    walk the list of work ahead of the others, announce it in a ring and load Q
+//   warps 8-11      load tiles of K (8, 9) and V (10, 11), page by page, through TMA into a ring of
+//                   slots; two warps share a tile's copies: one warp cannot issue those of small pages
+//                   fast enough (a streaming loop over 16-token pages reached 3.6 TB/s with one warp
+//                   issuing, 6.0 with two, 6.6 with four)
+//   warp 12         issues the matrix products (one thread)
+//   warps 13-15     walk the list of work ahead of the others, announce it in a ring and load Q
 // A block of more than 128 rows ("wide") gives each group 128 of them and both use every tile: the
 // products of one group run while the other computes its exponentials.  A block of at most 128 rows
 // ("narrow": decoding and most verify steps) gives both groups the same rows and every other tile,
@@ -36,8 +39,9 @@ namespace {
 
 constexpr int kTile = 128;          // keys per tile, and rows per softmax group
 constexpr int kBlockRows = 256;     // query rows of a (request, head, row block)
-constexpr int kSoftmaxWarps = 8, kLoadWarp = 8, kMmaWarp = 9, kQueryWarp = 10;
-constexpr int kAttnThreads = 384;
+constexpr int kSoftmaxWarps = 8, kLoadWarp = 8, kLoadWarps = 4, kMmaWarp = 12, kQueryWarp = 13, kQueryWarps = 3;
+constexpr int kAttnThreads = 512;
+constexpr int kSoftmaxRegs = 144, kOtherRegs = 112;  // 256 threads of each: within the 128 a thread of the launch
 constexpr int kItems = 4;           // row blocks announced ahead
 constexpr int kMaxGrid = 160;       // blocks a call may use (SMs of the device, 152 on GB300)
 constexpr int kMinTiles = 2;        // least tiles of a block's share
@@ -55,7 +59,8 @@ struct AttentionParams {
     char *out;
     float *lse;
     int64_t q_token, q_head, out_token, out_head;  // elements
-    int32_t heads, group, B, box;
+    int32_t heads, group, B;
+    int32_t box;  // tokens per copy
     int64_t N;
     const int32_t *cu, *parent;
     float scale_log2;
@@ -115,7 +120,7 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const float *x)
 
 // Shared-memory matrix descriptor, 128-byte swizzle.  Rows of 128 bytes in groups of 8 (1024 bytes
 // apart: the stride byte offset); `leading` is the distance between 64-element chunks of an operand
-// whose contiguous dimension is not the summed one (V), and unused (1) for Q and K.
+// whose contiguous dimension is not the summed one (V), and unused (16) for Q and K.
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t leading)
 {
     return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(leading >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
@@ -192,6 +197,12 @@ struct alignas(16) Item {
     uint32_t slots;        // K / V slots used before
     int32_t last;          // the last block that works on the row block
 };
+
+// 16 bytes to shared memory, or zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool real)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
 
 // What a block keeps behind the operand tiles.
 template <int SLOTS> struct alignas(16) AttnShared {
@@ -333,7 +344,6 @@ struct Walk {
         return true;
     }
     __device__ __forceinline__ int rows() const { return min(kBlockRows, q.rows - b * kBlockRows); }
-    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
 };
 
 // ---------------------------------------------------------------------------------------
@@ -466,19 +476,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
     if (tid == 0) {
         for (int i = 0; i < SLOTS; ++i) {
-            mbar_init(&S.full[i], 1);
+            mbar_init(&S.full[i], 2);
             mbar_init(&S.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&S.s_full[i], 1);
             mbar_init(&S.p_full[i], 4);
             mbar_init(&S.o_full[i], 1);
-            mbar_init(&S.q_full[i], 2);
+            mbar_init(&S.q_full[i], kQueryWarps);
             mbar_init(&S.q_empty[i], 1);
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&S.item_full[i], 1);
-            mbar_init(&S.item_empty[i], kSoftmaxWarps + 3);  // loads, products, the second query warp
+            mbar_init(&S.item_empty[i], kSoftmaxWarps + kLoadWarps + 1 + kQueryWarps - 1);  // all but the writer
         }
         mbar_init(&S.merge, kSoftmaxWarps);
         mbar_init(&S.done, 1);
@@ -506,74 +516,77 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             mbar_arrive(&S.item_empty[k % kItems]);
     };
 
-    if (warp == kLoadWarp) {
+    if (warp < kSoftmaxWarps)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    else
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+
+    if (warp >= kLoadWarp && warp < kLoadWarp + kLoadWarps) {
         // Slot order: K of tile 0, then K of tile t + 1 and V of tile t, as the products use them.
+        const bool is_v = warp >= kLoadWarp + 2;
+        const int half = warp & 1;  // copies (piece, chunk) of every second number
+        const CUtensorMap *map = is_v ? &vmap : &kmap;
         const int pieces = kTile / p.box;
-        uint32_t slot = 0, turn = 0;  // turn: parity of the slots' next use
-        bool first_turn = true;
-        struct Pages {
-            int page, token;  // of the lane's piece; token < 0: behind the last key
+        // Copies of 32 pieces, one per lane; token < 0: behind the last key.
+        struct Pieces {
+            int page, token;
         };
         for (uint32_t k = 0;; ++k) {
             if (!announced(k))
                 break;
             const Item &item = S.item[k % kItems];
             const int r = item.r, h = item.h, keys = item.keys, t0 = item.t0, nt = item.nt;
+            const uint32_t slots = item.slots;
             done_with(k);
             if (nt == 0)
                 break;
             const int32_t *row = c.table + r * c.table_stride;
-            // The pages of a tile, a piece per lane.  Looked up two tiles ahead: `page` is not looked
-            // at before the tile is loaded.
-            auto lookup = [&](int t) {
-                Pages x{-1, -1};
-                const int at = (t0 + t) * kTile + lane * p.box;
-                if (t < nt && lane < pieces && at < keys) {
+            const int end = min(keys, (t0 + nt) * kTile);
+            // the pieces from number 32 * i of the share's part; looked at 32 pieces later
+            auto lookup = [&](int i) {
+                Pieces x{-1, -1};
+                const int at = t0 * kTile + (i * 32 + lane) * p.box;
+                if (at < end) {
                     const int column = at / c.page_size;
                     x.page = row[column];
                     x.token = at - column * c.page_size;
                 }
                 return x;
             };
-            auto load = [&](const CUtensorMap *map, const Pages &x) {
-                const int count = __popc(__ballot_sync(kFull, x.token >= 0));
-                int page = x.page;
-                if (x.token >= 0 && (page < 0 || page >= c.num_pages)) {
-                    cache_error(c.error, SPEC_DEVERR_PAGE, r);
-                    page = c.num_pages;  // outside the tensor: reads as zeros
-                }
-                if (!first_turn)
-                    wait(&S.empty[slot], turn ^ 1);
-                __syncwarp();
-                if (!S.gave_up) {
-                    const uint32_t dst = smem_addr(ring) + slot * Z::kSlotBytes;
-                    if (elect_one())
-                        mbar_arrive_expect_tx(&S.full[slot], count * p.box * 128 * (DP / 64));
-                    for (int i = 0; i < count; ++i) {
-                        const int pg = __shfl_sync(kFull, page, i), tk = __shfl_sync(kFull, x.token, i);
-                        if (elect_one()) {
-#pragma unroll
-                            for (int j = 0; j < DP / 64; ++j)
-                                tma_box(dst + i * p.box * 128 + j * Z::kChunk, map, j * 64, tk, h, pg, &S.full[slot]);
-                        }
+            const int per = 32 / pieces;  // tiles of 32 pieces
+            Pieces now{-1, -1}, ahead = lookup(0);
+            for (int t = 0; t < nt; ++t) {
+                const int from = t % per * pieces;
+                if (from == 0) {
+                    now = ahead;
+                    ahead = lookup(t / per + 1);
+                    if (now.token >= 0 && (now.page < 0 || now.page >= c.num_pages)) {
+                        cache_error(c.error, SPEC_DEVERR_PAGE, r);
+                        now.page = c.num_pages;  // outside the tensor: reads as zeros
                     }
                 }
+                const uint32_t use = slots + (is_v ? min(2 * t + 2, 2 * nt - 1) : max(2 * t - 1, 0));
+                const uint32_t slot = use % SLOTS, turn = use / SLOTS;
+                const int count = __popc(__ballot_sync(kFull, now.token >= 0) >> from & low_bits(pieces));
+                if (turn > 0)
+                    wait(&S.empty[slot], (turn & 1) ^ 1);
                 __syncwarp();
-                if (++slot == SLOTS) {
-                    slot = 0;
-                    turn ^= 1;
-                    first_turn = false;
+                if (S.gave_up)
+                    continue;
+                const uint32_t dst = smem_addr(ring) + slot * Z::kSlotBytes;
+                uint64_t *bar = &S.full[slot];
+                constexpr int kChunks = DP / 64;
+                const int mine = kChunks == 2 ? count : (count + 1 - half) / 2;
+                if (elect_one())
+                    mbar_arrive_expect_tx(bar, mine * p.box * 128);
+                for (int i = 0; i < mine; ++i) {
+                    const int piece = kChunks == 2 ? i : 2 * i + half, chunk = kChunks == 2 ? half : 0;
+                    const int page = __shfl_sync(kFull, now.page, from + piece);
+                    const int token = __shfl_sync(kFull, now.token, from + piece);
+                    if (elect_one())
+                        tma_box(dst + piece * p.box * 128 + chunk * Z::kChunk, map, chunk * 64, token, h, page, bar);
                 }
-            };
-            Pages now = lookup(0), next = lookup(1);
-            load(&kmap, now);
-            for (int t = 0; t < nt; ++t) {
-                const Pages later = lookup(t + 2);
-                if (t + 1 < nt)
-                    load(&kmap, next);
-                load(&vmap, now);
-                now = next;
-                next = later;
+                __syncwarp();
             }
         }
     } else if (warp == kMmaWarp) {
@@ -715,31 +728,29 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const int count = item.rows > kTile ? 2 : 1;
             q_use = item.q_use + count;
             slots = item.slots + 2 * item.nt;
-            constexpr int kVecs = DP / 8, U = 8;
+            constexpr int kVecs = DP / 8, kStep = 32 * kQueryWarps / kVecs;  // 16-byte units of a row, rows of a turn
             for (int g = 0; g < count; ++g) {
                 const int use = item.q_use + g;
                 if (use >= 2)
                     wait(&S.q_empty[use & 1], (use >> 1 & 1) ^ 1);
-                char *dst = qtile + (use & 1) * Z::kSlotBytes;
+                const int at = (warp - kQueryWarp) * 32 + lane, vec = at % kVecs;
+                const uint32_t dst = smem_addr(qtile) + (use & 1) * Z::kSlotBytes + vec / 8 * Z::kChunk;
                 const int m0 = item.b * kBlockRows + g * kTile, rows = min(kTile, item.rows - g * kTile);
-                for (int i0 = (warp - kQueryWarp) * 32 + lane; i0 < rows * kVecs; i0 += 64 * U) {
-                    uint4 val[U];
-#pragma unroll
-                    for (int j = 0; j < U; ++j) {
-                        const int i = i0 + j * 64, x = i / kVecs, vec = i % kVecs, m = m0 + x;
-                        val[j] = make_uint4(0, 0, 0, 0);
-                        if (i < rows * kVecs && vec * 8 < c.dim)
-                            val[j] = ld_stream(p.q + 2 * ((int64_t)(item.first + m / p.group) * p.q_token +
-                                                          (item.h * p.group + m % p.group) * p.q_head + vec * 8));
-                    }
-#pragma unroll
-                    for (int j = 0; j < U; ++j) {
-                        const int i = i0 + j * 64, x = i / kVecs, vec = i % kVecs;
-                        if (i < rows * kVecs)
-                            *reinterpret_cast<uint4 *>(dst + vec / 8 * Z::kChunk + x * 128 +
-                                                       ((vec % 8) ^ (x % 8)) * 16) = val[j];
+                int x = at / kVecs, token = (m0 + x) / p.group, head = (m0 + x) - token * p.group;
+                const int more_tokens = kStep / p.group, more_heads = kStep % p.group;
+                const char *src = p.q + 2 * ((int64_t)item.first * p.q_token +
+                                             (int64_t)(item.h * p.group) * p.q_head + vec * 8);
+                for (; x < rows; x += kStep) {
+                    copy16(dst + x * 128 + ((vec % 8) ^ (x % 8)) * 16,
+                           vec * 8 < c.dim ? src + 2 * (token * p.q_token + head * p.q_head) : p.q, vec * 8 < c.dim);
+                    token += more_tokens;
+                    head += more_heads;
+                    if (head >= p.group) {
+                        head -= p.group;
+                        ++token;
                     }
                 }
+                asm volatile("cp.async.wait_all;" ::: "memory");
                 fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0)
@@ -1123,19 +1134,21 @@ EncodeTiled encode_tiled()
     return f;
 }
 
-// The pages of one layer as a tensor (head_dim, token, head, page); boxes of 64 elements by `box`
-// tokens, written to shared memory with the 128-byte swizzle that the products read.
+// The pages of one layer as a tensor (head_dim, token, head, page); a copy brings 64 elements of `box`
+// tokens to shared memory, with the 128-byte swizzle that the products read.  What lies behind
+// head_dim reads as zeros.  (One copy for both 64-element halves of a row, through a tensor of five
+// dimensions, halves the copies and was slower: 180 ns per 4 KB copy against 43 ns per 2 KB.)
 bool encode_pages(CUtensorMap *map, const CacheView &c, int dtype, char *base, int box)
 {
     const EncodeTiled f = encode_tiled();
     if (!f)
         return false;
-    const int64_t least = 2 * (int64_t)c.dim;  // any valid stride does for a dimension of size 1
+    const cuuint64_t least = 2 * (cuuint64_t)c.dim;  // any valid stride does for a dimension of size 1
     const cuuint64_t dims[4] = {(cuuint64_t)c.dim, (cuuint64_t)c.page_size, (cuuint64_t)c.heads,
                                 (cuuint64_t)c.num_pages};
-    const cuuint64_t strides[3] = {(cuuint64_t)(c.page_size > 1 ? 2 * c.token_stride : least),
-                                   (cuuint64_t)(c.heads > 1 ? 2 * c.head_stride : least),
-                                   (cuuint64_t)(c.num_pages > 1 ? 2 * c.page_stride : least)};
+    const cuuint64_t strides[3] = {c.page_size > 1 ? 2 * (cuuint64_t)c.token_stride : least,
+                                   c.heads > 1 ? 2 * (cuuint64_t)c.head_stride : least,
+                                   c.num_pages > 1 ? 2 * (cuuint64_t)c.page_stride : least};
     const cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1}, steps[4] = {1, 1, 1, 1};
     return f(map, dtype == SPEC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, base,
              dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
