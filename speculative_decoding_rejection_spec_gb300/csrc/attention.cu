@@ -10,12 +10,14 @@
 //                   maximum, exponentials, P back over S.  M only moves when a row's maximum has
 //                   grown by more than 2^8 since (P stays below 2^8, exact in its sum's fp32), so
 //                   the accumulator in tensor memory is rarely rescaled.
-//   warps 8-11      load tiles of K (8, 9) and V (10, 11), page by page, through TMA into a ring of
-//                   slots; two warps share a tile's copies: one warp cannot issue those of small pages
-//                   fast enough (a streaming loop over 16-token pages reached 3.6 TB/s with one warp
-//                   issuing, 6.0 with two, 6.6 with four)
-//   warp 12         issues the matrix products (one thread)
-//   warps 13-15     walk the list of work ahead of the others, announce it in a ring and load Q
+//   warps 9, 10 / 11, 15  load tiles of K / V, page by page, through TMA into a ring of slots; two
+//                   warps share a tile's copies: one warp cannot issue those of small pages fast enough
+//                   (a streaming loop over 16-token pages reached 3.6 TB/s with one warp issuing, 6.0
+//                   with two, 6.6 with four)
+//   warp 13         issues the matrix products (one thread)
+//   warps 14, 8, 12 load Q; the first walks the list of work ahead of the others and announces it in
+//                   a ring.  Warps 8 and 12 share a scheduler with warps 0 and 4, which have all of the
+//                   softmax's work when a row block has at most 32 rows, so they have the least to do.
 // A block of more than 128 rows ("wide") gives each group 128 of them and both use every tile: the
 // products of one group run while the other computes its exponentials.  A block of at most 128 rows
 // ("narrow": decoding and most verify steps) gives both groups the same rows and every other tile,
@@ -24,7 +26,8 @@
 // their two products take 0.55 us).
 //
 // The work of a call is the list of all (request, head, row block, key tile), cut into equal
-// contiguous shares, one per block, whatever the lengths.  A (request, head, row block) that is cut
+// contiguous shares, one per block, whatever the lengths; each row block counts as kBlockCost tiles
+// more.  A (request, head, row block) that is cut
 // leaves partial sums (O, M, l), which a second kernel joins.
 #include <algorithm>
 
@@ -39,12 +42,13 @@ namespace {
 
 constexpr int kTile = 128;          // keys per tile, and rows per softmax group
 constexpr int kBlockRows = 256;     // query rows of a (request, head, row block)
-constexpr int kSoftmaxWarps = 8, kLoadWarp = 8, kLoadWarps = 4, kMmaWarp = 12, kQueryWarp = 13, kQueryWarps = 3;
+constexpr int kSoftmaxWarps = 8, kLoadWarps = 4, kMmaWarp = 13, kWalkWarp = 14, kQueryWarps = 3;
 constexpr int kAttnThreads = 512;
-constexpr int kSoftmaxRegs = 144, kOtherRegs = 112;  // 256 threads of each: within the 128 a thread of the launch
+constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;  // 256 threads of each: the launch's 128 a thread in all
 constexpr int kItems = 4;           // row blocks announced ahead
 constexpr int kMaxGrid = 160;       // blocks a call may use (SMs of the device, 152 on GB300)
-constexpr int kMinTiles = 2;        // least tiles of a block's share
+constexpr int kBlockCost = 3;       // what beginning and ending a row block costs, in tiles
+constexpr int kMinShare = 2;        // least places of a block's share
 constexpr float kLazy = 8.0f;       // log2 of the growth that moves a row's maximum
 constexpr int kTmemColumns = 512;   // two groups: 128 of S (P over it), up to 128 of O
 
@@ -244,7 +248,8 @@ __device__ __forceinline__ bool attn_wait(uint64_t *bar, uint32_t parity, volati
 // ---------------------------------------------------------------------------------------
 
 struct Request {
-    int n, len, rows, tiles;  // new tokens, committed tokens, query rows, tiles of all its row blocks (one head)
+    int n, len, rows;  // new tokens, committed tokens, query rows
+    int cost;          // of all its row blocks (one head), in tiles
 };
 
 // Tiles of row block b: the keys up to the last row's own.
@@ -259,14 +264,14 @@ __device__ __forceinline__ int block_tiles(const Request &q, int group, int b)
     return (block_keys(q, group, b) + kTile - 1) / kTile;
 }
 
-// The request's sizes; tiles = 0 when there is nothing to do, or an error, which is recorded on demand.
+// The request's sizes; cost = 0 when there is nothing to do, or an error, which is recorded on demand.
 __device__ __forceinline__ Request request_of(const CacheView &c, const AttentionParams &p, int r, bool report)
 {
     Request q;
     q.n = p.cu[r + 1] - p.cu[r];
     q.len = c.lens[r];
     q.rows = q.n * p.group;
-    q.tiles = 0;
+    q.cost = 0;
     if (q.n <= 0)
         return q;
     if (q.len < 0 || (int64_t)q.len + q.n > (int64_t)c.max_pages * c.page_size || (p.parent && q.n > kMaxTree)) {
@@ -275,28 +280,31 @@ __device__ __forceinline__ Request request_of(const CacheView &c, const Attentio
         return q;
     }
     for (int b = 0; b * kBlockRows < q.rows; ++b)
-        q.tiles += block_tiles(q, p.group, b);
+        q.cost += kBlockCost + block_tiles(q, p.group, b);
     return q;
 }
 
-// Tiles of a block's share: [begin(x), begin(x + 1)).
+// A block's share of the list: [begin(x), begin(x + 1)), in tiles of cost.
 struct Shares {
     int64_t total;
     int blocks;
     __device__ __forceinline__ int64_t begin(int x) const { return total * x / blocks; }
-    // the block whose share holds tile t
+    // the block whose share holds place t
     __device__ __forceinline__ int owner(int64_t t) const { return (int)(((t + 1) * blocks - 1) / total); }
 };
 
-// Walks a block's share, one (request, head, row block) at a time; a whole warp.
+// Walks a block's share, one (request, head, row block) at a time; a whole warp.  A row block takes
+// kBlockCost places of the list before those of its tiles; a share that ends within them leaves the
+// row block to the next.
 struct Walk {
     Request q;
     int r, h, b;
     int tiles;        // of this row block
-    int t0, t1;       // those in the share
-    int64_t pos, end; // place in the list
+    int t0, t1;       // those in the share; t1 > t0 but for a share of no tile
+    int64_t pos, end; // place of the row block's part in the list
 
-    __device__ __forceinline__ void start(const CacheView &c, const AttentionParams &p, const Shares &s, int first,
+    // false when the share holds no tile
+    __device__ __forceinline__ bool start(const CacheView &c, const AttentionParams &p, const Shares &s, int first,
                                           int64_t base)
     {
         pos = s.begin(blockIdx.x);
@@ -304,22 +312,27 @@ struct Walk {
         r = first;
         q = request_of(c, p, r, false);
         int64_t at = pos - base;
-        h = (int)(at / q.tiles);
-        at %= q.tiles;
-        for (b = 0; at >= block_tiles(q, p.group, b); ++b)
-            at -= block_tiles(q, p.group, b);
-        here(p, (int)at);
+        h = (int)(at / q.cost);
+        at %= q.cost;
+        for (b = 0; at >= kBlockCost + block_tiles(q, p.group, b); ++b)
+            at -= kBlockCost + block_tiles(q, p.group, b);
+        return here(p, (int)at);
     }
-    __device__ __forceinline__ void here(const AttentionParams &p, int from)
+    // the part of the row block from its place `from` on
+    __device__ __forceinline__ bool here(const AttentionParams &p, int from)
     {
         tiles = block_tiles(q, p.group, b);
-        t0 = from;
-        t1 = (int)min((int64_t)tiles, from + (end - pos));
+        const int to = (int)min((int64_t)(kBlockCost + tiles), from + (end - pos));
+        t0 = max(from - kBlockCost, 0);
+        t1 = max(to - kBlockCost, 0);
+        pos += to - from;
+        return t1 > t0;
     }
+    // place of the row block's last tile
+    __device__ __forceinline__ int64_t last_place() const { return pos + (tiles - t1) - 1; }
     // to the next row block; false at the share's end
     __device__ __forceinline__ bool next(const CacheView &c, const AttentionParams &p)
     {
-        pos += t1 - t0;
         if (pos >= end)
             return false;
         if (++b * kBlockRows >= q.rows) {
@@ -328,7 +341,7 @@ struct Walk {
                 h = 0;
                 const int lane = threadIdx.x & 31;
                 for (++r;; r += 32) {
-                    const bool some = r + lane < p.B && request_of(c, p, r + lane, false).tiles > 0;
+                    const bool some = r + lane < p.B && request_of(c, p, r + lane, false).cost > 0;
                     const unsigned any = __ballot_sync(kFull, some);
                     if (any) {
                         r += __ffs(any) - 1;
@@ -340,8 +353,7 @@ struct Walk {
                 q = request_of(c, p, r, false);
             }
         }
-        here(p, 0);
-        return true;
+        return here(p, 0);
     }
     __device__ __forceinline__ int rows() const { return min(kBlockRows, q.rows - b * kBlockRows); }
 };
@@ -431,40 +443,48 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (blockIdx.x == 0 && tid == 0)
             cache_error(c.error, SPEC_DEVERR_LAYOUT, -1);
     } else {
+        // twice: the total makes the shares, then each block finds its own; a batch of no more
+        // requests than threads keeps its sums in between
+        int64_t mine = 0, at = 0;
         for (int pass = 0; pass < 2; ++pass) {
             int64_t before = 0;
             for (int r0 = 0; r0 < p.B; r0 += kAttnThreads) {
                 const int r = r0 + tid;
-                int64_t mine = 0;
-                if (r < p.B)
-                    mine = (int64_t)request_of(c, p, r, pass == 0 && blockIdx.x == 0).tiles * c.heads;
-                int64_t incl = mine;
+                if (pass == 0 || p.B > kAttnThreads) {
+                    mine = 0;
+                    if (r < p.B)
+                        mine = (int64_t)request_of(c, p, r, pass == 0 && blockIdx.x == 0).cost * c.heads;
+                    int64_t incl = mine;
 #pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const int64_t y = __shfl_up_sync(kFull, incl, d);
-                    incl += lane >= d ? y : 0;
-                }
-                __syncthreads();
-                if (lane == 31)
-                    S.group[0].sums[warp] = incl;
-                __syncthreads();
-                int64_t all = 0, lower = 0;
+                    for (int d = 1; d < 32; d <<= 1) {
+                        const int64_t y = __shfl_up_sync(kFull, incl, d);
+                        incl += lane >= d ? y : 0;
+                    }
+                    __syncthreads();
+                    if (lane == 31)
+                        S.group[0].sums[warp] = incl;
+                    __syncthreads();
+                    int64_t all = 0, lower = 0;
 #pragma unroll
-                for (int i = 0; i < kAttnThreads / 32; ++i) {
-                    lower += i < warp ? S.group[0].sums[i] : 0;
-                    all += S.group[0].sums[i];
+                    for (int i = 0; i < kAttnThreads / 32; ++i) {
+                        lower += i < warp ? S.group[0].sums[i] : 0;
+                        all += S.group[0].sums[i];
+                    }
+                    at = before + lower + incl - mine;
+                    before += all;
                 }
                 if (pass == 1) {
-                    const int64_t at = before + lower + incl - mine, want = shares.begin(blockIdx.x);
+                    const int64_t want = shares.begin(blockIdx.x);
                     if (mine > 0 && at <= want && want < at + mine) {
                         S.r = r;
                         S.base = at;
                     }
                 }
-                before += all;
             }
+            if (pass == 1)
+                break;
             shares.total = before;
-            shares.blocks = (int)max((int64_t)1, min((int64_t)gridDim.x, (before + kMinTiles - 1) / kMinTiles));
+            shares.blocks = (int)max((int64_t)1, min((int64_t)gridDim.x, (before + kMinShare - 1) / kMinShare));
             if (blockIdx.x >= shares.blocks || before == 0)
                 break;
         }
@@ -516,250 +536,252 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             mbar_arrive(&S.item_empty[k % kItems]);
     };
 
-    if (warp < kSoftmaxWarps)
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    else
+    // A warpgroup sets its registers together; the roles that follow are compiled for that number.
+    if (warp >= kSoftmaxWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-
-    if (warp >= kLoadWarp && warp < kLoadWarp + kLoadWarps) {
-        // Slot order: K of tile 0, then K of tile t + 1 and V of tile t, as the products use them.
-        const bool is_v = warp >= kLoadWarp + 2;
-        const int half = warp & 1;  // copies (piece, chunk) of every second number
-        const CUtensorMap *map = is_v ? &vmap : &kmap;
-        const int pieces = kTile / p.box;
-        // Copies of 32 pieces, one per lane; token < 0: behind the last key.
-        struct Pieces {
-            int page, token;
-        };
-        for (uint32_t k = 0;; ++k) {
-            if (!announced(k))
-                break;
-            const Item &item = S.item[k % kItems];
-            const int r = item.r, h = item.h, keys = item.keys, t0 = item.t0, nt = item.nt;
-            const uint32_t slots = item.slots;
-            done_with(k);
-            if (nt == 0)
-                break;
-            const int32_t *row = c.table + r * c.table_stride;
-            const int end = min(keys, (t0 + nt) * kTile);
-            // the pieces from number 32 * i of the share's part; looked at 32 pieces later
-            auto lookup = [&](int i) {
-                Pieces x{-1, -1};
-                const int at = t0 * kTile + (i * 32 + lane) * p.box;
-                if (at < end) {
-                    const int column = at / c.page_size;
-                    x.page = row[column];
-                    x.token = at - column * c.page_size;
-                }
-                return x;
-            };
-            const int per = 32 / pieces;  // tiles of 32 pieces
-            Pieces now{-1, -1}, ahead = lookup(0);
-            for (int t = 0; t < nt; ++t) {
-                const int from = t % per * pieces;
-                if (from == 0) {
-                    now = ahead;
-                    ahead = lookup(t / per + 1);
-                    if (now.token >= 0 && (now.page < 0 || now.page >= c.num_pages)) {
-                        cache_error(c.error, SPEC_DEVERR_PAGE, r);
-                        now.page = c.num_pages;  // outside the tensor: reads as zeros
-                    }
-                }
-                const uint32_t use = slots + (is_v ? min(2 * t + 2, 2 * nt - 1) : max(2 * t - 1, 0));
-                const uint32_t slot = use % SLOTS, turn = use / SLOTS;
-                const int count = __popc(__ballot_sync(kFull, now.token >= 0) >> from & low_bits(pieces));
-                if (turn > 0)
-                    wait(&S.empty[slot], (turn & 1) ^ 1);
-                __syncwarp();
-                if (S.gave_up)
-                    continue;
-                const uint32_t dst = smem_addr(ring) + slot * Z::kSlotBytes;
-                uint64_t *bar = &S.full[slot];
-                constexpr int kChunks = DP / 64;
-                const int mine = kChunks == 2 ? count : (count + 1 - half) / 2;
-                if (elect_one())
-                    mbar_arrive_expect_tx(bar, mine * p.box * 128);
-                for (int i = 0; i < mine; ++i) {
-                    const int piece = kChunks == 2 ? i : 2 * i + half, chunk = kChunks == 2 ? half : 0;
-                    const int page = __shfl_sync(kFull, now.page, from + piece);
-                    const int token = __shfl_sync(kFull, now.token, from + piece);
-                    if (elect_one())
-                        tma_box(dst + piece * p.box * 128 + chunk * Z::kChunk, map, chunk * 64, token, h, page, bar);
-                }
-                __syncwarp();
-            }
-        }
-    } else if (warp == kMmaWarp) {
-        if (elect_one()) {
-            const uint64_t q_desc = smem_desc(smem_addr(qtile), 16), k_desc = smem_desc(smem_addr(ring), 16),
-                           v_desc = smem_desc(smem_addr(ring), Z::kChunk);
-            uint32_t slot = 0, turn = 0, p_turn = 0;  // p_turn: a bit per group
-            auto take = [&]() {                       // the next slot, landed
-                wait(&S.full[slot], turn);
-                const uint32_t s = slot;
-                if (++slot == SLOTS) {
-                    slot = 0;
-                    turn ^= 1;
-                }
-                return s;
-            };
-            auto scores = [&](int g, uint32_t kslot, int qslot) {
-                const uint64_t a = q_desc + qslot * (Z::kSlotBytes >> 4), b = k_desc + kslot * (Z::kSlotBytes >> 4);
-#pragma unroll
-                for (int i = 0; i < DP / 16; ++i) {
-                    const uint32_t o = (i / 4 * Z::kChunk + i % 4 * 32) >> 4;
-                    mma_ss(tmem + g * 256, a + o, b + o, mma_desc<DT>(kTile, false), i > 0);
-                }
-            };
-            auto outputs = [&](int g, uint32_t vslot, bool add) {
-                const uint64_t b = v_desc + vslot * (Z::kSlotBytes >> 4);
-#pragma unroll
-                for (int i = 0; i < kTile / 16; ++i)
-                    mma_ts(tmem + g * 256 + kTile, tmem + g * 256 + i * 8, b + (i * 2048 >> 4),
-                           mma_desc<DT>(DP, true), i > 0 || add);
-            };
-            auto p_ready = [&](int g) {
-                wait(&S.p_full[g], p_turn >> g & 1);
-                p_turn ^= 1u << g;
-                tmem_fence_after();
+        const int load_warp = warp == 15 ? 3 : warp - 9;  // 0, 1: K; 2, 3: V
+        if (load_warp >= 0 && load_warp < kLoadWarps && warp != 12) {
+            // Slot order: K of tile 0, then K of tile t + 1 and V of tile t, as the products use them.
+            const bool is_v = load_warp >= 2;
+            const int half = load_warp & 1;  // copies (piece, chunk) of every second number
+            const CUtensorMap *map = is_v ? &vmap : &kmap;
+            const int pieces = kTile / p.box;
+            // Copies of 32 pieces, one per lane; token < 0: behind the last key.
+            struct Pieces {
+                int page, token;
             };
             for (uint32_t k = 0;; ++k) {
                 if (!announced(k))
                     break;
                 const Item &item = S.item[k % kItems];
-                const int nt = item.nt, q_use = item.q_use;
-                const bool wide = item.rows > kTile;
-                mbar_arrive(&S.item_empty[k % kItems]);
+                const int r = item.r, h = item.h, keys = item.keys, t0 = item.t0, nt = item.nt;
+                const uint32_t slots = item.slots;
+                done_with(k);
                 if (nt == 0)
                     break;
-                for (int g = 0; g <= (int)wide; ++g)
-                    wait(&S.q_full[(q_use + g) & 1], (q_use + g) >> 1 & 1);
-                if (!wide) {
-                    for (int t = 0; t <= nt; ++t) {
-                        if (t < nt) {
-                            const uint32_t kslot = take();
-                            scores(t & 1, kslot, q_use & 1);
-                            mma_commit(&S.s_full[t & 1]);
-                            mma_commit(&S.empty[kslot]);
-                            if (t == nt - 1)
-                                mma_commit(&S.q_empty[q_use & 1]);
-                        }
-                        if (t > 0) {
-                            const int u = t - 1, g = u & 1;
-                            const uint32_t vslot = take();
-                            p_ready(g);
-                            outputs(g, vslot, u >= 2);
-                            mma_commit(&S.empty[vslot]);
-                            if (u + 2 >= nt)
-                                mma_commit(&S.o_full[g]);
+                const int32_t *row = c.table + r * c.table_stride;
+                const int end = min(keys, (t0 + nt) * kTile);
+                // the pieces from number 32 * i of the share's part; looked at 32 pieces later
+                auto lookup = [&](int i) {
+                    Pieces x{-1, -1};
+                    const int at = t0 * kTile + (i * 32 + lane) * p.box;
+                    if (at < end) {
+                        const int column = at / c.page_size;
+                        x.page = row[column];
+                        x.token = at - column * c.page_size;
+                    }
+                    return x;
+                };
+                const int per = 32 / pieces;  // tiles of 32 pieces
+                Pieces now{-1, -1}, ahead = lookup(0);
+                for (int t = 0; t < nt; ++t) {
+                    const int from = t % per * pieces;
+                    if (from == 0) {
+                        now = ahead;
+                        ahead = lookup(t / per + 1);
+                        if (now.token >= 0 && (now.page < 0 || now.page >= c.num_pages)) {
+                            cache_error(c.error, SPEC_DEVERR_PAGE, r);
+                            now.page = c.num_pages;  // outside the tensor: reads as zeros
                         }
                     }
-                } else {
-                    for (int t = 0; t <= nt; ++t) {
-                        const uint32_t kslot = t < nt ? take() : 0, vslot = t > 0 ? take() : 0;
-                        for (int g = 0; g < 2; ++g) {
-                            if (t > 0) {
-                                p_ready(g);
-                                outputs(g, vslot, t > 1);
+                    const uint32_t use = slots + (is_v ? min(2 * t + 2, 2 * nt - 1) : max(2 * t - 1, 0));
+                    const uint32_t slot = use % SLOTS, turn = use / SLOTS;
+                    const int count = __popc(__ballot_sync(kFull, now.token >= 0) >> from & low_bits(pieces));
+                    if (turn > 0)
+                        wait(&S.empty[slot], (turn & 1) ^ 1);
+                    __syncwarp();
+                    if (S.gave_up)
+                        continue;
+                    const uint32_t dst = smem_addr(ring) + slot * Z::kSlotBytes;
+                    uint64_t *bar = &S.full[slot];
+                    constexpr int kChunks = DP / 64;
+                    const int mine = kChunks == 2 ? count : (count + 1 - half) / 2;
+                    if (elect_one())
+                        mbar_arrive_expect_tx(bar, mine * p.box * 128);
+                    for (int i = 0; i < mine; ++i) {
+                        const int piece = kChunks == 2 ? i : 2 * i + half, chunk = kChunks == 2 ? half : 0;
+                        const int page = __shfl_sync(kFull, now.page, from + piece);
+                        const int token = __shfl_sync(kFull, now.token, from + piece);
+                        if (elect_one())
+                            tma_box(dst + piece * p.box * 128 + chunk * Z::kChunk, map, chunk * 64, token, h, page, bar);
+                    }
+                    __syncwarp();
+                }
+            }
+        } else if (warp == kMmaWarp) {
+            if (elect_one()) {
+                const uint64_t q_desc = smem_desc(smem_addr(qtile), 16), k_desc = smem_desc(smem_addr(ring), 16),
+                               v_desc = smem_desc(smem_addr(ring), Z::kChunk);
+                uint32_t slot = 0, turn = 0, p_turn = 0;  // p_turn: a bit per group
+                auto take = [&]() {                       // the next slot, landed
+                    wait(&S.full[slot], turn);
+                    const uint32_t s = slot;
+                    if (++slot == SLOTS) {
+                        slot = 0;
+                        turn ^= 1;
+                    }
+                    return s;
+                };
+                auto scores = [&](int g, uint32_t kslot, int qslot) {
+                    const uint64_t a = q_desc + qslot * (Z::kSlotBytes >> 4), b = k_desc + kslot * (Z::kSlotBytes >> 4);
+#pragma unroll
+                    for (int i = 0; i < DP / 16; ++i) {
+                        const uint32_t o = (i / 4 * Z::kChunk + i % 4 * 32) >> 4;
+                        mma_ss(tmem + g * 256, a + o, b + o, mma_desc<DT>(kTile, false), i > 0);
+                    }
+                };
+                auto outputs = [&](int g, uint32_t vslot, bool add) {
+                    const uint64_t b = v_desc + vslot * (Z::kSlotBytes >> 4);
+#pragma unroll
+                    for (int i = 0; i < kTile / 16; ++i)
+                        mma_ts(tmem + g * 256 + kTile, tmem + g * 256 + i * 8, b + (i * 2048 >> 4),
+                               mma_desc<DT>(DP, true), i > 0 || add);
+                };
+                auto p_ready = [&](int g) {
+                    wait(&S.p_full[g], p_turn >> g & 1);
+                    p_turn ^= 1u << g;
+                    tmem_fence_after();
+                };
+                for (uint32_t k = 0;; ++k) {
+                    if (!announced(k))
+                        break;
+                    const Item &item = S.item[k % kItems];
+                    const int nt = item.nt, q_use = item.q_use;
+                    const bool wide = item.rows > kTile;
+                    mbar_arrive(&S.item_empty[k % kItems]);
+                    if (nt == 0)
+                        break;
+                    for (int g = 0; g <= (int)wide; ++g)
+                        wait(&S.q_full[(q_use + g) & 1], (q_use + g) >> 1 & 1);
+                    if (!wide) {
+                        for (int t = 0; t <= nt; ++t) {
+                            if (t < nt) {
+                                const uint32_t kslot = take();
+                                scores(t & 1, kslot, q_use & 1);
+                                mma_commit(&S.s_full[t & 1]);
+                                mma_commit(&S.empty[kslot]);
+                                if (t == nt - 1)
+                                    mma_commit(&S.q_empty[q_use & 1]);
                             }
+                            if (t > 0) {
+                                const int u = t - 1, g = u & 1;
+                                const uint32_t vslot = take();
+                                p_ready(g);
+                                outputs(g, vslot, u >= 2);
+                                mma_commit(&S.empty[vslot]);
+                                if (u + 2 >= nt)
+                                    mma_commit(&S.o_full[g]);
+                            }
+                        }
+                    } else {
+                        for (int t = 0; t <= nt; ++t) {
+                            const uint32_t kslot = t < nt ? take() : 0, vslot = t > 0 ? take() : 0;
+                            for (int g = 0; g < 2; ++g) {
+                                if (t > 0) {
+                                    p_ready(g);
+                                    outputs(g, vslot, t > 1);
+                                }
+                                if (t < nt)
+                                    scores(g, kslot, (q_use + g) & 1);
+                                mma_commit(t < nt ? &S.s_full[g] : &S.o_full[g]);
+                            }
+                            if (t > 0)
+                                mma_commit(&S.empty[vslot]);
                             if (t < nt)
-                                scores(g, kslot, (q_use + g) & 1);
-                            mma_commit(t < nt ? &S.s_full[g] : &S.o_full[g]);
-                        }
-                        if (t > 0)
-                            mma_commit(&S.empty[vslot]);
-                        if (t < nt)
-                            mma_commit(&S.empty[kslot]);
-                        if (t == nt - 1) {
-                            mma_commit(&S.q_empty[0]);
-                            mma_commit(&S.q_empty[1]);
+                                mma_commit(&S.empty[kslot]);
+                            if (t == nt - 1) {
+                                mma_commit(&S.q_empty[0]);
+                                mma_commit(&S.q_empty[1]);
+                            }
                         }
                     }
                 }
+                // every product is done before the block gives its memory back
+                mma_commit(&S.done);
+                for (uint32_t i = 0; i < kWaitLimit && !mbar_try_wait(&S.done, 0); ++i) {
+                }
             }
-            // every product is done before the block gives its memory back
-            mma_commit(&S.done);
-            for (uint32_t i = 0; i < kWaitLimit && !mbar_try_wait(&S.done, 0); ++i) {
-            }
-        }
-        __syncwarp();
-    } else if (warp >= kQueryWarp) {
-        Walk w;
-        if (warp == kQueryWarp)
-            w.start(c, p, shares, S.r, S.base);
-        int q_use = 0;
-        uint32_t slots = 0;
-        bool more = true;
-        for (uint32_t k = 0;; ++k) {
-            Item *mine = &S.item[k % kItems];
-            if (warp == kQueryWarp) {
-                if (k >= kItems && !wait(&S.item_empty[k % kItems], (k / kItems & 1) ^ 1))
+            __syncwarp();
+        } else {
+            Walk w;
+            const int part = warp == kWalkWarp ? 0 : warp == 8 ? 1 : 2;
+            int q_use = 0;
+            uint32_t slots = 0;
+            bool more = false;
+            if (warp == kWalkWarp)
+                more = w.start(c, p, shares, S.r, S.base) || w.next(c, p);
+            for (uint32_t k = 0;; ++k) {
+                Item *mine = &S.item[k % kItems];
+                if (warp == kWalkWarp) {
+                    if (k >= kItems && !wait(&S.item_empty[k % kItems], (k / kItems & 1) ^ 1))
+                        break;
+                    if (lane == 0) {
+                        Item x{};
+                        if (more) {
+                            x.r = w.r;
+                            x.h = w.h;
+                            x.b = w.b;
+                            x.rows = w.rows();
+                            x.nt = w.t1 - w.t0;
+                            x.t0 = w.t0;
+                            x.tiles = w.tiles;
+                            x.keys = block_keys(w.q, p.group, w.b);
+                            x.len = w.q.len;
+                            x.n = w.q.n;
+                            x.first = p.cu[w.r];
+                            x.q_use = q_use;
+                            x.slots = slots;
+                            x.last = shares.owner(w.last_place());
+                        }
+                        *mine = x;
+                        mbar_arrive(&S.item_full[k % kItems]);
+                    }
+                    __syncwarp();
+                } else if (!announced(k)) {
                     break;
-                if (lane == 0) {
-                    Item x{};
-                    if (more) {
-                        x.r = w.r;
-                        x.h = w.h;
-                        x.b = w.b;
-                        x.rows = w.rows();
-                        x.nt = w.t1 - w.t0;
-                        x.t0 = w.t0;
-                        x.tiles = w.tiles;
-                        x.keys = block_keys(w.q, p.group, w.b);
-                        x.len = w.q.len;
-                        x.n = w.q.n;
-                        x.first = p.cu[w.r];
-                        x.q_use = q_use;
-                        x.slots = slots;
-                        x.last = shares.owner(w.pos - w.t0 + w.tiles - 1);
-                    }
-                    *mine = x;
-                    mbar_arrive(&S.item_full[k % kItems]);
                 }
-                __syncwarp();
-            } else if (!announced(k)) {
-                break;
-            }
-            const Item item = *mine;
-            if (warp != kQueryWarp)
-                done_with(k);
-            if (item.nt == 0)
-                break;
-            const int count = item.rows > kTile ? 2 : 1;
-            q_use = item.q_use + count;
-            slots = item.slots + 2 * item.nt;
-            constexpr int kVecs = DP / 8, kStep = 32 * kQueryWarps / kVecs;  // 16-byte units of a row, rows of a turn
-            for (int g = 0; g < count; ++g) {
-                const int use = item.q_use + g;
-                if (use >= 2)
-                    wait(&S.q_empty[use & 1], (use >> 1 & 1) ^ 1);
-                const int at = (warp - kQueryWarp) * 32 + lane, vec = at % kVecs;
-                const uint32_t dst = smem_addr(qtile) + (use & 1) * Z::kSlotBytes + vec / 8 * Z::kChunk;
-                const int m0 = item.b * kBlockRows + g * kTile, rows = min(kTile, item.rows - g * kTile);
-                int x = at / kVecs, token = (m0 + x) / p.group, head = (m0 + x) - token * p.group;
-                const int more_tokens = kStep / p.group, more_heads = kStep % p.group;
-                const char *src = p.q + 2 * ((int64_t)item.first * p.q_token +
-                                             (int64_t)(item.h * p.group) * p.q_head + vec * 8);
-                for (; x < rows; x += kStep) {
-                    copy16(dst + x * 128 + ((vec % 8) ^ (x % 8)) * 16,
-                           vec * 8 < c.dim ? src + 2 * (token * p.q_token + head * p.q_head) : p.q, vec * 8 < c.dim);
-                    token += more_tokens;
-                    head += more_heads;
-                    if (head >= p.group) {
-                        head -= p.group;
-                        ++token;
+                const Item item = *mine;
+                if (warp != kWalkWarp)
+                    done_with(k);
+                if (item.nt == 0)
+                    break;
+                const int count = item.rows > kTile ? 2 : 1;
+                q_use = item.q_use + count;
+                slots = item.slots + 2 * item.nt;
+                constexpr int kVecs = DP / 8, kStep = 32 * kQueryWarps / kVecs;  // 16-byte units of a row, rows of a turn
+                for (int g = 0; g < count; ++g) {
+                    const int use = item.q_use + g;
+                    if (use >= 2)
+                        wait(&S.q_empty[use & 1], (use >> 1 & 1) ^ 1);
+                    const int at = part * 32 + lane, vec = at % kVecs;
+                    const uint32_t dst = smem_addr(qtile) + (use & 1) * Z::kSlotBytes + vec / 8 * Z::kChunk;
+                    const int m0 = item.b * kBlockRows + g * kTile, rows = min(kTile, item.rows - g * kTile);
+                    int x = at / kVecs, token = (m0 + x) / p.group, head = (m0 + x) - token * p.group;
+                    const int more_tokens = kStep / p.group, more_heads = kStep % p.group;
+                    const char *src = p.q + 2 * ((int64_t)item.first * p.q_token +
+                                                 (int64_t)(item.h * p.group) * p.q_head + vec * 8);
+                    for (; x < rows; x += kStep) {
+                        copy16(dst + x * 128 + ((vec % 8) ^ (x % 8)) * 16,
+                               vec * 8 < c.dim ? src + 2 * (token * p.q_token + head * p.q_head) : p.q, vec * 8 < c.dim);
+                        token += more_tokens;
+                        head += more_heads;
+                        if (head >= p.group) {
+                            head -= p.group;
+                            ++token;
+                        }
                     }
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    fence_proxy_async_shared();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&S.q_full[use & 1]);
                 }
-                asm volatile("cp.async.wait_all;" ::: "memory");
-                fence_proxy_async_shared();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&S.q_full[use & 1]);
+                if (warp == kWalkWarp)
+                    more = w.next(c, p);
             }
-            if (warp == kQueryWarp)
-                more = w.next(c, p);
         }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         const int g = warp >> 2, row = tid & (kTile - 1), sub = warp & 3;
         const uint32_t lanes = (uint32_t)sub * 32 << 16;
         const uint32_t s_addr = tmem + g * 256 + lanes;
@@ -822,38 +844,40 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 const int column = (item.t0 + t) * kTile;
                 if (warp_on) {
                     tmem_fence_after();
-                    // 64 columns at a time, read once for the maximum and once for the exponentials:
-                    // a short loop that stays in the instruction cache, and no spills
+                    // the second half is on its way while the first is looked at
+                    float x[kTile];
                     const bool cut = column + kTile > all_see;
-                    auto columns = [&](int j, float *x) {
-                        tmem_ld32(s_addr + j * 64, x);
-                        tmem_ld32(s_addr + j * 64 + 32, x + 32);
-                        tmem_wait_ld();
-                        if (cut) {
+                    auto mask = [&](int from) {  // 64 columns
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const int col = column + j * 64 + i * 32;
-                                const uint32_t see = p.parent ? tree_columns(bits, item.len, col)
-                                                              : low_bits(item.len + token + 1 - col);
+                        for (int i = from; i < from + 64; i += 32) {
+                            const uint32_t see = p.parent ? tree_columns(bits, item.len, column + i)
+                                                          : low_bits(item.len + token + 1 - column - i);
 #pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    x[i * 32 + e] = see >> e & 1 ? x[i * 32 + e] : -INFINITY;
-                            }
+                            for (int e = 0; e < 32; ++e)
+                                x[i + e] = see >> e & 1 ? x[i + e] : -INFINITY;
                         }
                     };
-                    float mx = -INFINITY;
-#pragma unroll 1
-                    for (int j = 0; j < kTile / 64; ++j) {
-                        float x[64];
-                        columns(j, x);
-                        float top[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
+                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    auto maximum = [&](int from) {
 #pragma unroll
-                        for (int e = 0; e < 64; e += 8)
+                        for (int e = from; e < from + 64; e += 8)
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 top[i] = max3(top[i], x[e + 2 * i], x[e + 2 * i + 1]);
-                        mx = max3(fmaxf(top[0], top[1]), top[2], top[3]);
-                    }
+                    };
+                    tmem_ld32(s_addr, x);
+                    tmem_ld32(s_addr + 32, x + 32);
+                    tmem_wait_ld();
+                    tmem_ld32(s_addr + 64, x + 64);
+                    tmem_ld32(s_addr + 96, x + 96);
+                    if (cut)
+                        mask(0);
+                    maximum(0);
+                    tmem_wait_ld();
+                    if (cut)
+                        mask(64);
+                    maximum(64);
+                    float mx = max3(fmaxf(top[0], top[1]), top[2], top[3]);
                     mx *= p.scale_log2;
                     const bool grown = mx > M + kLazy;  // also from -inf
                     const float f = grown ? ex2(M - mx) : 1.0f;
@@ -878,12 +902,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     const float base = M == -INFINITY ? 0.0f : -M;
                     const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2), base2 = pack2(base, base);
                     uint64_t sum[4] = {};
-#pragma unroll 1
-                    for (int j = 0; j < kTile / 64; ++j) {
-                        float x[64];
-                        columns(j, x);
 #pragma unroll
-                        for (int e = 0; e < 64; e += 2) {
+                    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                        for (int e = j * 64; e < j * 64 + 64; e += 2) {
                             float a, b;
                             unpack2(fma2(pack2(x[e], x[e + 1]), scale2, base2), a, b);
                             a = ex2(a);
@@ -891,7 +913,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             sum[e / 2 & 3] = add2(sum[e / 2 & 3], pack2(a, b));
                             x[e / 2] = __uint_as_float(from_float2<DT>(a, b));
                         }
-                        tmem_st32(s_addr + j * 32, x);
+                        tmem_st32(s_addr + j * 32, x + j * 32);
                     }
                     float a, b;
                     unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
@@ -1010,7 +1032,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         tmem_fence_before();
     }
     __syncthreads();
-    if (warp == kLoadWarp && S.gave_up) {
+    if (warp == 9 && S.gave_up) {
         // copies that nobody waited for; a slot that none was started into waits in vain, for a while
         for (int i = 0; i < SLOTS; ++i)
             for (uint32_t n = 0; n < 4096 && !(mbar_try_wait(&S.full[i], 0) && mbar_try_wait(&S.full[i], 1)); ++n) {
@@ -1024,16 +1046,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
 }
 
-// Joins the partial sums of the row blocks that were cut: blocks (share, 8 rows), a warp per row.
-template <int DT, int DP>
+// Joins the partial sums of the row blocks that were cut: blocks (share, 8 / W rows), W warps per row,
+// each for every W-th part.  Row blocks of many rows are cut into few parts (one warp per row), those of
+// few rows into as many as there are SMs (four: 38 parts of 48 rows took 15 us with one, 6 with four);
+// with four, the 19456 blocks that 256 rows need cost 14 us though most have nothing to do.
+template <int DT, int DP, int W>
 __global__ void __launch_bounds__(256) join_kernel(CacheView c, AttentionParams p)
 {
+    __shared__ float4 sums[8][32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Partial x = p.partial[blockIdx.x];
-    const int lane = threadIdx.x & 31, row = blockIdx.y * 8 + (threadIdx.x >> 5);
-    if (row >= x.rows)
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp % W;
+    const int row = blockIdx.y * (8 / W) + warp / W;
+    if (blockIdx.y * (8 / W) >= x.rows)
         return;
-    const int parts = x.last - (int)blockIdx.x + 1;
+    const int parts = row < x.rows ? x.last - (int)blockIdx.x + 1 : 0;
     // the first part is the tail of its block's share, the others lie at the head of theirs
     auto place = [&](int i) { return ((int64_t)(blockIdx.x + i) * 2 + (i == 0)) * p.max_rows + row; };
     constexpr int kMost = (kMaxGrid + 31) / 32;
@@ -1054,18 +1081,18 @@ __global__ void __launch_bounds__(256) join_kernel(CacheView c, AttentionParams 
     }
     l = warp_sum(l);
     constexpr int E = DP / 32;  // elements per lane
-    float acc[E] = {};
+    float acc[4] = {};
 #pragma unroll
     for (int j = 0; j < kMost; ++j) {
         const int some = min(32, parts - j * 32);
-#pragma unroll 4
-        for (int i = 0; i < some; ++i) {
+#pragma unroll 8
+        for (int i = mine; i < some; i += W) {
             const float f = __shfl_sync(kFull, ml[j].x, i);
             const float *o = p.part_o + place(j * 32 + i) * DP + lane * E;
-            float v[E];
+            float v[4] = {};
             if (E == 4) {
                 const float4 y = *reinterpret_cast<const float4 *>(o);
-                v[0] = y.x, v[1] = y.y, v[E > 2 ? 2 : 0] = y.z, v[E > 3 ? 3 : 0] = y.w;
+                v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
             } else {
                 const float2 y = *reinterpret_cast<const float2 *>(o);
                 v[0] = y.x, v[1] = y.y;
@@ -1075,17 +1102,30 @@ __global__ void __launch_bounds__(256) join_kernel(CacheView c, AttentionParams 
                 acc[e] = f == 0.0f ? acc[e] : fmaf(f, v[e], acc[e]);
         }
     }
+    if (W > 1) {
+        sums[warp][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        __syncthreads();
+        if (mine > 0)
+            return;
+#pragma unroll
+        for (int i = 1; i < W; ++i) {
+            const float4 y = sums[warp + i][lane];
+            acc[0] += y.x, acc[1] += y.y, acc[2] += y.z, acc[3] += y.w;
+        }
+    }
+    if (row >= x.rows)
+        return;
     const int m = x.b * kBlockRows + row;
     const int64_t t = (int64_t)p.cu[x.r] + m / p.group;
     const int head = x.h * p.group + m % p.group;
     const float by = 1.0f / l;
     if (lane * E < c.dim) {
         char *out = p.out + 2 * (t * p.out_token + head * p.out_head + lane * E);
+        const uint32_t low = from_float2<DT>(acc[0] * by, acc[1] * by);
         if (E == 4)
-            *reinterpret_cast<uint2 *>(out) = make_uint2(from_float2<DT>(acc[0] * by, acc[1] * by),
-                                                         from_float2<DT>(acc[E > 2 ? 2 : 0] * by, acc[E > 3 ? 3 : 0] * by));
+            *reinterpret_cast<uint2 *>(out) = make_uint2(low, from_float2<DT>(acc[2] * by, acc[3] * by));
         else
-            *reinterpret_cast<uint32_t *>(out) = from_float2<DT>(acc[0] * by, acc[1] * by);
+            *reinterpret_cast<uint32_t *>(out) = low;
     }
     if (lane == 0 && p.lse)
         p.lse[t * p.heads + head] = (top + log2f(l)) * 0.69314718055994531f;
@@ -1201,7 +1241,8 @@ cudaError_t launch_attention(const CUtensorMap &kmap, const CUtensorMap &vmap, c
     if (e)
         return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid, (p.max_rows + 7) / 8);
+    const int warps = p.max_rows <= 64 ? 4 : 1;  // per row
+    cfg.gridDim = dim3(grid, (p.max_rows * warps + 7) / 8);
     cfg.blockDim = dim3(256);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -1209,7 +1250,8 @@ cudaError_t launch_attention(const CUtensorMap &kmap, const CUtensorMap &vmap, c
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<DT, DP>, c, p);
+    return warps == 4 ? cudaLaunchKernelEx(&cfg, join_kernel<DT, DP, 4>, c, p)
+                      : cudaLaunchKernelEx(&cfg, join_kernel<DT, DP, 1>, c, p);
 }
 
 spec_status check_attention(const spec_cache *cache, CacheView *c, int32_t num_q_heads, int32_t B, int64_t N)
