@@ -44,7 +44,7 @@ constexpr int kTile = 128;          // keys per tile, and rows per softmax group
 constexpr int kBlockRows = 256;     // query rows of a (request, head, row block)
 constexpr int kSoftmaxWarps = 8, kLoadWarps = 4, kMmaWarp = 13, kWalkWarp = 14, kQueryWarps = 3;
 constexpr int kAttnThreads = 512;
-constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;  // 256 threads of each: the launch's 128 a thread in all
+constexpr int kSoftmaxRegs = 144, kOtherRegs = 112;  // 256 threads of each: the launch's 128 a thread in all
 constexpr int kItems = 4;           // row blocks announced ahead
 constexpr int kMaxGrid = 160;       // blocks a call may use (SMs of the device, 152 on GB300)
 constexpr int kBlockCost = 3;       // what beginning and ending a row block costs, in tiles
@@ -64,6 +64,7 @@ struct AttentionParams {
     float *lse;
     int64_t q_token, q_head, out_token, out_head;  // elements
     int32_t heads, group, B;
+    uint32_t group_mul, group_shift;  // m / group = m * group_mul >> group_shift for 0 <= m < 2^31
     int32_t box;  // tokens per copy
     int64_t N;
     const int32_t *cu, *parent;
@@ -202,6 +203,11 @@ struct alignas(16) Item {
     int32_t last;          // the last block that works on the row block
 };
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 // 16 bytes to shared memory, or zeros.
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool real)
 {
@@ -214,7 +220,6 @@ template <int SLOTS> struct alignas(16) AttnShared {
     union {
         float2 ml[kTile];
         int32_t parent[kMaxTree];
-        int64_t sums[kAttnThreads / 32];
     } group[2];
     Item item[kItems];
     uint64_t full[SLOTS], empty[SLOTS];  // a slot's tile has landed / has been used
@@ -222,8 +227,6 @@ template <int SLOTS> struct alignas(16) AttnShared {
     uint64_t q_full[2], q_empty[2];      // a slot's Q is there / has been used
     uint64_t item_full[kItems], item_empty[kItems];
     uint64_t merge, done;
-    int64_t base;                        // work before request r
-    int32_t r;                           // first request of this block's share
     uint32_t tmem;
     volatile int32_t gave_up;
 };
@@ -243,6 +246,11 @@ __device__ __forceinline__ bool attn_wait(uint64_t *bar, uint32_t parity, volati
     return false;
 }
 
+__device__ __forceinline__ int by_group(const AttentionParams &p, int m)
+{
+    return (int)((uint64_t)(uint32_t)m * p.group_mul >> p.group_shift);
+}
+
 // ---------------------------------------------------------------------------------------
 // The list of work
 // ---------------------------------------------------------------------------------------
@@ -253,44 +261,71 @@ struct Request {
 };
 
 // Tiles of row block b: the keys up to the last row's own.
-__device__ __forceinline__ int block_keys(const Request &q, int group, int b)
+__device__ __forceinline__ int block_keys(const AttentionParams &p, const Request &q, int b)
 {
     const int end = min((b + 1) * kBlockRows, q.rows);
-    return q.len + (end - 1) / group + 1;
+    return q.len + by_group(p, end - 1) + 1;
 }
 
-__device__ __forceinline__ int block_tiles(const Request &q, int group, int b)
+__device__ __forceinline__ int block_tiles(const AttentionParams &p, const Request &q, int b)
 {
-    return (block_keys(q, group, b) + kTile - 1) / kTile;
+    return (block_keys(p, q, b) + kTile - 1) / kTile;
 }
 
 // The request's sizes; cost = 0 when there is nothing to do, or an error, which is recorded on demand.
-__device__ __forceinline__ Request request_of(const CacheView &c, const AttentionParams &p, int r, bool report)
+__device__ __forceinline__ Request request_of(const CacheView &c, const AttentionParams &p, int r, int n, int len,
+                                              bool report)
 {
     Request q;
-    q.n = p.cu[r + 1] - p.cu[r];
-    q.len = c.lens[r];
-    q.rows = q.n * p.group;
+    q.n = n;
+    q.len = len;
+    q.rows = n * p.group;
     q.cost = 0;
-    if (q.n <= 0)
+    if (n <= 0)
         return q;
-    if (q.len < 0 || (int64_t)q.len + q.n > (int64_t)c.max_pages * c.page_size || (p.parent && q.n > kMaxTree)) {
+    const int64_t blocks = (q.rows + kBlockRows - 1) / kBlockRows;
+    if (len < 0 || (int64_t)len + n > (int64_t)c.max_pages * c.page_size || (p.parent && n > kMaxTree) ||
+        blocks * (kBlockCost + 1 + ((int64_t)len + n) / kTile) > INT32_MAX) {
         if (report)
-            cache_error(c.error, p.parent && q.n > kMaxTree ? SPEC_DEVERR_TREE : SPEC_DEVERR_LENGTH, r);
+            cache_error(c.error, p.parent && n > kMaxTree ? SPEC_DEVERR_TREE : SPEC_DEVERR_LENGTH, r);
         return q;
     }
+#pragma unroll 1
     for (int b = 0; b * kBlockRows < q.rows; ++b)
-        q.cost += kBlockCost + block_tiles(q, p.group, b);
+        q.cost += kBlockCost + block_tiles(p, q, b);
     return q;
+}
+
+__device__ __forceinline__ Request request_of(const CacheView &c, const AttentionParams &p, int r, bool report)
+{
+    return request_of(c, p, r, p.cu[r + 1] - p.cu[r], c.lens[r], report);
 }
 
 // A block's share of the list: [begin(x), begin(x + 1)), in tiles of cost.
 struct Shares {
-    int64_t total;
-    int blocks;
-    __device__ __forceinline__ int64_t begin(int x) const { return total * x / blocks; }
+    int64_t total, each;  // the first `more` shares have one more than each
+    int blocks, more;
+    __device__ __forceinline__ void cut(int64_t cost, int most)
+    {
+        total = cost;
+        if (cost < INT32_MAX) {  // nearly always: a 64-bit division takes some hundred cycles
+            blocks = max(1, min(most, ((int)cost + kMinShare - 1) / kMinShare));
+            each = (int)cost / blocks;
+        } else {
+            blocks = most;
+            each = cost / blocks;
+        }
+        more = (int)(cost - each * blocks);
+    }
+    __device__ __forceinline__ int64_t begin(int x) const { return each * x + min(x, more); }
     // the block whose share holds place t
-    __device__ __forceinline__ int owner(int64_t t) const { return (int)(((t + 1) * blocks - 1) / total); }
+    __device__ __forceinline__ int owner(int64_t t) const
+    {
+        const int64_t big = (each + 1) * more;
+        if (total < INT32_MAX)
+            return t < big ? (int)t / (int)(each + 1) : more + (int)(t - big) / (int)each;
+        return (int)(t < big ? t / (each + 1) : more + (t - big) / each);
+    }
 };
 
 // Walks a block's share, one (request, head, row block) at a time; a whole warp.  A row block takes
@@ -312,16 +347,16 @@ struct Walk {
         r = first;
         q = request_of(c, p, r, false);
         int64_t at = pos - base;
-        h = (int)(at / q.cost);
-        at %= q.cost;
-        for (b = 0; at >= kBlockCost + block_tiles(q, p.group, b); ++b)
-            at -= kBlockCost + block_tiles(q, p.group, b);
+        h = at < INT32_MAX ? (int)at / q.cost : (int)(at / q.cost);
+        at -= (int64_t)h * q.cost;
+        for (b = 0; at >= kBlockCost + block_tiles(p, q, b); ++b)
+            at -= kBlockCost + block_tiles(p, q, b);
         return here(p, (int)at);
     }
     // the part of the row block from its place `from` on
     __device__ __forceinline__ bool here(const AttentionParams &p, int from)
     {
-        tiles = block_tiles(q, p.group, b);
+        tiles = block_tiles(p, q, b);
         const int to = (int)min((int64_t)(kBlockCost + tiles), from + (end - pos));
         t0 = max(from - kBlockCost, 0);
         t1 = max(to - kBlockCost, 0);
@@ -419,6 +454,89 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     return d;
 }
 
+// The shares of the list, and the request in which this block's begins (with the work before it); a
+// whole warp.  False when the block has no share, or cu is malformed.
+__device__ __forceinline__ bool find_share(const CacheView &c, const AttentionParams &p, Shares *shares, int *first,
+                                           int64_t *base, int lane)
+{
+    constexpr int U = 4;  // requests of a lane in a turn
+    int cost[U];
+    int64_t before = 0, at = 0;
+    bool bad = false, wrong = false;
+    // Twice: the total makes the shares, then the block finds its own.  A batch of one turn keeps its
+    // costs in between.
+    for (int pass = 0; pass < 2; ++pass) {
+        before = 0;
+#pragma unroll 1
+        for (int r0 = 0; r0 < p.B; r0 += 32 * U) {
+            const int r = r0 + lane * U;
+            if (pass == 0 || p.B > 32 * U) {
+                int32_t cu[U + 1], len[U];
+#pragma unroll
+                for (int i = 0; i <= U; ++i)
+                    cu[i] = p.cu[min(r + i, p.B)];
+#pragma unroll
+                for (int i = 0; i < U; ++i)
+                    len[i] = c.lens[min(r + i, p.B - 1)];
+                bad |= (r == 0 && cu[0] != 0) || cu[0] < 0;
+                int64_t sum = 0;
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    bad |= cu[i] > cu[i + 1] || cu[i + 1] > p.N;
+                    cost[i] = 0;
+                    if (r + i < p.B && !bad) {
+                        cost[i] = request_of(c, p, r + i, cu[i + 1] - cu[i], len[i], false).cost;
+                        wrong |= cost[i] == 0 && cu[i + 1] > cu[i];
+                    }
+                    sum += (int64_t)cost[i] * c.heads;
+                }
+                int64_t incl = sum;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int64_t y = __shfl_up_sync(kFull, incl, d);
+                    incl += lane >= d ? y : 0;
+                }
+                at = before + incl - sum;
+                before += __shfl_sync(kFull, incl, 31);
+            }
+            if (pass == 1) {
+                const int64_t want = shares->begin(blockIdx.x);
+                int found = -1;
+                int64_t place = at, found_at = 0;
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    const int64_t work = (int64_t)cost[i] * c.heads;
+                    if (place <= want && want < place + work) {
+                        found = r + i;
+                        found_at = place;
+                    }
+                    place += work;
+                }
+                const unsigned who = __ballot_sync(kFull, found >= 0);
+                if (who) {
+                    *first = __shfl_sync(kFull, found, __ffs(who) - 1);
+                    *base = __shfl_sync(kFull, found_at, __ffs(who) - 1);
+                    return true;
+                }
+            }
+        }
+        if (pass == 0) {
+            if (__any_sync(kFull, bad)) {
+                if (blockIdx.x == 0 && lane == 0)
+                    cache_error(c.error, SPEC_DEVERR_LAYOUT, -1);
+                return false;
+            }
+            if (blockIdx.x == 0 && __any_sync(kFull, wrong))
+                for (int r = lane; r < p.B; r += 32)
+                    request_of(c, p, r, true);
+            shares->cut(before, gridDim.x);
+            if (before == 0 || blockIdx.x >= shares->blocks)
+                return false;
+        }
+    }
+    return false;  // cannot be: every place belongs to a request
+}
+
 template <int DT, int DP>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, CacheView c,
@@ -431,69 +549,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     auto &S = *reinterpret_cast<typename Z::Shared *>(smem + (2 + SLOTS) * Z::kSlotBytes);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-    // The whole list's length, and this block's place in it.
-    bool bad = false;
-    for (int r = tid; r <= p.B; r += kAttnThreads) {
-        const int32_t x = p.cu[r];
-        bad |= (r == 0 ? x != 0 : p.cu[r - 1] > x) || x > p.N;
+    if (tid == 0) {
+        prefetch_map(&kmap);
+        prefetch_map(&vmap);
     }
-    bad = __syncthreads_or(bad);
-    Shares shares{0, 1};
-    if (bad) {
-        if (blockIdx.x == 0 && tid == 0)
-            cache_error(c.error, SPEC_DEVERR_LAYOUT, -1);
-    } else {
-        // twice: the total makes the shares, then each block finds its own; a batch of no more
-        // requests than threads keeps its sums in between
-        int64_t mine = 0, at = 0;
-        for (int pass = 0; pass < 2; ++pass) {
-            int64_t before = 0;
-            for (int r0 = 0; r0 < p.B; r0 += kAttnThreads) {
-                const int r = r0 + tid;
-                if (pass == 0 || p.B > kAttnThreads) {
-                    mine = 0;
-                    if (r < p.B)
-                        mine = (int64_t)request_of(c, p, r, pass == 0 && blockIdx.x == 0).cost * c.heads;
-                    int64_t incl = mine;
-#pragma unroll
-                    for (int d = 1; d < 32; d <<= 1) {
-                        const int64_t y = __shfl_up_sync(kFull, incl, d);
-                        incl += lane >= d ? y : 0;
-                    }
-                    __syncthreads();
-                    if (lane == 31)
-                        S.group[0].sums[warp] = incl;
-                    __syncthreads();
-                    int64_t all = 0, lower = 0;
-#pragma unroll
-                    for (int i = 0; i < kAttnThreads / 32; ++i) {
-                        lower += i < warp ? S.group[0].sums[i] : 0;
-                        all += S.group[0].sums[i];
-                    }
-                    at = before + lower + incl - mine;
-                    before += all;
-                }
-                if (pass == 1) {
-                    const int64_t want = shares.begin(blockIdx.x);
-                    if (mine > 0 && at <= want && want < at + mine) {
-                        S.r = r;
-                        S.base = at;
-                    }
-                }
-            }
-            if (pass == 1)
-                break;
-            shares.total = before;
-            shares.blocks = (int)max((int64_t)1, min((int64_t)gridDim.x, (before + kMinShare - 1) / kMinShare));
-            if (blockIdx.x >= shares.blocks || before == 0)
-                break;
-        }
-    }
-    if (tid == 0)
-        p.partial[blockIdx.x].rows = 0;
-    if (shares.total == 0 || blockIdx.x >= shares.blocks)
-        return;
-
     if (tid == 0) {
         for (int i = 0; i < SLOTS; ++i) {
             mbar_init(&S.full[i], 2);
@@ -704,12 +763,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             __syncwarp();
         } else {
             Walk w;
+            Shares shares;
             const int part = warp == kWalkWarp ? 0 : warp == 8 ? 1 : 2;
             int q_use = 0;
             uint32_t slots = 0;
             bool more = false;
-            if (warp == kWalkWarp)
-                more = w.start(c, p, shares, S.r, S.base) || w.next(c, p);
+            if (warp == kWalkWarp) {
+                if (lane == 0)
+                    p.partial[blockIdx.x].rows = 0;
+                int first;
+                int64_t base;
+                more = find_share(c, p, &shares, &first, &base, lane) &&
+                       (w.start(c, p, shares, first, base) || w.next(c, p));
+            }
             for (uint32_t k = 0;; ++k) {
                 Item *mine = &S.item[k % kItems];
                 if (warp == kWalkWarp) {
@@ -725,7 +791,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             x.nt = w.t1 - w.t0;
                             x.t0 = w.t0;
                             x.tiles = w.tiles;
-                            x.keys = block_keys(w.q, p.group, w.b);
+                            x.keys = block_keys(p, w.q, w.b);
                             x.len = w.q.len;
                             x.n = w.q.n;
                             x.first = p.cu[w.r];
@@ -756,8 +822,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     const int at = part * 32 + lane, vec = at % kVecs;
                     const uint32_t dst = smem_addr(qtile) + (use & 1) * Z::kSlotBytes + vec / 8 * Z::kChunk;
                     const int m0 = item.b * kBlockRows + g * kTile, rows = min(kTile, item.rows - g * kTile);
-                    int x = at / kVecs, token = (m0 + x) / p.group, head = (m0 + x) - token * p.group;
-                    const int more_tokens = kStep / p.group, more_heads = kStep % p.group;
+                    int x = at / kVecs, token = by_group(p, m0 + x), head = (m0 + x) - token * p.group;
+                    const int more_tokens = by_group(p, kStep), more_heads = kStep - more_tokens * p.group;
                     const char *src = p.q + 2 * ((int64_t)item.first * p.q_token +
                                                  (int64_t)(item.h * p.group) * p.q_head + vec * 8);
                     for (; x < rows; x += kStep) {
@@ -809,7 +875,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const int mine = min(kTile, item.rows - m0);     // its rows
             const bool warp_on = sub * 32 < mine, on = row < mine;
             const int m = item.b * kBlockRows + m0 + row;    // row of the request
-            const int token = m / p.group, head = item.h * p.group + m % p.group;
+            const int token = by_group(p, m), head = item.h * p.group + m - token * p.group;
 
             const int turns = wide ? nt : (nt - g + 1) / 2;  // this group's tiles
 
@@ -835,7 +901,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
             // keys that every row of this warp sees
             const int all_see = p.parent ? item.len
-                                         : item.len + (item.b * kBlockRows + m0 + sub * 32) / p.group + 1;
+                                         : item.len + by_group(p, item.b * kBlockRows + m0 + sub * 32) + 1;
             float M = -INFINITY, l = 0;
             bool any = false;  // the accumulator holds something
             for (int t = wide ? 0 : g; t < nt; t += wide ? 1 : 2) {
@@ -844,40 +910,39 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 const int column = (item.t0 + t) * kTile;
                 if (warp_on) {
                     tmem_fence_after();
-                    // the second half is on its way while the first is looked at
-                    float x[kTile];
+                    // 64 columns at a time, read once for the maximum and once for the exponentials: the
+                    // code of a tile is fetched anew by every block, and runs at a fetch's pace then
+                    // (all 128 in registers, unrolled: 2% faster on prompt chunks, first tile 2 us)
                     const bool cut = column + kTile > all_see;
-                    auto mask = [&](int from) {  // 64 columns
+                    auto columns = [&](int j, float *x) {
+                        tmem_ld32(s_addr + j * 64, x);
+                        tmem_ld32(s_addr + j * 64 + 32, x + 32);
+                        tmem_wait_ld();
+                        if (cut) {
 #pragma unroll
-                        for (int i = from; i < from + 64; i += 32) {
-                            const uint32_t see = p.parent ? tree_columns(bits, item.len, column + i)
-                                                          : low_bits(item.len + token + 1 - column - i);
+                            for (int i = 0; i < 2; ++i) {
+                                const int col = column + j * 64 + i * 32;
+                                const uint32_t see = p.parent ? tree_columns(bits, item.len, col)
+                                                              : low_bits(item.len + token + 1 - col);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                x[i + e] = see >> e & 1 ? x[i + e] : -INFINITY;
+                                for (int e = 0; e < 32; ++e)
+                                    x[i * 32 + e] = see >> e & 1 ? x[i * 32 + e] : -INFINITY;
+                            }
                         }
                     };
-                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    auto maximum = [&](int from) {
+                    float mx = -INFINITY;
+#pragma unroll 1
+                    for (int j = 0; j < kTile / 64; ++j) {
+                        float x[64];
+                        columns(j, x);
+                        float top[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int e = from; e < from + 64; e += 8)
+                        for (int e = 0; e < 64; e += 8)
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 top[i] = max3(top[i], x[e + 2 * i], x[e + 2 * i + 1]);
-                    };
-                    tmem_ld32(s_addr, x);
-                    tmem_ld32(s_addr + 32, x + 32);
-                    tmem_wait_ld();
-                    tmem_ld32(s_addr + 64, x + 64);
-                    tmem_ld32(s_addr + 96, x + 96);
-                    if (cut)
-                        mask(0);
-                    maximum(0);
-                    tmem_wait_ld();
-                    if (cut)
-                        mask(64);
-                    maximum(64);
-                    float mx = max3(fmaxf(top[0], top[1]), top[2], top[3]);
+                        mx = max3(fmaxf(top[0], top[1]), top[2], top[3]);
+                    }
                     mx *= p.scale_log2;
                     const bool grown = mx > M + kLazy;  // also from -inf
                     const float f = grown ? ex2(M - mx) : 1.0f;
@@ -902,10 +967,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     const float base = M == -INFINITY ? 0.0f : -M;
                     const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2), base2 = pack2(base, base);
                     uint64_t sum[4] = {};
+#pragma unroll 1
+                    for (int j = 0; j < kTile / 64; ++j) {
+                        float x[64];
+                        columns(j, x);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-#pragma unroll
-                        for (int e = j * 64; e < j * 64 + 64; e += 2) {
+                        for (int e = 0; e < 64; e += 2) {
                             float a, b;
                             unpack2(fma2(pack2(x[e], x[e + 1]), scale2, base2), a, b);
                             a = ex2(a);
@@ -913,7 +980,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             sum[e / 2 & 3] = add2(sum[e / 2 & 3], pack2(a, b));
                             x[e / 2] = __uint_as_float(from_float2<DT>(a, b));
                         }
-                        tmem_st32(s_addr + j * 32, x + j * 32);
+                        tmem_st32(s_addr + j * 32, x);
                     }
                     float a, b;
                     unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
@@ -1116,8 +1183,8 @@ __global__ void __launch_bounds__(256) join_kernel(CacheView c, AttentionParams 
     if (row >= x.rows)
         return;
     const int m = x.b * kBlockRows + row;
-    const int64_t t = (int64_t)p.cu[x.r] + m / p.group;
-    const int head = x.h * p.group + m % p.group;
+    const int token = by_group(p, m), head = x.h * p.group + m - token * p.group;
+    const int64_t t = (int64_t)p.cu[x.r] + token;
     const float by = 1.0f / l;
     if (lane * E < c.dim) {
         char *out = p.out + 2 * (t * p.out_token + head * p.out_head + lane * E);
@@ -1315,6 +1382,12 @@ spec_status spec_attention(const spec_cache *cache, int32_t layer, const void *q
     p.out_head = num_q_heads > 1 ? out_head_stride : 0;
     p.heads = num_q_heads;
     p.group = num_q_heads / c.heads;
+    // 1 / group in 31 + ceil(log2(group)) bits, rounded up: it is off by less than group / 2^bits <=
+    // 2^-31, too little to move the floor of m / group for any m < 2^31
+    p.group_shift = 31;
+    while ((1 << (p.group_shift - 31)) < p.group)
+        ++p.group_shift;
+    p.group_mul = (uint32_t)((((uint64_t)1 << p.group_shift) + p.group - 1) / p.group);
     p.B = B;
     p.N = N;
     p.cu = cu_new;
