@@ -19,7 +19,6 @@ request r.  Chains of k_r drafts are k_r + 1 new tokens: ``cu_new = cu_num_draft
 from __future__ import annotations
 
 import ctypes
-from contextlib import nullcontext
 from dataclasses import dataclass, field
 
 import torch
@@ -73,11 +72,6 @@ def load():
         f.restype, f.argtypes = result, args
     _lib = lib
     return lib
-
-
-def _check(status: int, what: str):
-    if status != 0:
-        raise SpecRejectError(status, what)
 
 
 @dataclass
@@ -138,7 +132,8 @@ class PagedCache:
             ref_counts=self.ref_counts.data_ptr(), free_pages=self.free_pages.data_ptr(),
             num_free=self.num_free.data_ptr(), error=self.error.data_ptr(), scratch=self.scratch.data_ptr())
         # what every call needs, looked up once: the tensors of a cache do not change
-        self.ref, self.device, self.dtype, self.heads, self.dim = ctypes.byref(self.struct), dev, k.dtype, H, D
+        self.ref, self.device, self.index = ctypes.byref(self.struct), dev, dev.index
+        self.dtype, self.heads, self.dim = k.dtype, H, D
 
 
 def _code(t) -> int:
@@ -156,17 +151,17 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-_SAME_DEVICE = nullcontext()
-
-
-def _on(c):
-    """A context in which the cache's device is current."""
-    return _SAME_DEVICE if torch.cuda.current_device() == c.device.index else torch.cuda.device(c.device)
-
-
-def _stream(c, stream) -> int:
-    # the raw handle of the device's current stream, without a Stream object around it
-    return torch._C._cuda_getCurrentRawStream(c.device.index) if stream is None else stream.cuda_stream
+def _call(c, name, stream, *args):
+    """Calls a library function on the cache's device and a stream (the device's current one, by its raw
+    handle, unless one is given)."""
+    index = c.index
+    if torch._C._cuda_getDevice() != index:
+        with torch.cuda.device(index):
+            return _call(c, name, stream, *args)
+    status = getattr(_lib, name)(c.ref, *args, torch._C._cuda_getCurrentRawStream(index) if stream is None
+                                 else stream.cuda_stream)
+    if status != 0:
+        raise SpecRejectError(status, name)
 
 
 def make_cache(num_layers: int, num_pages: int, page_size: int, num_kv_heads: int, head_dim: int, num_requests: int,
@@ -180,16 +175,16 @@ def make_cache(num_layers: int, num_pages: int, page_size: int, num_kv_heads: in
                      dtype=torch.bfloat16 if dtype is None else dtype, device=dev)
     c = PagedCache(kv[0], kv[1], page_table=ints(num_requests, max_pages), lens=ints(num_requests),
                    held=ints(num_requests), ref_counts=ints(num_pages), free_pages=ints(num_pages), num_free=ints(1))
-    with _on(c):
-        _check(load().spec_cache_init(c.ref, _stream(c, stream)), "spec_cache_init")
+    _call(c, "spec_cache_init", stream)
     return c
 
 
 def last_error(c: PagedCache, stream=None):
     """(status, error_bits, first_bad_request) since the last call, and clears them (synchronises)."""
     bits, first = ctypes.c_int32(0), ctypes.c_int32(0)
-    with _on(c):
-        st = load().spec_cache_error(c.ref, _stream(c, stream), ctypes.byref(bits), ctypes.byref(first))
+    with torch.cuda.device(c.device):
+        s = torch.cuda.current_stream() if stream is None else stream
+        st = load().spec_cache_error(c.ref, s.cuda_stream, ctypes.byref(bits), ctypes.byref(first))
     if st not in (0, 5, 6):
         raise SpecRejectError(st, "spec_cache_error")
     return int(st), int(bits.value), int(first.value)
@@ -217,8 +212,7 @@ def _rows(c, t, heads, name):
 def reserve(c: PagedCache, cu_new, stream=None):
     """Pages for the new tokens of every request (spec_cache_reserve)."""
     B = _cu(c, cu_new)
-    with _on(c):
-        _check(load().spec_cache_reserve(c.ref, cu_new.data_ptr(), B, _stream(c, stream)), "spec_cache_reserve")
+    _call(c, "spec_cache_reserve", stream, cu_new.data_ptr(), B)
 
 
 def append(c: PagedCache, layer: int, k_new, v_new, cu_new, stream=None):
@@ -229,9 +223,8 @@ def append(c: PagedCache, layer: int, k_new, v_new, cu_new, stream=None):
     N = k_new.shape[0]
     if v_new.shape[0] != N:
         raise ValueError("k_new and v_new must have the same rows")
-    with _on(c):
-        _check(load().spec_cache_append(c.ref, layer, k_new.data_ptr(), kt, kh, v_new.data_ptr(), vt, vh,
-                                        cu_new.data_ptr(), B, N, _stream(c, stream)), "spec_cache_append")
+    _call(c, "spec_cache_append", stream, layer, k_new.data_ptr(), kt, kh, v_new.data_ptr(), vt, vh,
+          cu_new.data_ptr(), B, N)
 
 
 def commit(c: PagedCache, cu_new, num_accepted, parent=None, last_node=None, out_lens=None, stream=None):
@@ -248,9 +241,8 @@ def commit(c: PagedCache, cu_new, num_accepted, parent=None, last_node=None, out
         _int32(last_node, (B,), "last_node", c.device)
     if out_lens is not None:
         _int32(out_lens, (B,) if out_lens is not c.lens else c.lens.shape, "out_lens", c.device)
-    with _on(c):
-        _check(load().spec_cache_commit(c.ref, cu_new.data_ptr(), B, N, num_accepted.data_ptr(), _ptr(parent),
-                                        _ptr(last_node), _ptr(out_lens), _stream(c, stream)), "spec_cache_commit")
+    _call(c, "spec_cache_commit", stream, cu_new.data_ptr(), B, N, num_accepted.data_ptr(), _ptr(parent),
+          _ptr(last_node), _ptr(out_lens))
 
 
 def fork(c: PagedCache, src, dst, stream=None):
@@ -258,9 +250,7 @@ def fork(c: PagedCache, src, dst, stream=None):
     F = int(src.shape[0])
     _int32(src, (F,), "src", c.device)
     _int32(dst, (F,), "dst", c.device)
-    with _on(c):
-        _check(load().spec_cache_fork(c.ref, src.data_ptr(), dst.data_ptr(), F, _stream(c, stream)),
-               "spec_cache_fork")
+    _call(c, "spec_cache_fork", stream, src.data_ptr(), dst.data_ptr(), F)
 
 
 def release(c: PagedCache, keep_lens=None, stream=None):
@@ -270,8 +260,7 @@ def release(c: PagedCache, keep_lens=None, stream=None):
     if keep_lens is not None:
         B = int(keep_lens.shape[0])
         _int32(keep_lens, (B,), "keep_lens", c.device)
-    with _on(c):
-        _check(load().spec_cache_release(c.ref, _ptr(keep_lens), B, _stream(c, stream)), "spec_cache_release")
+    _call(c, "spec_cache_release", stream, _ptr(keep_lens), B)
 
 
 def attention_workspace_size(c: PagedCache, num_q_heads: int, B: int, N: int) -> int:
@@ -304,17 +293,14 @@ def attention(c: PagedCache, layer: int, q, cu_new, parent=None, scale=None, out
     if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (N, H) or not lse.is_contiguous() or
                             lse.device != c.device):
         raise TypeError(f"lse must be a contiguous float32 tensor of shape {(N, H)} on {c.device}")
-    lib = load()
-    with _on(c):
-        if workspace is None:
-            n = lib.spec_attention_workspace_size(c.ref, H, B, N)
-            workspace = torch.empty(n, dtype=torch.uint8, device=c.device)
-            if stream is not None:
-                workspace.record_stream(stream)
-        elif workspace.dtype is not torch.uint8 or workspace.device != c.device or not workspace.is_contiguous():
-            raise TypeError(f"workspace must be a contiguous uint8 tensor on {c.device}")
-        _check(lib.spec_attention(
-            c.ref, layer, q.data_ptr(), qt, qh, H, cu_new.data_ptr(), B, N, _ptr(parent),
-            c.dim ** -0.5 if scale is None else scale, out.data_ptr(), ot, oh, _ptr(lse), workspace.data_ptr(),
-            workspace.numel(), _stream(c, stream)), "spec_attention")
+    if workspace is None:
+        workspace = torch.empty(_lib.spec_attention_workspace_size(c.ref, H, B, N), dtype=torch.uint8,
+                                device=c.device)
+        if stream is not None:
+            workspace.record_stream(stream)
+    elif workspace.dtype is not torch.uint8 or workspace.device != c.device or not workspace.is_contiguous():
+        raise TypeError(f"workspace must be a contiguous uint8 tensor on {c.device}")
+    _call(c, "spec_attention", stream, layer, q.data_ptr(), qt, qh, H, cu_new.data_ptr(), B, N, _ptr(parent),
+          c.dim ** -0.5 if scale is None else scale, out.data_ptr(), ot, oh, _ptr(lse), workspace.data_ptr(),
+          workspace.numel())
     return out

@@ -120,11 +120,122 @@ __device__ __forceinline__ Ask reserve_ask(const CacheView &c, const int32_t *cu
     return a;
 }
 
-// One block: lists the requests that write to a shared page, decides which of them copy it (request
-// order: each copies while others hold the page; the last of its holders keeps it), finds every
-// request's place in the stack of free pages by a prefix sum, and hands the pages out.
+// Reserve is one block: it lists the requests that write to a shared page, decides which of them copy
+// it (request order: each copies while others hold the page; the last of its holders keeps it), finds
+// every request's place in the stack of free pages by a prefix sum, and hands the pages out.  It is
+// bound by the chain of dependent loads (lengths, table, counts, stack), not by work.
+//
+// A thread per request, all of it in registers and shared memory; new pages are handed out a thread
+// each, which finds its request by bisection.
 __global__ void __launch_bounds__(kBookThreads) reserve_kernel(CacheView c, const int32_t *cu, int B)
 {
+    __shared__ int32_t held_of[kBookThreads], copies_of[kBookThreads], shared_of[kBookThreads];
+    __shared__ int64_t base_of[kBookThreads + 1];
+    __shared__ int first_short, ncopy;
+    const int r = threadIdx.x;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the copies wait for the whole of this
+    const int32_t have = *c.num_free;
+    int32_t here = 0, next = 0, len = 0, held = 0;
+    if (r < B) {
+        here = cu[r];
+        next = cu[r + 1];
+        len = c.lens[r];
+        held = c.held[r];
+    }
+    if (r == 0) {
+        first_short = INT_MAX;
+        ncopy = 0;
+    }
+    if (__syncthreads_or(here > next || (r == 0 && here != 0))) {
+        if (r == 0) {
+            *c.ncopy = 0;
+            cache_error(c.error, SPEC_DEVERR_LAYOUT, -1);
+        }
+        return;
+    }
+    int need = 0, shared = -1;
+    if (next > here) {
+        const int n = next - here;
+        if (len < 0 || held < 0 || held > c.max_pages || len > (int64_t)held * c.page_size ||
+            (int64_t)len + n > (int64_t)c.max_pages * c.page_size) {
+            cache_error(c.error, SPEC_DEVERR_LENGTH, r);
+        } else {
+            need = pages_of((int64_t)len + n, c.page_size);
+            if (len % c.page_size) {
+                const int page = c.table[r * c.table_stride + len / c.page_size];
+                const int refs = page >= 0 && page < c.num_pages ? c.ref[page] : 0;
+                if (refs < 1) {
+                    cache_error(c.error, SPEC_DEVERR_PAGE, r);
+                    need = 0;
+                } else if (refs > 1) {
+                    shared = page;
+                }
+            }
+        }
+    }
+    bool copies = false;
+    shared_of[r] = shared;
+    if (__syncthreads_or(shared >= 0) && shared >= 0) {
+        int before = 0;
+#pragma unroll 8
+        for (int j = 0; j < r; ++j)
+            before += shared_of[j] == shared;
+        copies = c.ref[shared] - before > 1;
+    }
+    const int fresh = (need > held ? need - held : 0) + copies;
+    int64_t used;
+    const int64_t at = block_scan<kBookThreads>(fresh, &used);
+    held_of[r] = held;
+    copies_of[r] = copies;
+    base_of[r] = at;
+    if (fresh && at + fresh > have)
+        atomicMin(&first_short, r);
+    __syncthreads();  // also: no count is changed before every thread has read its page's
+    if (used > have || have > c.num_pages) {
+        if (r == 0) {
+            *c.ncopy = 0;
+            cache_error(c.error, SPEC_DEVERR_CAPACITY, first_short);
+        }
+        return;
+    }
+    for (int64_t k = r; k < used; k += kBookThreads) {
+        int lo = 0, hi = B;  // the last request with base <= k; those of no new page lie before it
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (base_of[mid] <= k)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        const int page = c.free_pages[have - 1 - k];
+        const int i = (int)(k - base_of[lo]) - copies_of[lo];  // -1: the copy of its last page
+        if (page < 0 || page >= c.num_pages)
+            cache_error(c.error, SPEC_DEVERR_PAGE, lo);
+        else
+            c.ref[page] = 1;
+        if (i >= 0)
+            c.table[lo * c.table_stride + held_of[lo] + i] = page;
+    }
+    if (copies) {
+        const int page = c.free_pages[have - 1 - at];
+        c.table[r * c.table_stride + len / c.page_size] = page;
+        atomicSub(&c.ref[shared], 1);
+        if (page >= 0 && page < c.num_pages)
+            c.copies[atomicAdd(&ncopy, 1)] = make_int4(shared, page, len % c.page_size, 0);
+    }
+    if (need > held)
+        c.held[r] = need;
+    __syncthreads();
+    if (r == 0) {
+        *c.ncopy = ncopy;
+        *c.num_free = have - (int32_t)used;
+    }
+}
+
+// The same for more requests than the block has threads, in turns, with its lists in the scratch.
+__global__ void __launch_bounds__(kBookThreads) reserve_many_kernel(CacheView c, const int32_t *cu, int B)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     if (tid == 0)
         *c.ncopy = 0;
@@ -232,41 +343,39 @@ __global__ void __launch_bounds__(kBookThreads) reserve_kernel(CacheView c, cons
         *c.num_free = have - (int32_t)used;
 }
 
-// The rows of the copy list, in every layer.  Units of one page's keys or values in one layer,
-// each split over as many blocks as the grid has for it.
+// The rows of the copy list, in every layer, in parts of a page's keys or values in one layer: four
+// 16-byte vectors a thread, all loaded before any is stored.
 __global__ void __launch_bounds__(kCopyThreads) copy_rows_kernel(CacheView c)
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t units = (int64_t)*c.ncopy * c.num_layers * 2;
-    if (units == 0)
-        return;
-    const int64_t parts = units < gridDim.x ? gridDim.x / units : 1;
+    constexpr int U = 4;
     const int vecs = c.dim / 8;
-    for (int64_t u = blockIdx.x; u < units * parts; u += gridDim.x) {
+    const int parts = (c.page_size * c.heads * vecs + U * kCopyThreads - 1) / (U * kCopyThreads);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t units = (int64_t)*c.ncopy * c.num_layers * 2 * parts;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
         const int64_t unit = u / parts;
-        const int part = (int)(u % parts);
+        const int part = (int)(u - unit * parts);
         const int4 pair = c.copies[unit / (c.num_layers * 2)];
         const int which = (int)(unit % (c.num_layers * 2));
+        const int count = pair.z * c.heads * vecs, i0 = part * U * kCopyThreads + threadIdx.x;
+        if (i0 >= count)
+            continue;
         char *base = (which & 1 ? c.v : c.k) + 2 * ((which >> 1) * c.layer_stride);
         const char *src = base + 2 * (pair.x * c.page_stride);
         char *dst = base + 2 * (pair.y * c.page_stride);
-        const int count = pair.z * c.heads * vecs;  // 16-byte vectors
-        const int stride = (int)parts * kCopyThreads;
-        auto offset = [&](int i) {
-            const int vec = i % vecs, row = i / vecs;
-            return 2 * (row / c.heads * c.token_stride + row % c.heads * c.head_stride + vec * 8);
-        };
-        for (int i0 = part * kCopyThreads + threadIdx.x; i0 < count; i0 += 4 * stride) {
-            uint4 x[4];
+        int64_t offset[U];
+        uint4 x[U];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (i0 + j * stride < count)
-                    x[j] = *reinterpret_cast<const uint4 *>(src + offset(i0 + j * stride));
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (i0 + j * stride < count)
-                    *reinterpret_cast<uint4 *>(dst + offset(i0 + j * stride)) = x[j];
+        for (int j = 0; j < U; ++j) {
+            const int i = i0 + j * kCopyThreads, row = i / vecs;
+            offset[j] = 2 * (row / c.heads * c.token_stride + row % c.heads * c.head_stride + (i - row * vecs) * 8);
+            if (i < count)
+                x[j] = *reinterpret_cast<const uint4 *>(src + offset[j]);
         }
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            if (i0 + j * kCopyThreads < count)
+                *reinterpret_cast<uint4 *>(dst + offset[j]) = x[j];
     }
 }
 
@@ -671,9 +780,12 @@ spec_status spec_cache_reserve(const spec_cache *cache, const int32_t *cu_new, i
     if (B == 0)
         return SPEC_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    reserve_kernel<<<1, kBookThreads, 0, st>>>(c, cu_new, B);
+    if (B <= kBookThreads)
+        reserve_kernel<<<1, kBookThreads, 0, st>>>(c, cu_new, B);
+    else
+        reserve_many_kernel<<<1, kBookThreads, 0, st>>>(c, cu_new, B);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(sms * 4);
+    cfg.gridDim = dim3(sms * 8);
     cfg.blockDim = dim3(kCopyThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
