@@ -208,10 +208,14 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
-// 16 bytes to shared memory, or zeros.
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool real)
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void zero16(uint32_t dst)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
 }
 
 // What a block keeps behind the operand tiles.
@@ -226,7 +230,7 @@ template <int SLOTS> struct alignas(16) AttnShared {
     uint64_t s_full[2], p_full[2], o_full[2];  // a group's S is there / its P / the last of its O
     uint64_t q_full[2], q_empty[2];      // a slot's Q is there / has been used
     uint64_t item_full[kItems], item_empty[kItems];
-    uint64_t merge, done;
+    uint64_t ready, merge, done;
     uint32_t tmem;
     volatile int32_t gave_up;
 };
@@ -569,6 +573,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             mbar_init(&S.item_full[i], 1);
             mbar_init(&S.item_empty[i], kSoftmaxWarps + kLoadWarps + 1 + kQueryWarps - 1);  // all but the writer
         }
+        mbar_init(&S.ready, kSoftmaxWarps);
         mbar_init(&S.merge, kSoftmaxWarps);
         mbar_init(&S.done, 1);
         S.gave_up = 0;
@@ -598,6 +603,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // A warpgroup sets its registers together; the roles that follow are compiled for that number.
     if (warp >= kSoftmaxWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        // Up to here the block may run beside the end of the kernel before; what that wrote is read behind.
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         const int load_warp = warp == 15 ? 3 : warp - 9;  // 0, 1: K; 2, 3: V
         if (load_warp >= 0 && load_warp < kLoadWarps && warp != 12) {
             // Slot order: K of tile 0, then K of tile t + 1 and V of tile t, as the products use them.
@@ -701,6 +708,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     p_turn ^= 1u << g;
                     tmem_fence_after();
                 };
+                wait(&S.ready, 0);
                 for (uint32_t k = 0;; ++k) {
                     if (!announced(k))
                         break;
@@ -826,15 +834,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     const int more_tokens = by_group(p, kStep), more_heads = kStep - more_tokens * p.group;
                     const char *src = p.q + 2 * ((int64_t)item.first * p.q_token +
                                                  (int64_t)(item.h * p.group) * p.q_head + vec * 8);
-                    for (; x < rows; x += kStep) {
-                        copy16(dst + x * 128 + ((vec % 8) ^ (x % 8)) * 16,
-                               vec * 8 < c.dim ? src + 2 * (token * p.q_token + head * p.q_head) : p.q, vec * 8 < c.dim);
-                        token += more_tokens;
-                        head += more_heads;
-                        if (head >= p.group) {
-                            head -= p.group;
-                            ++token;
+                    if (vec * 8 < c.dim) {
+                        for (; x < rows; x += kStep) {
+                            copy16(dst + x * 128 + ((vec % 8) ^ (x % 8)) * 16,
+                                   src + 2 * (token * p.q_token + head * p.q_head));
+                            token += more_tokens;
+                            head += more_heads;
+                            if (head >= p.group) {
+                                head -= p.group;
+                                ++token;
+                            }
                         }
+                    } else {
+                        for (; x < rows; x += kStep)
+                            zero16(dst + x * 128 + ((vec % 8) ^ (x % 8)) * 16);
                     }
                     asm volatile("cp.async.wait_all;" ::: "memory");
                     fence_proxy_async_shared();
@@ -862,11 +875,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             merge_turn ^= 1;
             tmem_fence_after();
         };
-        for (uint32_t k = 0;; ++k) {
-            if (!announced(k))
-                break;
-            const Item item = S.item[k % kItems];
-            done_with(k);
+        // First one tile of nothing, while the kernel before ends and the first keys are on their way: it
+        // fetches the code (a first tile took 5500 cycles, the others 2000), and ends before the first
+        // product writes S.
+        bool dry = true;
+        for (uint32_t k = 0;;) {
+            Item item{};
+            if (!dry) {
+                if (!announced(k))
+                    break;
+                item = S.item[k % kItems];
+                done_with(k);
+                ++k;
+            } else {
+                item.rows = kTile;
+                item.nt = 1 + g;
+                item.len = item.keys = 4 * kTile;
+            }
             const int nt = item.nt;
             if (nt == 0)
                 break;
@@ -880,7 +905,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const int turns = wide ? nt : (nt - g + 1) / 2;  // this group's tiles
 
             uint32_t bits[kMaxTree / 32] = {};
-            if (p.parent && turns > 0) {
+            if (p.parent && turns > 0 && !dry) {
                 int32_t *par = S.group[g].parent;  // every warp of the group writes the same there
                 for (int i = lane; i < item.n; i += 32)
                     par[i] = p.parent[item.first + i];
@@ -905,8 +930,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             float M = -INFINITY, l = 0;
             bool any = false;  // the accumulator holds something
             for (int t = wide ? 0 : g; t < nt; t += wide ? 1 : 2) {
-                wait(&S.s_full[g], s_turn);
-                s_turn ^= 1;
+                if (!dry) {
+                    wait(&S.s_full[g], s_turn);
+                    s_turn ^= 1;
+                }
                 const int column = (item.t0 + t) * kTile;
                 if (warp_on) {
                     tmem_fence_after();
@@ -1003,7 +1030,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 }
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(&S.p_full[g]);
+                    mbar_arrive(dry ? &S.ready : &S.p_full[g]);
+            }
+            if (dry) {
+                dry = false;
+                asm volatile("griddepcontrol.wait;" ::: "memory");
+                continue;
             }
             if (turns > 0) {
                 wait(&S.o_full[g], o_turn);  // its last product
@@ -1121,6 +1153,7 @@ template <int DT, int DP, int W>
 __global__ void __launch_bounds__(256) join_kernel(CacheView c, AttentionParams p)
 {
     __shared__ float4 sums[8][32];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Partial x = p.partial[blockIdx.x];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp % W;
@@ -1303,20 +1336,23 @@ template <int DT, int DP>
 cudaError_t launch_attention(const CUtensorMap &kmap, const CUtensorMap &vmap, const CacheView &c,
                              const AttentionParams &p, int grid, cudaStream_t st)
 {
-    attention_kernel<DT, DP><<<grid, kAttnThreads, AttnSizes<DP>::kBytes, st>>>(kmap, vmap, c, p);
-    cudaError_t e = cudaGetLastError();
-    if (e)
-        return e;
     cudaLaunchConfig_t cfg{};
-    const int warps = p.max_rows <= 64 ? 4 : 1;  // per row
-    cfg.gridDim = dim3(grid, (p.max_rows * warps + 7) / 8);
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    cfg.stream = st;
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kAttnThreads);
+    cfg.dynamicSmemBytes = AttnSizes<DP>::kBytes;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attention_kernel<DT, DP>, kmap, vmap, c, p);
+    if (e)
+        return e;
+    const int warps = p.max_rows <= 64 ? 4 : 1;  // per row
+    cfg.gridDim = dim3(grid, (p.max_rows * warps + 7) / 8);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
     return warps == 4 ? cudaLaunchKernelEx(&cfg, join_kernel<DT, DP, 4>, c, p)
                       : cudaLaunchKernelEx(&cfg, join_kernel<DT, DP, 1>, c, p);
 }

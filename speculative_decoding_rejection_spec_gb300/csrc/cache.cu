@@ -14,6 +14,15 @@ namespace {
 constexpr int kBookThreads = 1024;  // the one block of reserve
 constexpr int kCopyThreads = 256;
 
+// Every kernel here is launched as a programmatic dependent of the one before it in its stream, and lets
+// the next one's blocks take their places as soon as all of its own have: each waits here, before it
+// reads or writes anything, until the kernel before has ended.
+__device__ __forceinline__ void begin_kernel()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // Whether cu[0 .. B] starts at 0, does not decrease and ends within N rows; the whole block.
 __device__ __forceinline__ bool block_layout_ok(const int32_t *cu, int B, int64_t N)
 {
@@ -69,6 +78,7 @@ __device__ __forceinline__ bool last_block(int32_t *ticket, int blocks)
 
 __global__ void __launch_bounds__(kCopyThreads) init_kernel(CacheView c)
 {
+    begin_kernel();
     const int64_t n = (int64_t)gridDim.x * blockDim.x;
     const int64_t t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     for (int64_t i = t; i < c.num_pages; i += n) {
@@ -129,11 +139,11 @@ __device__ __forceinline__ Ask reserve_ask(const CacheView &c, const int32_t *cu
 // each, which finds its request by bisection.
 __global__ void __launch_bounds__(kBookThreads) reserve_kernel(CacheView c, const int32_t *cu, int B)
 {
+    begin_kernel();
     __shared__ int32_t held_of[kBookThreads], copies_of[kBookThreads], shared_of[kBookThreads];
     __shared__ int64_t base_of[kBookThreads + 1];
     __shared__ int first_short, ncopy;
     const int r = threadIdx.x;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the copies wait for the whole of this
     const int32_t have = *c.num_free;
     int32_t here = 0, next = 0, len = 0, held = 0;
     if (r < B) {
@@ -235,7 +245,8 @@ __global__ void __launch_bounds__(kBookThreads) reserve_kernel(CacheView c, cons
 // The same for more requests than the block has threads, in turns, with its lists in the scratch.
 __global__ void __launch_bounds__(kBookThreads) reserve_many_kernel(CacheView c, const int32_t *cu, int B)
 {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    begin_kernel();
+
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     if (tid == 0)
         *c.ncopy = 0;
@@ -350,7 +361,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_rows_kernel(CacheView c)
     constexpr int U = 4;
     const int vecs = c.dim / 8;
     const int parts = (c.page_size * c.heads * vecs + U * kCopyThreads - 1) / (U * kCopyThreads);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    begin_kernel();
     const int64_t units = (int64_t)*c.ncopy * c.num_layers * 2 * parts;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
         const int64_t unit = u / parts;
@@ -388,6 +399,7 @@ struct NewRows {
 __global__ void __launch_bounds__(kCopyThreads) append_kernel(CacheView c, NewRows in, int64_t layer_offset,
                                                               const int32_t *cu, int B, int64_t N)
 {
+    begin_kernel();
     const int lane = threadIdx.x & 31;
     const bool ok = block_layout_ok(cu, B, N);
     if (!ok) {
@@ -464,6 +476,7 @@ __device__ __forceinline__ int64_t commit_length(const CacheView &c, const int32
 __global__ void __launch_bounds__(kCopyThreads) commit_chain_kernel(CacheView c, const int32_t *cu, int B, int64_t N,
                                                                     const int32_t *accepted, int32_t *out_lens)
 {
+    begin_kernel();
     if (!block_layout_ok(cu, B, N)) {
         if (blockIdx.x == 0 && threadIdx.x == 0)
             cache_error(c.error, SPEC_DEVERR_LAYOUT, -1);
@@ -485,6 +498,7 @@ __global__ void __launch_bounds__(kCopyThreads) commit_tree_kernel(CacheView c, 
                                                                    const int32_t *accepted, const int32_t *parent,
                                                                    const int32_t *last_node, int32_t *out_lens)
 {
+    begin_kernel();
     __shared__ int32_t par[kMaxTree], path[kMaxTree];
     __shared__ int64_t from[kMaxTree], to[kMaxTree];
     __shared__ int bad, moves;
@@ -576,6 +590,7 @@ __global__ void __launch_bounds__(kCopyThreads) commit_tree_kernel(CacheView c, 
 // A block per fork.
 __global__ void __launch_bounds__(kCopyThreads) fork_kernel(CacheView c, const int32_t *src, const int32_t *dst, int F)
 {
+    begin_kernel();
     const int f = blockIdx.x, tid = threadIdx.x;
     const int s = src[f], d = dst[f];
     bool bad = s < 0 || s >= c.num_requests || d < 0 || d >= c.num_requests || s == d;
@@ -622,6 +637,7 @@ constexpr int kReleaseThreads = 512;
 // which the last block reads in ascending order: the list does not depend on the order of atomics.
 __global__ void __launch_bounds__(kReleaseThreads) release_kernel(CacheView c, const int32_t *keep, int B)
 {
+    begin_kernel();
     const int tid = threadIdx.x;
     for (int r = blockIdx.x; r < B; r += gridDim.x) {
         const int len = c.lens[r], held = c.held[r];
@@ -709,7 +725,20 @@ cudaError_t current_sms(int *sms)
     return cudaSuccess;
 }
 
-spec_status launched() { return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA; }
+template <class... Params, class... Args>
+spec_status launch(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t st, Args... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
 
 bool pending() { return cudaPeekAtLastError() != cudaSuccess; }
 
@@ -740,8 +769,8 @@ spec_status spec_cache_init(const spec_cache *cache, void *stream)
         cudaSuccess)
         return SPEC_ERR_CUDA;
     const int64_t most = std::max<int64_t>(c.num_pages, (int64_t)c.num_requests * c.max_pages);
-    init_kernel<<<(unsigned)std::min<int64_t>((most + kCopyThreads - 1) / kCopyThreads, 1024), kCopyThreads, 0, st>>>(c);
-    return launched();
+    return launch(init_kernel, dim3((unsigned)std::min<int64_t>((most + kCopyThreads - 1) / kCopyThreads, 1024)),
+                  kCopyThreads, st, c);
 }
 
 spec_status spec_cache_error(const spec_cache *cache, void *stream, int32_t *error_bits, int32_t *first_bad_request)
@@ -780,22 +809,10 @@ spec_status spec_cache_reserve(const spec_cache *cache, const int32_t *cu_new, i
     if (B == 0)
         return SPEC_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (B <= kBookThreads)
-        reserve_kernel<<<1, kBookThreads, 0, st>>>(c, cu_new, B);
-    else
-        reserve_many_kernel<<<1, kBookThreads, 0, st>>>(c, cu_new, B);
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(sms * 8);
-    cfg.blockDim = dim3(kCopyThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, copy_rows_kernel, c) != cudaSuccess)
-        return SPEC_ERR_CUDA;
-    return launched();
+    s = launch(B <= kBookThreads ? reserve_kernel : reserve_many_kernel, dim3(1), kBookThreads, st, c, cu_new, B);
+    if (s != SPEC_OK)
+        return s;
+    return launch(copy_rows_kernel, dim3(sms * 8), kCopyThreads, st, c);
 }
 
 spec_status spec_cache_append(const spec_cache *cache, int32_t layer, const void *k_new, int64_t k_token_stride,
@@ -822,9 +839,8 @@ spec_status spec_cache_append(const spec_cache *cache, int32_t layer, const void
                      N > 1 ? k_token_stride : 0, c.heads > 1 ? k_head_stride : 0,
                      N > 1 ? v_token_stride : 0, c.heads > 1 ? v_head_stride : 0};
     const int64_t blocks = (N + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
-    append_kernel<<<(unsigned)blocks, kCopyThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-        c, in, layer * c.layer_stride, cu_new, B, N);
-    return launched();
+    return launch(append_kernel, dim3((unsigned)blocks), kCopyThreads, static_cast<cudaStream_t>(stream), c, in,
+                  layer * c.layer_stride, cu_new, B, N);
 }
 
 spec_status spec_cache_commit(const spec_cache *cache, const int32_t *cu_new, int32_t B, int64_t N,
@@ -849,17 +865,15 @@ spec_status spec_cache_commit(const spec_cache *cache, const int32_t *cu_new, in
     int32_t *out = out_lens ? out_lens : c.lens;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (!parent) {
-        commit_chain_kernel<<<(B + kCopyThreads - 1) / kCopyThreads, kCopyThreads, 0, st>>>(c, cu_new, B, N,
-                                                                                         num_accepted, out);
-        return launched();
+        return launch(commit_chain_kernel, dim3((B + kCopyThreads - 1) / kCopyThreads), kCopyThreads, st, c, cu_new, B,
+                      N, num_accepted, out);
     }
     // Blocks for every column once, as far as the device holds them (8 blocks per SM).
     const int64_t columns = (int64_t)c.num_layers * 2 * c.heads * (c.dim / 8);
     const int64_t split = std::max<int64_t>(
         1, std::min<int64_t>((columns + kCopyThreads - 1) / kCopyThreads, (int64_t)sms * 8 / B));
-    commit_tree_kernel<<<dim3((unsigned)B, (unsigned)split), kCopyThreads, 0, st>>>(c, cu_new, B, N, num_accepted,
-                                                                                   parent, last_node, out);
-    return launched();
+    return launch(commit_tree_kernel, dim3((unsigned)B, (unsigned)split), kCopyThreads, st, c, cu_new, B, N,
+                  num_accepted, parent, last_node, out);
 }
 
 spec_status spec_cache_fork(const spec_cache *cache, const int32_t *src, const int32_t *dst, int32_t num_forks,
@@ -875,8 +889,7 @@ spec_status spec_cache_fork(const spec_cache *cache, const int32_t *src, const i
         return SPEC_ERR_CUDA;
     if (num_forks == 0)
         return SPEC_OK;
-    fork_kernel<<<num_forks, kCopyThreads, 0, static_cast<cudaStream_t>(stream)>>>(c, src, dst, num_forks);
-    return launched();
+    return launch(fork_kernel, dim3(num_forks), kCopyThreads, static_cast<cudaStream_t>(stream), c, src, dst, num_forks);
 }
 
 spec_status spec_cache_release(const spec_cache *cache, const int32_t *keep_lens, int32_t B, void *stream)
@@ -892,8 +905,8 @@ spec_status spec_cache_release(const spec_cache *cache, const int32_t *keep_lens
         return SPEC_ERR_CUDA;
     if (B == 0)
         return SPEC_OK;
-    release_kernel<<<std::min(B, sms * 2), kReleaseThreads, 0, static_cast<cudaStream_t>(stream)>>>(c, keep_lens, B);
-    return launched();
+    return launch(release_kernel, dim3(std::min(B, sms * 2)), kReleaseThreads, static_cast<cudaStream_t>(stream), c,
+                  keep_lens, B);
 }
 
 }  // extern "C"
