@@ -52,10 +52,34 @@ constexpr int kMinShare = 2;        // least places of a block's share
 constexpr float kLazy = 8.0f;       // log2 of the growth that moves a row's maximum
 constexpr int kTmemColumns = 512;   // two groups: 128 of S (P over it), up to 128 of O
 
+// A block's share of the list: [begin(x), begin(x + 1)), in tiles of cost.
+struct Shares {
+    int64_t each;  // the first `more` shares have one more than each
+    int32_t blocks, more;
+    __device__ __forceinline__ void cut(int64_t cost, int most)
+    {
+        if (cost < INT32_MAX) {  // nearly always: a 64-bit division takes some hundred cycles
+            blocks = max(1, min(most, ((int)cost + kMinShare - 1) / kMinShare));
+            each = (uint32_t)cost / (uint32_t)blocks;
+        } else {
+            blocks = most;
+            each = cost / blocks;
+        }
+        more = (int)(cost - each * blocks);
+    }
+    __device__ __forceinline__ int64_t begin(int x) const { return each * x + min(x, more); }
+    // the block whose share holds place t
+    __device__ __forceinline__ int owner(int64_t t) const
+    {
+        const int64_t big = (each + 1) * more;
+        return (int)(t < big ? t / (each + 1) : more + (t - big) / each);
+    }
+};
+
 struct Partial {  // of the row block that starts in a block's share and goes on behind it
     int32_t r, h, b, rows;  // rows 0: none
-    int32_t last;           // the last block that works on it
-    int32_t pad[3];
+    int64_t last_place;     // of its last tile in the list
+    Shares shares;
 };
 
 struct AttentionParams {
@@ -200,7 +224,6 @@ struct alignas(16) Item {
     int32_t len, n, first; // of the request: committed tokens, new tokens, its first row
     int32_t q_use;         // Q slots used before (a narrow row block takes one, a wide one both)
     uint32_t slots;        // K / V slots used before
-    int32_t last;          // the last block that works on the row block
 };
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
@@ -305,33 +328,6 @@ __device__ __forceinline__ Request request_of(const CacheView &c, const Attentio
     return request_of(c, p, r, p.cu[r + 1] - p.cu[r], c.lens[r], report);
 }
 
-// A block's share of the list: [begin(x), begin(x + 1)), in tiles of cost.
-struct Shares {
-    int64_t total, each;  // the first `more` shares have one more than each
-    int blocks, more;
-    __device__ __forceinline__ void cut(int64_t cost, int most)
-    {
-        total = cost;
-        if (cost < INT32_MAX) {  // nearly always: a 64-bit division takes some hundred cycles
-            blocks = max(1, min(most, ((int)cost + kMinShare - 1) / kMinShare));
-            each = (int)cost / blocks;
-        } else {
-            blocks = most;
-            each = cost / blocks;
-        }
-        more = (int)(cost - each * blocks);
-    }
-    __device__ __forceinline__ int64_t begin(int x) const { return each * x + min(x, more); }
-    // the block whose share holds place t
-    __device__ __forceinline__ int owner(int64_t t) const
-    {
-        const int64_t big = (each + 1) * more;
-        if (total < INT32_MAX)
-            return t < big ? (int)t / (int)(each + 1) : more + (int)(t - big) / (int)each;
-        return (int)(t < big ? t / (each + 1) : more + (t - big) / each);
-    }
-};
-
 // Walks a block's share, one (request, head, row block) at a time; a whole warp.  A row block takes
 // kBlockCost places of the list before those of its tiles; a share that ends within them leaves the
 // row block to the next.
@@ -343,16 +339,14 @@ struct Walk {
     int64_t pos, end; // place of the row block's part in the list
 
     // false when the share holds no tile
-    __device__ __forceinline__ bool start(const CacheView &c, const AttentionParams &p, const Shares &s, int first,
-                                          int64_t base)
+    // r and q: the request in which the share begins, after `base` places
+    __device__ __forceinline__ bool start(const AttentionParams &p, const Shares &s, int64_t base)
     {
         pos = s.begin(blockIdx.x);
         end = s.begin(blockIdx.x + 1);
-        r = first;
-        q = request_of(c, p, r, false);
         int64_t at = pos - base;
-        h = at < INT32_MAX ? (int)at / q.cost : (int)(at / q.cost);
-        at -= (int64_t)h * q.cost;
+        for (h = 0; at >= q.cost; ++h)
+            at -= q.cost;
         for (b = 0; at >= kBlockCost + block_tiles(p, q, b); ++b)
             at -= kBlockCost + block_tiles(p, q, b);
         return here(p, (int)at);
@@ -458,13 +452,13 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     return d;
 }
 
-// The shares of the list, and the request in which this block's begins (with the work before it); a
-// whole warp.  False when the block has no share, or cu is malformed.
-__device__ __forceinline__ bool find_share(const CacheView &c, const AttentionParams &p, Shares *shares, int *first,
+// The shares of the list, and the request in which this block's begins (w->r and w->q, with the work
+// before it); a whole warp.  False when the block has no share, or cu is malformed.
+__device__ __forceinline__ bool find_share(const CacheView &c, const AttentionParams &p, Shares *shares, Walk *w,
                                            int64_t *base, int lane)
 {
     constexpr int U = 4;  // requests of a lane in a turn
-    int cost[U];
+    int cost[U], size[U], len[U];
     int64_t before = 0, at = 0;
     bool bad = false, wrong = false;
     // Twice: the total makes the shares, then the block finds its own.  A batch of one turn keeps its
@@ -475,7 +469,7 @@ __device__ __forceinline__ bool find_share(const CacheView &c, const AttentionPa
         for (int r0 = 0; r0 < p.B; r0 += 32 * U) {
             const int r = r0 + lane * U;
             if (pass == 0 || p.B > 32 * U) {
-                int32_t cu[U + 1], len[U];
+                int32_t cu[U + 1];
 #pragma unroll
                 for (int i = 0; i <= U; ++i)
                     cu[i] = p.cu[min(r + i, p.B)];
@@ -488,9 +482,10 @@ __device__ __forceinline__ bool find_share(const CacheView &c, const AttentionPa
                 for (int i = 0; i < U; ++i) {
                     bad |= cu[i] > cu[i + 1] || cu[i + 1] > p.N;
                     cost[i] = 0;
+                    size[i] = cu[i + 1] - cu[i];
                     if (r + i < p.B && !bad) {
-                        cost[i] = request_of(c, p, r + i, cu[i + 1] - cu[i], len[i], false).cost;
-                        wrong |= cost[i] == 0 && cu[i + 1] > cu[i];
+                        cost[i] = request_of(c, p, r + i, size[i], len[i], false).cost;
+                        wrong |= cost[i] == 0 && size[i] > 0;
                     }
                     sum += (int64_t)cost[i] * c.heads;
                 }
@@ -505,21 +500,29 @@ __device__ __forceinline__ bool find_share(const CacheView &c, const AttentionPa
             }
             if (pass == 1) {
                 const int64_t want = shares->begin(blockIdx.x);
-                int found = -1;
+                int found = -1, its_size = 0, its_len = 0, its_cost = 0;
                 int64_t place = at, found_at = 0;
 #pragma unroll
                 for (int i = 0; i < U; ++i) {
                     const int64_t work = (int64_t)cost[i] * c.heads;
                     if (place <= want && want < place + work) {
                         found = r + i;
+                        its_size = size[i];
+                        its_len = len[i];
+                        its_cost = cost[i];
                         found_at = place;
                     }
                     place += work;
                 }
                 const unsigned who = __ballot_sync(kFull, found >= 0);
                 if (who) {
-                    *first = __shfl_sync(kFull, found, __ffs(who) - 1);
-                    *base = __shfl_sync(kFull, found_at, __ffs(who) - 1);
+                    const int from = __ffs(who) - 1;
+                    w->r = __shfl_sync(kFull, found, from);
+                    w->q.n = __shfl_sync(kFull, its_size, from);
+                    w->q.len = __shfl_sync(kFull, its_len, from);
+                    w->q.cost = __shfl_sync(kFull, its_cost, from);
+                    w->q.rows = w->q.n * p.group;
+                    *base = __shfl_sync(kFull, found_at, from);
                     return true;
                 }
             }
@@ -779,10 +782,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (warp == kWalkWarp) {
                 if (lane == 0)
                     p.partial[blockIdx.x].rows = 0;
-                int first;
                 int64_t base;
-                more = find_share(c, p, &shares, &first, &base, lane) &&
-                       (w.start(c, p, shares, first, base) || w.next(c, p));
+                more = find_share(c, p, &shares, &w, &base, lane) && (w.start(p, shares, base) || w.next(c, p));
             }
             for (uint32_t k = 0;; ++k) {
                 Item *mine = &S.item[k % kItems];
@@ -805,7 +806,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             x.first = p.cu[w.r];
                             x.q_use = q_use;
                             x.slots = slots;
-                            x.last = shares.owner(w.last_place());
+                            if (w.t0 == 0 && w.t1 < w.tiles) {  // goes on behind the share: for the join
+                                Partial &y = p.partial[blockIdx.x];
+                                y.r = w.r;
+                                y.h = w.h;
+                                y.b = w.b;
+                                y.rows = x.rows;
+                                y.last_place = w.last_place();
+                                y.shares = shares;
+                            }
                         }
                         *mine = x;
                         mbar_arrive(&S.item_full[k % kItems]);
@@ -1119,14 +1128,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 }
                 meet();
             }
-            if (!whole && item.t0 == 0 && tid == 0) {
-                Partial &x = p.partial[blockIdx.x];
-                x.r = item.r;
-                x.h = item.h;
-                x.b = item.b;
-                x.last = item.last;
-                x.rows = item.rows;
-            }
         }
         tmem_fence_before();
     }
@@ -1160,7 +1161,7 @@ __global__ void __launch_bounds__(256) join_kernel(CacheView c, AttentionParams 
     const int row = blockIdx.y * (8 / W) + warp / W;
     if (blockIdx.y * (8 / W) >= x.rows)
         return;
-    const int parts = row < x.rows ? x.last - (int)blockIdx.x + 1 : 0;
+    const int parts = row < x.rows ? x.shares.owner(x.last_place) - (int)blockIdx.x + 1 : 0;
     // the first part is the tail of its block's share, the others lie at the head of theirs
     auto place = [&](int i) { return ((int64_t)(blockIdx.x + i) * 2 + (i == 0)) * p.max_rows + row; };
     constexpr int kMost = (kMaxGrid + 31) / 32;
