@@ -10,14 +10,15 @@
 //                   maximum, exponentials, P back over S.  M only moves when a row's maximum has
 //                   grown by more than 2^8 since (P stays below 2^8, exact in its sum's fp32), so
 //                   the accumulator in tensor memory is rarely rescaled.
-//   warps 9, 10 / 11, 15  load tiles of K / V, page by page, through TMA into a ring of slots; two
+//   warps 10, 11 / 14, 15  load tiles of K / V, page by page, through TMA into a ring of slots; two
 //                   warps share a tile's copies: one warp cannot issue those of small pages fast enough
 //                   (a streaming loop over 16-token pages reached 3.6 TB/s with one warp issuing, 6.0
 //                   with two, 6.6 with four)
 //   warp 13         issues the matrix products (one thread)
-//   warps 14, 8, 12 load Q; the first walks the list of work ahead of the others and announces it in
-//                   a ring.  Warps 8 and 12 share a scheduler with warps 0 and 4, which have all of the
-//                   softmax's work when a row block has at most 32 rows, so they have the least to do.
+//   warps 12, 8, 9  load Q; the first walks the list of work ahead of the others and announces it in
+//                   a ring
+// (a scheduler serves the warps of one number modulo 4: the products share theirs with no loads, and
+// warps 0 and 4, which have all of the softmax's work when a row block has at most 32 rows, with none)
 // A block of more than 128 rows ("wide") gives each group 128 of them and both use every tile: the
 // products of one group run while the other computes its exponentials.  A block of at most 128 rows
 // ("narrow": decoding and most verify steps) gives both groups the same rows and every other tile,
@@ -42,7 +43,7 @@ namespace {
 
 constexpr int kTile = 128;          // keys per tile, and rows per softmax group
 constexpr int kBlockRows = 256;     // query rows of a (request, head, row block)
-constexpr int kSoftmaxWarps = 8, kLoadWarps = 4, kMmaWarp = 13, kWalkWarp = 14, kQueryWarps = 3;
+constexpr int kSoftmaxWarps = 8, kLoadWarps = 4, kMmaWarp = 13, kWalkWarp = 12, kQueryWarps = 3;
 constexpr int kAttnThreads = 512;
 constexpr int kSoftmaxRegs = 144, kOtherRegs = 112;  // 256 threads of each: the launch's 128 a thread in all
 constexpr int kItems = 4;           // row blocks announced ahead
@@ -608,11 +609,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         // Up to here the block may run beside the end of the kernel before; what that wrote is read behind.
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        const int load_warp = warp == 15 ? 3 : warp - 9;  // 0, 1: K; 2, 3: V
-        if (load_warp >= 0 && load_warp < kLoadWarps && warp != 12) {
+        if (warp & 2) {
             // Slot order: K of tile 0, then K of tile t + 1 and V of tile t, as the products use them.
-            const bool is_v = load_warp >= 2;
-            const int half = load_warp & 1;  // copies (piece, chunk) of every second number
+            const bool is_v = warp >= 14;
+            const int half = warp & 1;  // copies (piece, chunk) of every second number
             const CUtensorMap *map = is_v ? &vmap : &kmap;
             const int pieces = kTile / p.box;
             // Copies of 32 pieces, one per lane; token < 0: behind the last key.
@@ -775,7 +775,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         } else {
             Walk w;
             Shares shares;
-            const int part = warp == kWalkWarp ? 0 : warp == 8 ? 1 : 2;
+            const int part = warp == kWalkWarp ? 0 : warp - 7;
             int q_use = 0;
             uint32_t slots = 0;
             bool more = false;
@@ -1132,7 +1132,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         tmem_fence_before();
     }
     __syncthreads();
-    if (warp == 9 && S.gave_up) {
+    if (warp == 10 && S.gave_up) {
         // copies that nobody waited for; a slot that none was started into waits in vain, for a while
         for (int i = 0; i < SLOTS; ++i)
             for (uint32_t n = 0; n < 4096 && !(mbar_try_wait(&S.full[i], 0) && mbar_try_wait(&S.full[i], 1)); ++n) {
