@@ -134,6 +134,7 @@ class PagedCache:
         # what every call needs, looked up once: the tensors of a cache do not change
         self.ref, self.device, self.index = ctypes.byref(self.struct), dev, dev.index
         self.dtype, self.heads, self.dim = k.dtype, H, D
+        self.workspaces = {}  # attention's, by stream
 
 
 def _code(t) -> int:
@@ -270,6 +271,27 @@ def attention_workspace_size(c: PagedCache, num_q_heads: int, B: int, N: int) ->
     return int(n)
 
 
+def _workspace(c, H, B, N, stream):
+    """A workspace for one call: the stream's own, kept with the cache (calls of a stream run one after
+    the other); under capture a new one from the graph's memory, as graphs may run at the same time."""
+    rows = min(256, N * (H // c.heads))  # its size grows with these
+    handle = torch._C._cuda_getCurrentRawStream(c.index) if stream is None else stream.cuda_stream
+    kept = c.workspaces.get(handle)
+    if kept is not None and kept[0] >= rows and not torch._C._cuda_isCurrentStreamCapturing():
+        return kept[1]
+    size = _lib.spec_attention_workspace_size(c.ref, H, B, N)
+    if stream is None:
+        workspace = torch.empty(size, dtype=torch.uint8, device=c.device)
+    else:
+        with torch.cuda.stream(stream):
+            workspace = torch.empty(size, dtype=torch.uint8, device=c.device)
+            if torch._C._cuda_isCurrentStreamCapturing():
+                return workspace
+    if size and not torch._C._cuda_isCurrentStreamCapturing():
+        c.workspaces[handle] = (rows, workspace)
+    return workspace
+
+
 def attention(c: PagedCache, layer: int, q, cu_new, parent=None, scale=None, out=None, lse=None, workspace=None,
               stream=None):
     """Attention of the new tokens q [N, q_heads, head_dim] over the cache (spec_attention); returns
@@ -277,8 +299,8 @@ def attention(c: PagedCache, layer: int, q, cu_new, parent=None, scale=None, out
 
     ``parent`` (int32 [N]) makes the new tokens draft trees, otherwise they are chains; ``scale``
     defaults to head_dim ** -0.5; ``lse`` (float32 [N, q_heads], given) receives the log of each
-    row's softmax sum; ``workspace`` (uint8) may be given to reuse it: calls that can run at the
-    same time need one each.  Rows behind ``cu_new[B]`` are left as they were in ``out``.
+    row's softmax sum; ``workspace`` (uint8) may be given, calls that can run at the same time need
+    one each (without one, the cache keeps one per stream, and a captured graph has its own).  Rows behind ``cu_new[B]`` are left as they were in ``out``.
     """
     B = _cu(c, cu_new)
     qt, qh = _rows(c, q, None, "q")
@@ -287,17 +309,16 @@ def attention(c: PagedCache, layer: int, q, cu_new, parent=None, scale=None, out
         _int32(parent, (N,), "parent", c.device)
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        ot, oh = H * c.dim, c.dim
     elif out.shape != q.shape:
         raise ValueError("out must have the shape of q")
-    ot, oh = _rows(c, out, H, "out")
+    else:
+        ot, oh = _rows(c, out, H, "out")
     if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (N, H) or not lse.is_contiguous() or
                             lse.device != c.device):
         raise TypeError(f"lse must be a contiguous float32 tensor of shape {(N, H)} on {c.device}")
     if workspace is None:
-        workspace = torch.empty(_lib.spec_attention_workspace_size(c.ref, H, B, N), dtype=torch.uint8,
-                                device=c.device)
-        if stream is not None:
-            workspace.record_stream(stream)
+        workspace = _workspace(c, H, B, N, stream)
     elif workspace.dtype is not torch.uint8 or workspace.device != c.device or not workspace.is_contiguous():
         raise TypeError(f"workspace must be a contiguous uint8 tensor on {c.device}")
     _call(c, "spec_attention", stream, layer, q.data_ptr(), qt, qh, H, cu_new.data_ptr(), B, N, _ptr(parent),

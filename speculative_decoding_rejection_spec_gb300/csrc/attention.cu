@@ -193,6 +193,16 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *bar)
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
+__device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(ok)
+                 : "r"(smem_addr(bar)), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+
 __device__ __forceinline__ void fence_proxy_async_shared()
 {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -261,14 +271,18 @@ template <int SLOTS> struct alignas(16) AttnShared {
 
 // Waits for a barrier's phase, a bounded number of polls.  When one wait gives up, all do: no row block
 // is begun and no copy started any more, what has begun runs through without waiting (its indices are
-// those of an announced row block), and the roles leave together.
+// those of an announced row block), and the roles leave together.  A wait of try_wait is suspended and
+// woken late; the thread that issues the products polls instead (SPIN): prompt chunks 0.356 -> 0.330 ms.
+// The others do not, for the sake of the schedulers they share.
+template <bool SPIN>
 __device__ __forceinline__ bool attn_wait(uint64_t *bar, uint32_t parity, volatile int32_t *gave_up, int32_t *error)
 {
-    for (uint32_t i = 0; i < kWaitLimit; ++i)
-        if (mbar_try_wait(bar, parity))
+    for (uint32_t i = 0; i < (SPIN ? 64 * kWaitLimit : kWaitLimit); ++i) {
+        if (SPIN ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity))
             return true;
-        else if (*gave_up)
+        if ((!SPIN || i % 64 == 63) && *gave_up)
             return false;
+    }
     *gave_up = 1;
     atomicOr(error, SPEC_DEVERR_TIMEOUT);
     return false;
@@ -593,7 +607,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = S.tmem;
-    auto wait = [&](uint64_t *bar, uint32_t parity) { return attn_wait(bar, parity, &S.gave_up, c.error); };
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return attn_wait<false>(bar, parity, &S.gave_up, c.error); };
+    auto spin = [&](uint64_t *bar, uint32_t parity) { return attn_wait<true>(bar, parity, &S.gave_up, c.error); };
 
     // Waits for the row block announced as number k (in S.item[k % kItems]); the caller gives the entry
     // back with done_with() when it has read it.
@@ -683,7 +698,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                v_desc = smem_desc(smem_addr(ring), Z::kChunk);
                 uint32_t slot = 0, turn = 0, p_turn = 0;  // p_turn: a bit per group
                 auto take = [&]() {                       // the next slot, landed
-                    wait(&S.full[slot], turn);
+                    spin(&S.full[slot], turn);
                     const uint32_t s = slot;
                     if (++slot == SLOTS) {
                         slot = 0;
@@ -707,7 +722,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                mma_desc<DT>(DP, true), i > 0 || add);
                 };
                 auto p_ready = [&](int g) {
-                    wait(&S.p_full[g], p_turn >> g & 1);
+                    spin(&S.p_full[g], p_turn >> g & 1);
                     p_turn ^= 1u << g;
                     tmem_fence_after();
                 };
