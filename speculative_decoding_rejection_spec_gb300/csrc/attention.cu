@@ -90,7 +90,8 @@ struct AttentionParams {
     int64_t q_token, q_head, out_token, out_head;  // elements
     int32_t heads, group, B;
     uint32_t group_mul, group_shift;  // m / group = m * group_mul >> group_shift for 0 <= m < 2^31
-    int32_t box;  // tokens per copy
+    int32_t box;       // tokens per copy of K or V
+    int32_t q_tokens;  // tokens of 128 query rows, when the group divides them (then Q's wide tiles come as one copy)
     int64_t N;
     const int32_t *cu, *parent;
     float scale_log2;
@@ -236,6 +237,14 @@ struct alignas(16) Item {
     int32_t q_use;         // Q slots used before (a narrow row block takes one, a wide one both)
     uint32_t slots;        // K / V slots used before
 };
+
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap *map, int x, int head, int token, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+                 "l"(map), "r"(x), "r"(head), "r"(token), "r"(smem_addr(bar))
+                 : "memory");
+}
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
 {
@@ -561,8 +570,8 @@ __device__ __forceinline__ bool find_share(const CacheView &c, const AttentionPa
 
 template <int DT, int DP>
 __global__ void __launch_bounds__(kAttnThreads, 1)
-    attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, CacheView c,
-                     AttentionParams p)
+    attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                     const __grid_constant__ CUtensorMap qmap, CacheView c, AttentionParams p)
 {
     using Z = AttnSizes<DP>;
     constexpr int SLOTS = Z::kSlots;
@@ -574,6 +583,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (tid == 0) {
         prefetch_map(&kmap);
         prefetch_map(&vmap);
+        if (p.q_tokens)
+            prefetch_map(&qmap);
     }
     if (tid == 0) {
         for (int i = 0; i < SLOTS; ++i) {
@@ -696,9 +707,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (elect_one()) {
                 const uint64_t q_desc = smem_desc(smem_addr(qtile), 16), k_desc = smem_desc(smem_addr(ring), 16),
                                v_desc = smem_desc(smem_addr(ring), Z::kChunk);
+                // A wait costs this thread some 200 cycles even when there is nothing to wait for, and it has
+                // to stay ahead of the products it has issued (about seven fit the queue, 500 cycles): the
+                // barriers of the next step are looked at together, beside the commits of this one, and
+                // waited for only if they were not through then.
                 uint32_t slot = 0, turn = 0, p_turn = 0;  // p_turn: a bit per group
-                auto take = [&]() {                       // the next slot, landed
-                    spin(&S.full[slot], turn);
+                auto full_here = [&](uint32_t i) {        // slot i from the next
+                    const uint32_t s = slot + i;
+                    return s < SLOTS ? mbar_test_wait(&S.full[s], turn) : mbar_test_wait(&S.full[s - SLOTS], turn ^ 1);
+                };
+                auto take = [&](bool here) {  // the next slot, landed
+                    if (!here)
+                        spin(&S.full[slot], turn);
                     const uint32_t s = slot;
                     if (++slot == SLOTS) {
                         slot = 0;
@@ -721,8 +741,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         mma_ts(tmem + g * 256 + kTile, tmem + g * 256 + i * 8, b + (i * 2048 >> 4),
                                mma_desc<DT>(DP, true), i > 0 || add);
                 };
-                auto p_ready = [&](int g) {
-                    spin(&S.p_full[g], p_turn >> g & 1);
+                auto p_here = [&](int g) { return mbar_test_wait(&S.p_full[g], p_turn >> g & 1); };
+                auto p_ready = [&](int g, bool here) {
+                    if (!here)
+                        spin(&S.p_full[g], p_turn >> g & 1);
                     p_turn ^= 1u << g;
                     tmem_fence_after();
                 };
@@ -738,46 +760,66 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         break;
                     for (int g = 0; g <= (int)wide; ++g)
                         wait(&S.q_full[(q_use + g) & 1], (q_use + g) >> 1 & 1);
+                    // step t: scores of tile t, outputs of tile t - 1
+                    bool k_in = false, v_in = false, p_in = false;
                     if (!wide) {
                         for (int t = 0; t <= nt; ++t) {
+                            const int g = (t - 1) & 1;  // the group of tile t - 1
+                            uint32_t kslot = 0, vslot = 0;
                             if (t < nt) {
-                                const uint32_t kslot = take();
+                                kslot = take(k_in);
                                 scores(t & 1, kslot, q_use & 1);
                                 mma_commit(&S.s_full[t & 1]);
-                                mma_commit(&S.empty[kslot]);
-                                if (t == nt - 1)
-                                    mma_commit(&S.q_empty[q_use & 1]);
                             }
                             if (t > 0) {
-                                const int u = t - 1, g = u & 1;
-                                const uint32_t vslot = take();
-                                p_ready(g);
-                                outputs(g, vslot, u >= 2);
-                                mma_commit(&S.empty[vslot]);
-                                if (u + 2 >= nt)
+                                vslot = take(v_in);
+                                p_ready(g, p_in);
+                                outputs(g, vslot, t > 2);
+                                if (t + 1 >= nt)
                                     mma_commit(&S.o_full[g]);
                             }
+                            if (t < nt) {
+                                const bool more = t + 1 < nt;
+                                k_in = more && full_here(0);
+                                v_in = full_here(more);
+                                p_in = p_here(t & 1);
+                                mma_commit(&S.empty[kslot]);
+                                if (!more)
+                                    mma_commit(&S.q_empty[q_use & 1]);
+                            }
+                            if (t > 0)
+                                mma_commit(&S.empty[vslot]);
                         }
                     } else {
                         for (int t = 0; t <= nt; ++t) {
-                            const uint32_t kslot = t < nt ? take() : 0, vslot = t > 0 ? take() : 0;
+                            uint32_t kslot = 0, vslot = 0;
+                            if (t < nt)
+                                kslot = take(k_in);
+                            if (t > 0)
+                                vslot = take(v_in);
+#pragma unroll
                             for (int g = 0; g < 2; ++g) {
                                 if (t > 0) {
-                                    p_ready(g);
+                                    p_ready(g, g == 0 && p_in);
                                     outputs(g, vslot, t > 1);
                                 }
                                 if (t < nt)
                                     scores(g, kslot, (q_use + g) & 1);
                                 mma_commit(t < nt ? &S.s_full[g] : &S.o_full[g]);
                             }
+                            if (t < nt) {
+                                const bool more = t + 1 < nt;
+                                k_in = more && full_here(0);
+                                v_in = full_here(more);
+                                p_in = p_here(0);
+                                mma_commit(&S.empty[kslot]);
+                                if (!more) {
+                                    mma_commit(&S.q_empty[0]);
+                                    mma_commit(&S.q_empty[1]);
+                                }
+                            }
                             if (t > 0)
                                 mma_commit(&S.empty[vslot]);
-                            if (t < nt)
-                                mma_commit(&S.empty[kslot]);
-                            if (t == nt - 1) {
-                                mma_commit(&S.q_empty[0]);
-                                mma_commit(&S.q_empty[1]);
-                            }
                         }
                     }
                 }
@@ -854,6 +896,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     const int at = part * 32 + lane, vec = at % kVecs;
                     const uint32_t dst = smem_addr(qtile) + (use & 1) * Z::kSlotBytes + vec / 8 * Z::kChunk;
                     const int m0 = item.b * kBlockRows + g * kTile, rows = min(kTile, item.rows - g * kTile);
+                    if (count == 2 && p.q_tokens) {
+                        // a wide row block's: one copy for each 64 elements (rows behind the last are not
+                        // looked at); row by row they took 7 us, with the products waiting
+                        if (warp == kWalkWarp && !S.gave_up) {
+                            if (elect_one()) {
+                                mbar_arrive_expect_tx(&S.q_full[use & 1], Z::kSlotBytes);
+#pragma unroll
+                                for (int i = 0; i < DP / 64; ++i)
+                                    tma_rows(smem_addr(qtile) + (use & 1) * Z::kSlotBytes + i * Z::kChunk, &qmap,
+                                             i * 64, item.h * p.group, item.first + by_group(p, m0),
+                                             &S.q_full[use & 1]);
+                            }
+                        } else if (lane == 0) {
+                            mbar_arrive(&S.q_full[use & 1]);
+                        }
+                        __syncwarp();
+                        continue;
+                    }
                     int x = at / kVecs, token = by_group(p, m0 + x), head = (m0 + x) - token * p.group;
                     const int more_tokens = by_group(p, kStep), more_heads = kStep - more_tokens * p.group;
                     const char *src = p.q + 2 * ((int64_t)item.first * p.q_token +
@@ -1149,9 +1209,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     __syncthreads();
     if (warp == 10 && S.gave_up) {
         // copies that nobody waited for; a slot that none was started into waits in vain, for a while
-        for (int i = 0; i < SLOTS; ++i)
-            for (uint32_t n = 0; n < 4096 && !(mbar_try_wait(&S.full[i], 0) && mbar_try_wait(&S.full[i], 1)); ++n) {
+        for (int i = 0; i < SLOTS + 2; ++i) {
+            uint64_t *bar = i < SLOTS ? &S.full[i] : &S.q_full[i - SLOTS];
+            for (uint32_t n = 0; n < 4096 && !(mbar_try_wait(bar, 0) && mbar_try_wait(bar, 1)); ++n) {
             }
+        }
     }
     __syncthreads();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -1311,6 +1373,23 @@ bool encode_pages(CUtensorMap *map, const CacheView &c, int dtype, char *base, i
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The queries as a tensor (head_dim, head, token), whose boxes are the 128 rows of a softmax group.
+bool encode_queries(CUtensorMap *map, const CacheView &c, int dtype, const AttentionParams &p)
+{
+    const EncodeTiled f = encode_tiled();
+    if (!f)
+        return false;
+    const cuuint64_t least = 2 * (cuuint64_t)c.dim;
+    const cuuint64_t dims[3] = {(cuuint64_t)c.dim, (cuuint64_t)p.heads, (cuuint64_t)p.N};
+    const cuuint64_t strides[2] = {p.heads > 1 ? 2 * (cuuint64_t)p.q_head : least,
+                                   p.N > 1 ? 2 * (cuuint64_t)p.q_token : least};
+    const cuuint32_t boxes[3] = {64, (cuuint32_t)p.group, (cuuint32_t)p.q_tokens}, steps[3] = {1, 1, 1};
+    return f(map, dtype == SPEC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+             const_cast<char *>(p.q), dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 constexpr int kMaxDevices = 64;
 
 // SMs of the current device; sets the kernels' shared memory on its first call there.
@@ -1349,8 +1428,8 @@ cudaError_t current_sms(int *sms)
 }
 
 template <int DT, int DP>
-cudaError_t launch_attention(const CUtensorMap &kmap, const CUtensorMap &vmap, const CacheView &c,
-                             const AttentionParams &p, int grid, cudaStream_t st)
+cudaError_t launch_attention(const CUtensorMap &kmap, const CUtensorMap &vmap, const CUtensorMap &qmap,
+                             const CacheView &c, const AttentionParams &p, int grid, cudaStream_t st)
 {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
@@ -1362,7 +1441,7 @@ cudaError_t launch_attention(const CUtensorMap &kmap, const CUtensorMap &vmap, c
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kAttnThreads);
     cfg.dynamicSmemBytes = AttnSizes<DP>::kBytes;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, attention_kernel<DT, DP>, kmap, vmap, c, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attention_kernel<DT, DP>, kmap, vmap, qmap, c, p);
     if (e)
         return e;
     const int warps = p.max_rows <= 64 ? 4 : 1;  // per row
@@ -1451,22 +1530,25 @@ spec_status spec_attention(const spec_cache *cache, int32_t layer, const void *q
     p.part_ml = reinterpret_cast<float2 *>(ws + plan.ml);
     p.part_o = reinterpret_cast<float *>(ws + plan.o);
     p.max_rows = plan.max_rows;
+    // (only where a row block can have more than 128 rows)
+    p.q_tokens = kTile % p.group == 0 && N * p.group > kTile ? kTile / p.group : 0;
     p.box = 8;
     while (p.box < kTile && c.page_size % (2 * p.box) == 0)
         p.box *= 2;
-    CUtensorMap kmap, vmap;
+    CUtensorMap kmap, vmap, qmap{};
     if (!encode_pages(&kmap, c, cache->dtype, c.k + 2 * layer * c.layer_stride, p.box) ||
-        !encode_pages(&vmap, c, cache->dtype, c.v + 2 * layer * c.layer_stride, p.box))
+        !encode_pages(&vmap, c, cache->dtype, c.v + 2 * layer * c.layer_stride, p.box) ||
+        (p.q_tokens && !encode_queries(&qmap, c, cache->dtype, p)))
         return SPEC_ERR_UNSUPPORTED;
     const int grid = std::min(sms, kMaxGrid);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (cache->dtype == SPEC_BF16)
-        e = plan.dp == 64 ? launch_attention<SPEC_BF16, 64>(kmap, vmap, c, p, grid, st)
-                          : launch_attention<SPEC_BF16, 128>(kmap, vmap, c, p, grid, st);
+        e = plan.dp == 64 ? launch_attention<SPEC_BF16, 64>(kmap, vmap, qmap, c, p, grid, st)
+                          : launch_attention<SPEC_BF16, 128>(kmap, vmap, qmap, c, p, grid, st);
     else
-        e = plan.dp == 64 ? launch_attention<SPEC_F16, 64>(kmap, vmap, c, p, grid, st)
-                          : launch_attention<SPEC_F16, 128>(kmap, vmap, c, p, grid, st);
+        e = plan.dp == 64 ? launch_attention<SPEC_F16, 64>(kmap, vmap, qmap, c, p, grid, st)
+                          : launch_attention<SPEC_F16, 128>(kmap, vmap, qmap, c, p, grid, st);
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 

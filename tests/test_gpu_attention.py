@@ -65,6 +65,9 @@ class Case:
         k, v = (torch.zeros(shape, dtype=dt, device="cuda") for _ in range(2))
         if layout == "hnd":
             k, v = k.transpose(2, 3), v.transpose(2, 3)
+        if layout == "hpn":
+            k, v = (torch.zeros((layers, heads, NP, page, dim), dtype=dt, device="cuda").permute(0, 2, 3, 1, 4)
+                    for _ in range(2))
         k[layer], v[layer] = kv[0].cuda(), kv[1].cuda()
         ints = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")
         self.c = cache.PagedCache(k, v, page_table=dev(table), lens=dev(ctx), held=dev(need), ref_counts=ints(NP),
@@ -175,6 +178,37 @@ def test_tree_that_is_a_chain_equals_the_chain():
                                          ([129, 257], [0, 127], 5), ([1031], [100], 3)])
 def test_prompt_chunks(n, ctx, group):
     c = Case(n, ctx, heads=2, group=group, page=32, seed=sum(n))
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("dim,group,dtype", [(72, 4, "bf16"), (96, 1, "f16"), (40, 16, "bf16"), (128, 6, "f16"),
+                                             (64, 128, "f16")])
+@pytest.mark.parametrize("pad", [0, 5])
+def test_wide_blocks_of_odd_shapes(dim, group, dtype, pad):
+    """Row blocks of more than 128 rows, the last one ending with the tensor or before padding rows."""
+    n = [3 * 256 // group + 1, 130 // group + 1, 1]
+    c = Case(n, [140, 0, 77], heads=2, group=group, dim=dim, page=24, dtype=dtype, pad=pad, seed=dim)
+    c.check(*c.run())
+
+
+def test_many_row_blocks_per_share():
+    """More row blocks than the device has SMs by far, narrow and wide ones of one tile to several: every
+    share walks through a run of them, across requests without new tokens."""
+    rng = np.random.default_rng(8)
+    n = np.where(rng.random(1100) < 0.3, 0, rng.integers(1, 4, 1100))
+    n[::37] = 70
+    ctx = rng.integers(0, 200, 1100)
+    ctx[::10] = rng.integers(0, 900, 110)
+    c = Case(n, ctx, heads=2, group=4, dim=64, page=16, dtype="f16", seed=12, poison=False)
+    c.check(*c.run())
+    c = Case(n[:300], ctx[:300], heads=4, group=2, dim=128, page=32, seed=13, poison=False)
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("layout", ["hpn"])
+def test_pages_inside_heads(layout):
+    """A head's pages together: a page's stride is below a head's."""
+    c = Case([3, 1, 40], [500, 127, 77], page=16, layout=layout, layers=2, layer=1, seed=3)
     c.check(*c.run())
 
 
