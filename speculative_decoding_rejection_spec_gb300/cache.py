@@ -19,6 +19,7 @@ request r.  Chains of k_r drafts are k_r + 1 new tokens: ``cu_new = cu_num_draft
 from __future__ import annotations
 
 import ctypes
+import threading
 from dataclasses import dataclass, field
 
 import torch
@@ -97,6 +98,8 @@ class PagedCache:
 
     def __post_init__(self):
         k, v, dev = self.k, self.v, self.k.device
+        if dev.type != "cuda":
+            raise ValueError("a cache lives on a CUDA device")
         if k.dtype not in (torch.bfloat16, torch.float16) or v.dtype != k.dtype:
             raise TypeError("keys and values must both be bfloat16 or both float16")
         if k.dim() != 5 or k.shape != v.shape or k.stride(4) != 1 or v.stride(4) != 1:
@@ -272,10 +275,12 @@ def attention_workspace_size(c: PagedCache, num_q_heads: int, B: int, N: int) ->
 
 
 def _workspace(c, H, B, N, stream):
-    """A workspace for one call: the stream's own, kept with the cache (calls of a stream run one after
-    the other); under capture a new one from the graph's memory, as graphs may run at the same time."""
+    """A workspace for one call: that of the stream and the host thread, kept with the cache (their calls
+    run one after the other); under capture a new one from the graph's memory, as graphs may run at the
+    same time."""
     rows = min(256, N * (H // c.heads))  # its size grows with these
-    handle = torch._C._cuda_getCurrentRawStream(c.index) if stream is None else stream.cuda_stream
+    handle = (torch._C._cuda_getCurrentRawStream(c.index) if stream is None else stream.cuda_stream,
+              threading.get_ident())
     kept = c.workspaces.get(handle)
     if kept is not None and kept[0] >= rows and not torch._C._cuda_isCurrentStreamCapturing():
         return kept[1]

@@ -633,8 +633,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // A warpgroup sets its registers together; the roles that follow are compiled for that number.
     if (warp >= kSoftmaxWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        // Up to here the block may run beside the end of the kernel before; what that wrote is read behind.
-        asm volatile("griddepcontrol.wait;" ::: "memory");
         if (warp & 2) {
             // Slot order: K of tile 0, then K of tile t + 1 and V of tile t, as the products use them.
             const bool is_v = warp >= 14;
@@ -959,9 +957,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             merge_turn ^= 1;
             tmem_fence_after();
         };
-        // First one tile of nothing, while the kernel before ends and the first keys are on their way: it
-        // fetches the code (a first tile took 5500 cycles, the others 2000), and ends before the first
-        // product writes S.
+        // First one tile of nothing, while the first keys are on their way: it fetches the code (a first
+        // tile took 5500 cycles, the others 2000), and ends before the first product writes S.
         bool dry = true;
         for (uint32_t k = 0;;) {
             Item item{};
@@ -1118,7 +1115,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
             if (dry) {
                 dry = false;
-                asm volatile("griddepcontrol.wait;" ::: "memory");
                 continue;
             }
             if (turns > 0) {
@@ -1231,7 +1227,6 @@ template <int DT, int DP, int W>
 __global__ void __launch_bounds__(256) join_kernel(CacheView c, AttentionParams p)
 {
     __shared__ float4 sums[8][32];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Partial x = p.partial[blockIdx.x];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp % W;
@@ -1436,7 +1431,7 @@ cudaError_t launch_attention(const CUtensorMap &kmap, const CUtensorMap &vmap, c
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 0;  // what other calls launched before, some as dependents of one another, has all ended
     cfg.stream = st;
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kAttnThreads);
@@ -1444,6 +1439,7 @@ cudaError_t launch_attention(const CUtensorMap &kmap, const CUtensorMap &vmap, c
     const cudaError_t e = cudaLaunchKernelEx(&cfg, attention_kernel<DT, DP>, kmap, vmap, qmap, c, p);
     if (e)
         return e;
+    cfg.numAttrs = 1;  // the join starts as the blocks end, and waits for the last of them itself
     const int warps = p.max_rows <= 64 ? 4 : 1;  // per row
     cfg.gridDim = dim3(grid, (p.max_rows * warps + 7) / 8);
     cfg.blockDim = dim3(256);

@@ -14,15 +14,6 @@ namespace {
 constexpr int kBookThreads = 1024;  // the one block of reserve
 constexpr int kCopyThreads = 256;
 
-// Every kernel here is launched as a programmatic dependent of the one before it in its stream, and lets
-// the next one's blocks take their places as soon as all of its own have: each waits here, before it
-// reads or writes anything, until the kernel before has ended.
-__device__ __forceinline__ void begin_kernel()
-{
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 // Whether cu[0 .. B] starts at 0, does not decrease and ends within N rows; the whole block.
 __device__ __forceinline__ bool block_layout_ok(const int32_t *cu, int B, int64_t N)
 {
@@ -78,7 +69,6 @@ __device__ __forceinline__ bool last_block(int32_t *ticket, int blocks)
 
 __global__ void __launch_bounds__(kCopyThreads) init_kernel(CacheView c)
 {
-    begin_kernel();
     const int64_t n = (int64_t)gridDim.x * blockDim.x;
     const int64_t t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     for (int64_t i = t; i < c.num_pages; i += n) {
@@ -139,7 +129,7 @@ __device__ __forceinline__ Ask reserve_ask(const CacheView &c, const int32_t *cu
 // each, which finds its request by bisection.
 __global__ void __launch_bounds__(kBookThreads) reserve_kernel(CacheView c, const int32_t *cu, int B)
 {
-    begin_kernel();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the copies wait for the whole of this
     __shared__ int32_t held_of[kBookThreads], copies_of[kBookThreads], shared_of[kBookThreads];
     __shared__ int64_t base_of[kBookThreads + 1];
     __shared__ int first_short, ncopy;
@@ -245,7 +235,7 @@ __global__ void __launch_bounds__(kBookThreads) reserve_kernel(CacheView c, cons
 // The same for more requests than the block has threads, in turns, with its lists in the scratch.
 __global__ void __launch_bounds__(kBookThreads) reserve_many_kernel(CacheView c, const int32_t *cu, int B)
 {
-    begin_kernel();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     if (tid == 0)
@@ -361,7 +351,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_rows_kernel(CacheView c)
     constexpr int U = 4;
     const int vecs = c.dim / 8;
     const int parts = (c.page_size * c.heads * vecs + U * kCopyThreads - 1) / (U * kCopyThreads);
-    begin_kernel();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t units = (int64_t)*c.ncopy * c.num_layers * 2 * parts;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
         const int64_t unit = u / parts;
@@ -399,7 +389,6 @@ struct NewRows {
 __global__ void __launch_bounds__(kCopyThreads) append_kernel(CacheView c, NewRows in, int64_t layer_offset,
                                                               const int32_t *cu, int B, int64_t N)
 {
-    begin_kernel();
     const int lane = threadIdx.x & 31;
     const bool ok = block_layout_ok(cu, B, N);
     if (!ok) {
@@ -476,7 +465,6 @@ __device__ __forceinline__ int64_t commit_length(const CacheView &c, const int32
 __global__ void __launch_bounds__(kCopyThreads) commit_chain_kernel(CacheView c, const int32_t *cu, int B, int64_t N,
                                                                     const int32_t *accepted, int32_t *out_lens)
 {
-    begin_kernel();
     if (!block_layout_ok(cu, B, N)) {
         if (blockIdx.x == 0 && threadIdx.x == 0)
             cache_error(c.error, SPEC_DEVERR_LAYOUT, -1);
@@ -498,7 +486,6 @@ __global__ void __launch_bounds__(kCopyThreads) commit_tree_kernel(CacheView c, 
                                                                    const int32_t *accepted, const int32_t *parent,
                                                                    const int32_t *last_node, int32_t *out_lens)
 {
-    begin_kernel();
     __shared__ int32_t par[kMaxTree], path[kMaxTree];
     __shared__ int64_t from[kMaxTree], to[kMaxTree];
     __shared__ int bad, moves;
@@ -590,7 +577,6 @@ __global__ void __launch_bounds__(kCopyThreads) commit_tree_kernel(CacheView c, 
 // A block per fork.
 __global__ void __launch_bounds__(kCopyThreads) fork_kernel(CacheView c, const int32_t *src, const int32_t *dst, int F)
 {
-    begin_kernel();
     const int f = blockIdx.x, tid = threadIdx.x;
     const int s = src[f], d = dst[f];
     bool bad = s < 0 || s >= c.num_requests || d < 0 || d >= c.num_requests || s == d;
@@ -637,7 +623,6 @@ constexpr int kReleaseThreads = 512;
 // which the last block reads in ascending order: the list does not depend on the order of atomics.
 __global__ void __launch_bounds__(kReleaseThreads) release_kernel(CacheView c, const int32_t *keep, int B)
 {
-    begin_kernel();
     const int tid = threadIdx.x;
     for (int r = blockIdx.x; r < B; r += gridDim.x) {
         const int len = c.lens[r], held = c.held[r];
@@ -725,8 +710,11 @@ cudaError_t current_sms(int *sms)
     return cudaSuccess;
 }
 
+// `follows`: as a programmatic dependent of the call's kernel before it, which it waits for itself.  The
+// first kernel of a call is launched plainly: what other calls launched before it, some as dependents of
+// one another, has all ended then.
 template <class... Params, class... Args>
-spec_status launch(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t st, Args... args)
+spec_status launch(bool follows, void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t st, Args... args)
 {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
@@ -736,7 +724,7 @@ spec_status launch(void (*kernel)(Params...), dim3 grid, int threads, cudaStream
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = follows ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
@@ -769,7 +757,7 @@ spec_status spec_cache_init(const spec_cache *cache, void *stream)
         cudaSuccess)
         return SPEC_ERR_CUDA;
     const int64_t most = std::max<int64_t>(c.num_pages, (int64_t)c.num_requests * c.max_pages);
-    return launch(init_kernel, dim3((unsigned)std::min<int64_t>((most + kCopyThreads - 1) / kCopyThreads, 1024)),
+    return launch(false, init_kernel, dim3((unsigned)std::min<int64_t>((most + kCopyThreads - 1) / kCopyThreads, 1024)),
                   kCopyThreads, st, c);
 }
 
@@ -809,10 +797,10 @@ spec_status spec_cache_reserve(const spec_cache *cache, const int32_t *cu_new, i
     if (B == 0)
         return SPEC_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    s = launch(B <= kBookThreads ? reserve_kernel : reserve_many_kernel, dim3(1), kBookThreads, st, c, cu_new, B);
+    s = launch(false, B <= kBookThreads ? reserve_kernel : reserve_many_kernel, dim3(1), kBookThreads, st, c, cu_new, B);
     if (s != SPEC_OK)
         return s;
-    return launch(copy_rows_kernel, dim3(sms * 8), kCopyThreads, st, c);
+    return launch(true, copy_rows_kernel, dim3(sms * 8), kCopyThreads, st, c);
 }
 
 spec_status spec_cache_append(const spec_cache *cache, int32_t layer, const void *k_new, int64_t k_token_stride,
@@ -839,7 +827,7 @@ spec_status spec_cache_append(const spec_cache *cache, int32_t layer, const void
                      N > 1 ? k_token_stride : 0, c.heads > 1 ? k_head_stride : 0,
                      N > 1 ? v_token_stride : 0, c.heads > 1 ? v_head_stride : 0};
     const int64_t blocks = (N + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
-    return launch(append_kernel, dim3((unsigned)blocks), kCopyThreads, static_cast<cudaStream_t>(stream), c, in,
+    return launch(false, append_kernel, dim3((unsigned)blocks), kCopyThreads, static_cast<cudaStream_t>(stream), c, in,
                   layer * c.layer_stride, cu_new, B, N);
 }
 
@@ -865,14 +853,14 @@ spec_status spec_cache_commit(const spec_cache *cache, const int32_t *cu_new, in
     int32_t *out = out_lens ? out_lens : c.lens;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (!parent) {
-        return launch(commit_chain_kernel, dim3((B + kCopyThreads - 1) / kCopyThreads), kCopyThreads, st, c, cu_new, B,
+        return launch(false, commit_chain_kernel, dim3((B + kCopyThreads - 1) / kCopyThreads), kCopyThreads, st, c, cu_new, B,
                       N, num_accepted, out);
     }
     // Blocks for every column once, as far as the device holds them (8 blocks per SM).
     const int64_t columns = (int64_t)c.num_layers * 2 * c.heads * (c.dim / 8);
     const int64_t split = std::max<int64_t>(
         1, std::min<int64_t>((columns + kCopyThreads - 1) / kCopyThreads, (int64_t)sms * 8 / B));
-    return launch(commit_tree_kernel, dim3((unsigned)B, (unsigned)split), kCopyThreads, st, c, cu_new, B, N,
+    return launch(false, commit_tree_kernel, dim3((unsigned)B, (unsigned)split), kCopyThreads, st, c, cu_new, B, N,
                   num_accepted, parent, last_node, out);
 }
 
@@ -889,7 +877,7 @@ spec_status spec_cache_fork(const spec_cache *cache, const int32_t *src, const i
         return SPEC_ERR_CUDA;
     if (num_forks == 0)
         return SPEC_OK;
-    return launch(fork_kernel, dim3(num_forks), kCopyThreads, static_cast<cudaStream_t>(stream), c, src, dst, num_forks);
+    return launch(false, fork_kernel, dim3(num_forks), kCopyThreads, static_cast<cudaStream_t>(stream), c, src, dst, num_forks);
 }
 
 spec_status spec_cache_release(const spec_cache *cache, const int32_t *keep_lens, int32_t B, void *stream)
@@ -905,7 +893,7 @@ spec_status spec_cache_release(const spec_cache *cache, const int32_t *keep_lens
         return SPEC_ERR_CUDA;
     if (B == 0)
         return SPEC_OK;
-    return launch(release_kernel, dim3(std::min(B, sms * 2)), kReleaseThreads, static_cast<cudaStream_t>(stream), c,
+    return launch(false, release_kernel, dim3(std::min(B, sms * 2)), kReleaseThreads, static_cast<cudaStream_t>(stream), c,
                   keep_lens, B);
 }
 
