@@ -477,76 +477,50 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
 }
 
 // The shares of the list, and the request in which this block's begins (w->r and w->q, with the work
-// before it); a whole warp.  False when the block has no share, or cu is malformed.
+// before it); a whole warp, a request per lane.  False when the block has no share, or cu is malformed.
 __device__ __forceinline__ bool find_share(const CacheView &c, const AttentionParams &p, Shares *shares, Walk *w,
                                            int64_t *base, int lane)
 {
-    constexpr int U = 4;  // requests of a lane in a turn
-    int cost[U], size[U], len[U];
-    int64_t before = 0, at = 0;
-    bool bad = false, wrong = false;
     // Twice: the total makes the shares, then the block finds its own.  A batch of one turn keeps its
     // costs in between.
+    int64_t before = 0, at = 0, work = 0;
+    Request q{};
+    bool bad = false, wrong = false;
+#pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
         before = 0;
 #pragma unroll 1
-        for (int r0 = 0; r0 < p.B; r0 += 32 * U) {
-            const int r = r0 + lane * U;
-            if (pass == 0 || p.B > 32 * U) {
-                int32_t cu[U + 1];
-#pragma unroll
-                for (int i = 0; i <= U; ++i)
-                    cu[i] = p.cu[min(r + i, p.B)];
-#pragma unroll
-                for (int i = 0; i < U; ++i)
-                    len[i] = c.lens[min(r + i, p.B - 1)];
-                bad |= (r == 0 && cu[0] != 0) || cu[0] < 0;
-                int64_t sum = 0;
-#pragma unroll
-                for (int i = 0; i < U; ++i) {
-                    bad |= cu[i] > cu[i + 1] || cu[i + 1] > p.N;
-                    cost[i] = 0;
-                    size[i] = cu[i + 1] - cu[i];
-                    if (r + i < p.B && !bad) {
-                        cost[i] = request_of(c, p, r + i, size[i], len[i], false).cost;
-                        wrong |= cost[i] == 0 && size[i] > 0;
-                    }
-                    sum += (int64_t)cost[i] * c.heads;
+        for (int r0 = 0; r0 < p.B; r0 += 32) {
+            const int r = r0 + lane;
+            if (pass == 0 || p.B > 32) {
+                const int32_t here = p.cu[min(r, p.B)], next = p.cu[min(r + 1, p.B)], len = c.lens[min(r, p.B - 1)];
+                bad |= here > next || next > p.N || here < 0 || (r == 0 && here != 0);
+                q.cost = 0;
+                if (r < p.B && !bad) {
+                    q = request_of(c, p, r, next - here, len, false);
+                    wrong |= q.cost == 0 && q.n > 0;
                 }
-                int64_t incl = sum;
+                work = (int64_t)q.cost * c.heads;
+                int64_t incl = work;
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {
                     const int64_t y = __shfl_up_sync(kFull, incl, d);
                     incl += lane >= d ? y : 0;
                 }
-                at = before + incl - sum;
+                at = before + incl - work;
                 before += __shfl_sync(kFull, incl, 31);
             }
             if (pass == 1) {
                 const int64_t want = shares->begin(blockIdx.x);
-                int found = -1, its_size = 0, its_len = 0, its_cost = 0;
-                int64_t place = at, found_at = 0;
-#pragma unroll
-                for (int i = 0; i < U; ++i) {
-                    const int64_t work = (int64_t)cost[i] * c.heads;
-                    if (place <= want && want < place + work) {
-                        found = r + i;
-                        its_size = size[i];
-                        its_len = len[i];
-                        its_cost = cost[i];
-                        found_at = place;
-                    }
-                    place += work;
-                }
-                const unsigned who = __ballot_sync(kFull, found >= 0);
+                const unsigned who = __ballot_sync(kFull, at <= want && want < at + work);
                 if (who) {
                     const int from = __ffs(who) - 1;
-                    w->r = __shfl_sync(kFull, found, from);
-                    w->q.n = __shfl_sync(kFull, its_size, from);
-                    w->q.len = __shfl_sync(kFull, its_len, from);
-                    w->q.cost = __shfl_sync(kFull, its_cost, from);
+                    w->r = r0 + from;
+                    w->q.n = __shfl_sync(kFull, q.n, from);
+                    w->q.len = __shfl_sync(kFull, q.len, from);
+                    w->q.cost = __shfl_sync(kFull, q.cost, from);
                     w->q.rows = w->q.n * p.group;
-                    *base = __shfl_sync(kFull, found_at, from);
+                    *base = __shfl_sync(kFull, at, from);
                     return true;
                 }
             }
