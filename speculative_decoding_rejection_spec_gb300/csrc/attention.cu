@@ -73,6 +73,8 @@ struct Shares {
     __device__ __forceinline__ int owner(int64_t t) const
     {
         const int64_t big = (each + 1) * more;
+        if (t < INT32_MAX)
+            return t < big ? (uint32_t)t / (uint32_t)(each + 1) : more + (uint32_t)(t - big) / (uint32_t)each;
         return (int)(t < big ? t / (each + 1) : more + (t - big) / each);
     }
 };
@@ -1210,6 +1212,23 @@ __global__ void __launch_bounds__(256) join_kernel(CacheView c, AttentionParams 
     const int parts = row < x.rows ? x.shares.owner(x.last_place) - (int)blockIdx.x + 1 : 0;
     // the first part is the tail of its block's share, the others lie at the head of theirs
     auto place = [&](int i) { return ((int64_t)(blockIdx.x + i) * 2 + (i == 0)) * p.max_rows + row; };
+    constexpr int E = DP / 32;  // elements per lane
+    auto load = [&](int i, float *v) {
+        const float *o = p.part_o + place(i) * DP + lane * E;
+        if (E == 4) {
+            const float4 y = *reinterpret_cast<const float4 *>(o);
+            v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
+        } else {
+            const float2 y = *reinterpret_cast<const float2 *>(o);
+            v[0] = y.x, v[1] = y.y;
+        }
+    };
+    // most row blocks are in two parts: these are on their way before the weights are known
+    float early[2][4] = {};
+    if (W == 1 && parts >= 2) {
+        load(0, early[0]);
+        load(1, early[1]);
+    }
     constexpr int kMost = (kMaxGrid + 31) / 32;
     float2 ml[kMost];
     float top = -INFINITY;
@@ -1227,26 +1246,25 @@ __global__ void __launch_bounds__(256) join_kernel(CacheView c, AttentionParams 
         l += ml[j].x * ml[j].y;
     }
     l = warp_sum(l);
-    constexpr int E = DP / 32;  // elements per lane
     float acc[4] = {};
+    auto add = [&](float f, const float *v) {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            acc[e] = f == 0.0f ? acc[e] : fmaf(f, v[e], acc[e]);
+    };
+    if (W == 1 && parts >= 2) {
+        add(__shfl_sync(kFull, ml[0].x, 0), early[0]);
+        add(__shfl_sync(kFull, ml[0].x, 1), early[1]);
+    }
 #pragma unroll
     for (int j = 0; j < kMost; ++j) {
         const int some = min(32, parts - j * 32);
 #pragma unroll 8
-        for (int i = mine; i < some; i += W) {
+        for (int i = W == 1 && j == 0 && parts >= 2 ? 2 : mine; i < some; i += W) {
             const float f = __shfl_sync(kFull, ml[j].x, i);
-            const float *o = p.part_o + place(j * 32 + i) * DP + lane * E;
-            float v[4] = {};
-            if (E == 4) {
-                const float4 y = *reinterpret_cast<const float4 *>(o);
-                v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
-            } else {
-                const float2 y = *reinterpret_cast<const float2 *>(o);
-                v[0] = y.x, v[1] = y.y;
-            }
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                acc[e] = f == 0.0f ? acc[e] : fmaf(f, v[e], acc[e]);
+            float v[4];
+            load(j * 32 + i, v);
+            add(f, v);
         }
     }
     if (W > 1) {
