@@ -58,8 +58,8 @@ extern "C" {
                                    request's alone, a page released more often than it is held */
 #define SPEC_DEVERR_CAPACITY 64 /* reserve: the free pages do not suffice */
 #define SPEC_DEVERR_LENGTH 128  /* a negative length, more tokens than max_pages pages (or, where
-                                   they are shared or released, the pages held) contain, an
-                                   accepted count outside [-1, n_r) */
+                                   they are shared, the pages held) contain, an accepted count
+                                   outside [-1, n_r) */
 #define SPEC_DEVERR_FORK 256    /* a fork's source or destination out of range, a destination that
                                    holds pages, is named twice or is also a source */
 
@@ -181,8 +181,8 @@ spec_status spec_cache_release(const spec_cache *cache, const int32_t *keep_lens
  *   scale         finite, > 0
  *   lse           device fp32 [N, num_q_heads], or NULL
  *   workspace     spec_attention_workspace_size() bytes; contents need no initialisation
- * page_size is a multiple of 8 and head_dim at most SPEC_ATTENTION_MAX_HEAD_DIM
- * (SPEC_ERR_UNSUPPORTED otherwise).  The keys and values of all lens[r] + n_r tokens are read,
+ * page_size is a multiple of 8, head_dim at most SPEC_ATTENTION_MAX_HEAD_DIM and N * num_q_heads
+ * below 2^30 (SPEC_ERR_UNSUPPORTED otherwise).  The keys and values of all lens[r] + n_r tokens are read,
  * rows behind them are not used whatever they hold.  A value row (or an accumulated product) that
  * is not finite reaches every row of its request, also those that do not see it.  A page id out of
  * range reads as zeros (SPEC_DEVERR_PAGE); the rows of other requests with errors are not written.

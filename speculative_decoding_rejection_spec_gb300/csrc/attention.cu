@@ -28,8 +28,14 @@
 //
 // The work of a call is the list of all (request, head, row block, key tile), cut into equal
 // contiguous shares, one per block, whatever the lengths; each row block counts as kBlockCost tiles
-// more.  A (request, head, row block) that is cut
-// leaves partial sums (O, M, l), which a second kernel joins.
+// more.  A (request, head, row block) that is cut leaves partial sums (O, M, l), which a second kernel
+// joins.
+//
+// What bounds it (GB300; measured rates 6779 GB/s, 1948.5 TFLOP/s): decoding and verifying long
+// contexts, HBM (64 requests of 1 to 8191 keys, 1.03 GB: 168 us, 6.1 TB/s, nothing read twice); short
+// ones, the start of a block (the search for its share, the tables, the first tile: 10 us) and the
+// join; prompt chunks, the thread that issues the products (3200 cycles per wide tile, whose products
+// take 2120: 1.28 PFLOP/s, the tensor pipe 55% active).
 #include <algorithm>
 
 #include <cuda.h>
@@ -41,16 +47,21 @@
 namespace specrej {
 namespace {
 
-constexpr int kTile = 128;          // keys per tile, and rows per softmax group
+// keys per tile, and rows per softmax group.  Tiles of 64 keys with two score buffers each, so that the
+// next scores run beside the exponentials, were slower everywhere (prompt chunks 0.516 ms against
+// 0.330): twice the steps of the issuing thread, and products of 64 columns are bound by shared memory.
+constexpr int kTile = 128;
 constexpr int kBlockRows = 256;     // query rows of a (request, head, row block)
 constexpr int kSoftmaxWarps = 8, kLoadWarps = 4, kMmaWarp = 13, kWalkWarp = 12, kQueryWarps = 3;
 constexpr int kAttnThreads = 512;
 constexpr int kSoftmaxRegs = 144, kOtherRegs = 112;  // 256 threads of each: the launch's 128 a thread in all
 constexpr int kItems = 4;           // row blocks announced ahead
 constexpr int kMaxGrid = 160;       // blocks a call may use (SMs of the device, 152 on GB300)
-constexpr int kBlockCost = 3;       // what beginning and ending a row block costs, in tiles
-constexpr int kMinShare = 2;        // least places of a block's share
-constexpr float kLazy = 8.0f;       // log2 of the growth that moves a row's maximum
+// What beginning and ending a row block costs, in tiles: without it blocks with many short contexts end
+// late (0 / 2 / 4 / 6: decoding 200 / 178 / 176 / 180 us, verifying 234 / 205 / 205 / 206).
+constexpr int kBlockCost = 3;
+constexpr int kMinShare = 2;        // least places of a block's share (2 / 4 / 8: one token 17 / 20 / 23 us)
+constexpr float kLazy = 8.0f;       // log2 of the growth that moves a row's maximum (4 is no faster)
 constexpr int kTmemColumns = 512;   // two groups: 128 of S (P over it), up to 128 of O
 
 // A block's share of the list: [begin(x), begin(x + 1)), in tiles of cost.
@@ -93,7 +104,8 @@ struct AttentionParams {
     int32_t heads, group, B;
     uint32_t group_mul, group_shift;  // m / group = m * group_mul >> group_shift for 0 <= m < 2^31
     int32_t box;       // tokens per copy of K or V
-    int32_t q_tokens;  // tokens of 128 query rows, when the group divides them (then Q's wide tiles come as one copy)
+    int32_t q_tokens;  // tokens of 128 query rows, when the group divides them: Q of wide row blocks then
+                       // comes as one copy per 64 elements; 0: row by row
     int64_t N;
     const int32_t *cu, *parent;
     float scale_log2;
@@ -364,8 +376,7 @@ struct Walk {
     int t0, t1;       // those in the share; t1 > t0 but for a share of no tile
     int64_t pos, end; // place of the row block's part in the list
 
-    // false when the share holds no tile
-    // r and q: the request in which the share begins, after `base` places
+    // r and q are the request in which the share begins, after `base` places; false when it holds no tile
     __device__ __forceinline__ bool start(const AttentionParams &p, const Shares &s, int64_t base)
     {
         pos = s.begin(blockIdx.x);
@@ -672,7 +683,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         const int page = __shfl_sync(kFull, now.page, from + piece);
                         const int token = __shfl_sync(kFull, now.token, from + piece);
                         if (elect_one())
-                            tma_box(dst + piece * p.box * 128 + chunk * Z::kChunk, map, chunk * 64, token, h, page, bar);
+                            tma_box(dst + piece * p.box * 128 + chunk * Z::kChunk, map, chunk * 64, token, h, page,
+                                    bar);
                     }
                     __syncwarp();
                 }
@@ -1197,7 +1209,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
 // Joins the partial sums of the row blocks that were cut: blocks (share, 8 / W rows), W warps per row,
 // each for every W-th part.  Row blocks of many rows are cut into few parts (one warp per row), those of
-// few rows into as many as there are SMs (four: 38 parts of 48 rows took 15 us with one, 6 with four);
+// few rows into as many as there are SMs (four: 38 parts of 48 rows took 15 us with one, 9 with four);
 // with four, the 19456 blocks that 256 rows need cost 14 us though most have nothing to do.
 template <int DT, int DP, int W>
 __global__ void __launch_bounds__(256) join_kernel(CacheView c, AttentionParams p)
@@ -1448,7 +1460,7 @@ spec_status check_attention(const spec_cache *cache, CacheView *c, int32_t num_q
     if (B < 0 || B > c->num_requests || N < 0 || num_q_heads < 1 || num_q_heads % c->heads)
         return SPEC_ERR_INVALID_ARG;
     if (c->dim > SPEC_ATTENTION_MAX_HEAD_DIM || c->page_size % 8 || num_q_heads / c->heads > 128 ||
-        N * num_q_heads > INT32_MAX)
+        N * num_q_heads > INT32_MAX / 2)
         return SPEC_ERR_UNSUPPORTED;
     return SPEC_OK;
 }
