@@ -73,8 +73,9 @@ extern "C" {
  * rows of head_dim elements, at the strides given (in elements, the same for k and v; element
  * (layer, page, token, head, i) at layer * layer_stride + page * page_stride + token *
  * token_stride + head * head_stride + i).  k and v are 16-byte aligned and the strides are
- * positive multiples of 8 elements (the stride of a dimension of size 1 is not looked at).  All
- * pointers are device memory of the caller's; the struct itself is read during the call only.
+ * positive multiples of 8 elements (the stride of a dimension of size 1 is not looked at); max_pages
+ * * page_size and page_size * num_kv_heads * head_dim / 8 are below 2^30 (SPEC_ERR_UNSUPPORTED
+ * otherwise).  All pointers are device memory of the caller's; the struct itself is read during the call only.
  */
 typedef struct spec_cache {
     void *k, *v;

@@ -74,8 +74,9 @@ inline spec_status view_cache(const spec_cache *c, CacheView *out)
         !ptr_aligned(c->ref_counts, 4) || !ptr_aligned(c->free_pages, 4) || !ptr_aligned(c->num_free, 4) ||
         !ptr_aligned(c->error, 4))
         return SPEC_ERR_INVALID_ARG;
-    // positions are 32-bit
-    if ((int64_t)c->max_pages * c->page_size > INT32_MAX / 2)
+    // positions are 32-bit, and so is the number of a 16-byte vector in a page of one layer
+    if ((int64_t)c->max_pages * c->page_size > INT32_MAX / 2 ||
+        (int64_t)c->num_kv_heads * (c->head_dim / 8) > INT32_MAX / 2 / c->page_size)
         return SPEC_ERR_UNSUPPORTED;
     CacheView v{};
     v.k = static_cast<char *>(c->k);

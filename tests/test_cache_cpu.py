@@ -190,3 +190,12 @@ def test_oracle_attention_sees_ancestors_only():
     keep = [0, 1, 2, 4]  # node 2's view alone
     s = np.exp(q[2, 1] @ k[keep].T * 0.3)
     assert np.allclose(out[2, 1], s @ v[keep] / s.sum()) and np.isclose(lse[2, 1], np.log(s.sum()))
+
+
+def test_pages_past_32_bits_are_refused(lib):
+    """The vectors of a page (of one layer, keys or values) are numbered in 32 bits: 2^30 are refused."""
+    wide = dict(max_pages=1, page_size=2 ** 23, num_kv_heads=16, head_dim=64)
+    s = struct(**wide, token_stride=1024, head_stride=64, page_stride=2 ** 33, layer_stride=2 ** 40)
+    assert lib.spec_cache_reserve(ctypes.byref(s), ctypes.c_void_p(FAKE), 1, None) == 2
+    s.page_size = 2 ** 23 - 8
+    assert lib.spec_attention_workspace_size(ctypes.byref(s), 16, 1, 4) > 0
