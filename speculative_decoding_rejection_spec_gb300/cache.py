@@ -314,6 +314,8 @@ def attention(c: PagedCache, layer: int, q, cu_new, parent=None, scale=None, out
         _int32(parent, (N,), "parent", c.device)
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if stream is not None:
+            out.record_stream(stream)
         ot, oh = H * c.dim, c.dim
     elif out.shape != q.shape:
         raise ValueError("out must have the shape of q")
