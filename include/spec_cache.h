@@ -183,10 +183,10 @@ spec_status spec_cache_release(const spec_cache *cache, const int32_t *keep_lens
  *   lse           device fp32 [N, num_q_heads], or NULL
  *   workspace     spec_attention_workspace_size() bytes; contents need no initialisation
  * page_size is a multiple of 8, head_dim at most SPEC_ATTENTION_MAX_HEAD_DIM and N * num_q_heads
- * below 2^30 (SPEC_ERR_UNSUPPORTED otherwise).  The keys and values of all lens[r] + n_r tokens are read,
- * rows behind them are not used whatever they hold.  A value row (or an accumulated product) that
- * is not finite reaches every row of its request, also those that do not see it.  A page id out of
- * range reads as zeros (SPEC_DEVERR_PAGE); the rows of other requests with errors are not written.
+ * below 2^30 (SPEC_ERR_UNSUPPORTED otherwise).  The keys and values of all lens[r] + n_r tokens are
+ * read, rows behind them are not used whatever they hold.  A key or value that is not finite reaches
+ * the rows that see it and no others.  A page id out of range reads as zeros (SPEC_DEVERR_PAGE); the
+ * rows of other requests with errors are not written.
  */
 size_t spec_attention_workspace_size(const spec_cache *cache, int32_t num_q_heads, int32_t B, int64_t N);
 spec_status spec_attention(const spec_cache *cache, int32_t layer, const void *q, int64_t q_token_stride,

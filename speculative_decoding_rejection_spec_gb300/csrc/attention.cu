@@ -97,7 +97,7 @@ struct Partial {  // of the row block that starts in a block's share and goes on
 };
 
 struct AttentionParams {
-    const char *q;
+    const char *q, *v;  // v: the layer's values
     char *out;
     float *lse;
     int64_t q_token, q_head, out_token, out_head;  // elements
@@ -288,8 +288,10 @@ template <int SLOTS> struct alignas(16) AttnShared {
     uint64_t q_full[2], q_empty[2];      // a slot's Q is there / has been used
     uint64_t item_full[kItems], item_empty[kItems];
     uint64_t ready, merge, done;
+    uint64_t known[2];  // group 0 of a wide row block has looked at its last values (by turns)
     uint32_t tmem;
     volatile int32_t gave_up;
+    volatile int32_t spoilt[2];  // the number of a row block among those with unseen keys, by its last bit
 };
 
 // Waits for a barrier's phase, a bounded number of polls.  When one wait gives up, all do: no row block
@@ -458,6 +460,56 @@ __device__ __forceinline__ uint32_t tree_columns(const uint32_t *bits, int len, 
     return low_bits(-o) | (o > -32 ? bits[0] << -o : 0u);
 }
 
+// Two 16-bit values: bits 15 and 31 are set where they are not finite (the exponent is all ones, and one
+// more carries out of it).
+template <int DT> __device__ __forceinline__ uint32_t not_finite(uint32_t x)
+{
+    constexpr uint32_t e = DT == SPEC_BF16 ? 0x7f807f80 : 0x7c007c00;
+    return (x & e) + (DT == SPEC_BF16 ? 0x00800080 : 0x04000400);
+}
+
+// Rows of V in shared memory, a thread's 16-byte units from i0 to i1 (every kTile-th): values that are not
+// finite become zeros.  (Called, not inlined: prompt chunks 319 -> 324 us.)
+template <int DT, int DP> __device__ __forceinline__ void drop_not_finite(char *base, int i0, int i1)
+{
+    for (int j = 0; j < DP / 64; ++j)
+        for (int i = i0; i < i1; i += kTile) {
+            uint32_t *at = reinterpret_cast<uint32_t *>(base + j * AttnSizes<DP>::kChunk + i * 16);
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t x = at[e], bad = not_finite<DT>(x);
+                at[e] = (bad & 0x8000u ? 0 : x & 0xffffu) | (bad & 0x80000000u ? 0 : x & 0xffff0000u);
+            }
+        }
+}
+
+// The values that are not finite among the keys [from, to) that a row sees, added to its result (a row
+// of 16-bit outputs, or of fp32 partial sums).
+template <int DT>
+__device__ __noinline__ void add_spoilt(const CacheView &c, const AttentionParams &p, int r, int h, int from, int to,
+                                        int len, int token, uint4 tree, char *result, bool fp32)
+{
+    using T = typename std::conditional<DT == SPEC_BF16, __nv_bfloat16, __half>::type;
+    const uint32_t bits[4] = {tree.x, tree.y, tree.z, tree.w};
+    for (int key = from; key < to; ++key) {
+        const int o = key - len;
+        const bool seen = p.parent ? o < 0 || (o < kMaxTree && bits[o >> 5 & 3] >> (o & 31) & 1) : o <= token;
+        const int place = key / c.page_size, page = seen ? c.table[r * c.table_stride + place] : -1;
+        if (page < 0 || page >= c.num_pages)
+            continue;
+        const T *v = reinterpret_cast<const T *>(p.v) + page * c.page_stride +
+                     (int64_t)(key - place * c.page_size) * c.token_stride + h * c.head_stride;
+        for (int e = 0; e < c.dim; ++e) {
+            const float x = (float)v[e];
+            if (fabsf(x) < INFINITY)
+                continue;
+            if (fp32)
+                reinterpret_cast<float *>(result)[e] += x;
+            else
+                reinterpret_cast<T *>(result)[e] = (T)((float)reinterpret_cast<T *>(result)[e] + x);
+        }
+    }
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float d;
@@ -592,7 +644,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         mbar_init(&S.ready, kSoftmaxWarps);
         mbar_init(&S.merge, kSoftmaxWarps);
         mbar_init(&S.done, 1);
+        mbar_init(&S.known[0], 4);
+        mbar_init(&S.known[1], 4);
         S.gave_up = 0;
+        S.spoilt[0] = S.spoilt[1] = 0;
         mbar_fence_init();
     }
     if (warp == kMmaWarp) {
@@ -935,6 +990,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const uint32_t lanes = (uint32_t)sub * 32 << 16;
         const uint32_t s_addr = tmem + g * 256 + lanes;
         uint32_t s_turn = 0, o_turn = 0, merge_turn = 0;
+        uint32_t wide_cuts = 0;
+        int cuts = 0;  // row blocks so far with keys that some of their rows do not see
         // all eight softmax warps
         auto meet = [&]() {
             tmem_fence_before();
@@ -996,6 +1053,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             // keys that every row of this warp sees
             const int all_see = p.parent ? item.len
                                          : item.len + by_group(p, item.b * kBlockRows + m0 + sub * 32) + 1;
+            // ... and of the whole row block
+            const int common = p.parent ? item.len + 1 : item.len + by_group(p, item.b * kBlockRows) + 1;
+            const int last = min(item.keys, (item.t0 + nt) * kTile);
+            const bool cut_block = last > common && !dry;
+            cuts += cut_block;
             float M = -INFINITY, l = 0;
             bool any = false;  // the accumulator holds something
             for (int t = wide ? 0 : g; t < nt; t += wide ? 1 : 2) {
@@ -1084,14 +1146,29 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     tmem_wait_st();
                     tmem_fence_before();
                 }
-                // Rows of V behind the last key: whatever the page (or the slot before) holds there, a
-                // weight of zero must meet a finite value.
-                const int behind = item.keys - column;
-                if (behind < kTile && (!wide || g == 0)) {
-                    const uint32_t use = item.slots + 2 * nt - 1;  // the share's last slot
+                // A weight of zero must meet a finite value: rows of V behind the last key become zeros,
+                // whatever the page (or the slot before) holds there, and so do values that are not
+                // finite at keys that only some of the rows see (add_spoilt() gives them to those).
+                const int behind = item.keys - column, unseen = min(common - column, behind);
+                if (unseen < kTile && (!wide || g == 0) && !dry) {
+                    const uint32_t use = item.slots + min(2 * t + 2, 2 * nt - 1);  // the slot of V
                     wait(&S.full[use % SLOTS], use / SLOTS & 1);
                     char *base = ring + use % SLOTS * Z::kSlotBytes;
-                    for (int i = behind * 8 + row; i < kTile * 8; i += kTile)
+                    const int i0 = max(unseen, 0) * 8 + row, i1 = min(behind, kTile) * 8;
+                    uint32_t bad = 0;
+#pragma unroll 4
+                    for (int i = i0; i < i1; i += kTile)
+#pragma unroll
+                        for (int j = 0; j < DP / 64; ++j) {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(base + j * Z::kChunk + i * 16);
+                            bad |= not_finite<DT>(x.x) | not_finite<DT>(x.y) | not_finite<DT>(x.z) |
+                                   not_finite<DT>(x.w);
+                        }
+                    if (bad & 0x80008000u) {
+                        drop_not_finite<DT, DP>(base, i0, i1);
+                        S.spoilt[cuts & 1] = cuts;
+                    }
+                    for (int i = i1 + row; i < kTile * 8; i += kTile)
 #pragma unroll
                         for (int j = 0; j < DP / 64; ++j)
                             *reinterpret_cast<uint4 *>(base + j * Z::kChunk + i * 16) = make_uint4(0, 0, 0, 0);
@@ -1141,7 +1218,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 else if (p.lse)
                     p.lse[(int64_t)(item.first + token) * p.heads + head] = (M + log2f(l)) * 0.69314718055994531f;
             };
+            // (The groups are less than two row blocks apart, by their meetings or, of wide ones, by the order
+            // of the products: nobody writes spoilt[] for the next but one before all have read it here.)
+            auto spoilt = [&]() {
+                if (cut_block && on && S.spoilt[cuts & 1] == cuts)
+                    add_spoilt<DT>(c, p, item.r, item.h, max(common, item.t0 * kTile), last, item.len, token,
+                                   make_uint4(bits[0], bits[1], bits[2], bits[3]),
+                                   whole ? out : reinterpret_cast<char *>(p.part_o + place * DP), !whole);
+            };
             if (wide) {
+                if (cut_block) {
+                    if (g == 1)
+                        wait(&S.known[wide_cuts & 1], wide_cuts >> 1 & 1);
+                    else if (lane == 0)
+                        mbar_arrive(&S.known[wide_cuts & 1]);
+                    ++wide_cuts;
+                }
                 if (warp_on) {
 #pragma unroll 1
                     for (int j = 0; j < DP / 32; ++j) {
@@ -1152,6 +1244,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     }
                     store_ml();
                 }
+                spoilt();
             } else {
                 S.group[g].ml[row] = make_float2(M, l);
                 meet();
@@ -1186,6 +1279,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         store_ml();
                 }
                 meet();
+                if (g == 0)  // (both halves are written; the other group may have had no tile, and no bits)
+                    spoilt();
             }
         }
         tmem_fence_before();
@@ -1262,7 +1357,7 @@ __global__ void __launch_bounds__(256) join_kernel(CacheView c, AttentionParams 
     auto add = [&](float f, const float *v) {
 #pragma unroll
         for (int e = 0; e < E; ++e)
-            acc[e] = f == 0.0f ? acc[e] : fmaf(f, v[e], acc[e]);
+            acc[e] = fmaf(f, v[e], acc[e]);
     };
     if (W == 1 && parts >= 2) {
         add(__shfl_sync(kFull, ml[0].x, 0), early[0]);
@@ -1505,6 +1600,7 @@ spec_status spec_attention(const spec_cache *cache, int32_t layer, const void *q
         return SPEC_OK;
     AttentionParams p{};
     p.q = static_cast<const char *>(q);
+    p.v = c.v + 2 * layer * c.layer_stride;
     p.out = static_cast<char *>(out);
     p.lse = lse;
     p.q_token = N > 1 ? q_token_stride : 0;

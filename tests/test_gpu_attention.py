@@ -479,3 +479,57 @@ def test_serving_loop(tree):
         assert cache.last_error(c) == (0, 0, -1)
         assert c.lens.cpu().tolist()[:B] == [len(x[0]) for x in history]
         assert c.held.cpu().tolist()[:B] == [-(-len(x[0]) // P) for x in history]
+
+
+@pytest.mark.parametrize("dtype,group,dim,tree,n,ctx", [
+    ("bf16", 4, 128, False, [9, 5, 1, 2], [300, 125, 64, 0]), ("f16", 4, 64, True, [60, 128, 20, 2], [100, 0, 127, 1]),
+    ("bf16", 4, 128, False, [700, 3, 64], [0, 20000, 1000]), ("bf16", 1, 128, True, [33], [9000]),
+    ("f16", 3, 80, False, [130, 400], [77, 5]), ("f16", 7, 40, True, [64, 128], [4000, 3])])
+def test_values_that_are_not_finite_reach_only_the_rows_that_see_them(dtype, group, dim, tree, n, ctx):
+    """A draft's value of inf or NaN leaves the rows that do not see it as they are with a zero there, bit for
+    bit; the others become its sum with theirs.  A key of NaN makes the rows that see it NaN, and no others."""
+    import torch
+    c = Case(n, ctx, group=group, dim=dim, dtype=dtype, tree=tree, seed=dim + group)
+    rng = np.random.default_rng(len(n) + dim)
+    spoilt = []  # request, new token, kv head, element, value
+    for r, m in enumerate(n):
+        for x in (np.inf, -np.inf, np.nan, np.inf, np.inf):
+            spoilt.append((r, int(rng.integers(min(1, m - 1), m)), int(rng.integers(2)), int(rng.integers(dim)), x))
+
+    def place(r, j):
+        t = ctx[r] + j
+        return int(c.table[r, t // c.page]), t % c.page
+
+    def write(which, values):
+        for r, j, h, e, x in values:
+            page, row = place(r, j)
+            c.kv[which][page, row, h, e] = x
+        (c.c.k, c.c.v)[which][0].copy_(c.kv[which])
+
+    write(1, [s[:4] + (0.0,) for s in spoilt])
+    clean, clean_lse = c.run()
+    c.check(clean, clean_lse)
+    for s in spoilt:  # (one element may be named twice)
+        write(1, [s])
+    out, lse = c.run()
+    want = clean.float().cpu().numpy()
+    seen = [oracle_cache.visible(m, ctx[r], c.parents[r] if tree else None) for r, m in enumerate(n)]
+    last = {s[:4]: s[4] for s in spoilt}
+    for (r, j, h, e), x in last.items():
+        rows = c.cu[r] + np.flatnonzero(seen[r][:, ctx[r] + j])
+        with np.errstate(invalid="ignore"):
+            want[rows, h * group:(h + 1) * group, e] += np.float32(x)
+    np.testing.assert_array_equal(out.float().cpu().numpy(), want)
+    assert torch.equal(lse, clean_lse)
+
+    write(1, [s[:4] + (0.0,) for s in spoilt])
+    write(0, spoilt[2::5])
+    out, lse = c.run()
+    want, want_lse = clean.float().cpu().numpy(), clean_lse.cpu().numpy()
+    for r, j, h, _, _ in spoilt[2::5]:
+        rows = c.cu[r] + np.flatnonzero(seen[r][:, ctx[r] + j])
+        want[rows, h * group:(h + 1) * group] = np.nan
+        want_lse[rows, h * group:(h + 1) * group] = np.nan
+    np.testing.assert_array_equal(out.float().cpu().numpy(), want)
+    np.testing.assert_array_equal(lse.cpu().numpy(), want_lse)
+    assert cache.last_error(c.c) == (0, 0, -1)
