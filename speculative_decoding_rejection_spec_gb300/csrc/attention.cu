@@ -1302,26 +1302,25 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
 }
 
-// Joins the partial sums of the row blocks that were cut: blocks (share, 8 / W rows), W warps per row,
-// each for every W-th part.  Row blocks of many rows are cut into few parts (one warp per row), those of
-// few rows into as many as there are SMs (four: 38 parts of 48 rows took 15 us with one, 9 with four);
-// with four, the 19456 blocks that 256 rows need cost 14 us though most have nothing to do.
-template <int DT, int DP, int W>
-__global__ void __launch_bounds__(256) join_kernel(CacheView c, AttentionParams p)
+// Joins the partial sums of the row blocks that were cut: blocks (share, y), W warps per row, each for
+// every W-th part, J rows per warp at the same time.  Bound by the latency of L2, a chain of three loads
+// (the row block, the weights, the parts): two parts of every row are on their way before the weights
+// are known.
+template <int DT, int DP, int W, int J>
+__device__ __forceinline__ void join(const CacheView &c, const AttentionParams &p, const Partial &x, float4 (*sums)[32],
+                                     int row0, int lane, int warp)
 {
-    __shared__ float4 sums[8][32];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const Partial x = p.partial[blockIdx.x];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp % W;
-    const int row = blockIdx.y * (8 / W) + warp / W;
-    if (blockIdx.y * (8 / W) >= x.rows)
-        return;
-    const int parts = row < x.rows ? x.shares.owner(x.last_place) - (int)blockIdx.x + 1 : 0;
-    // the first part is the tail of its block's share, the others lie at the head of theirs
-    auto place = [&](int i) { return ((int64_t)(blockIdx.x + i) * 2 + (i == 0)) * p.max_rows + row; };
+    const int mine = warp % W, next = gridDim.y * (8 / W);  // from a row of the warp's to its next
+    const int parts = x.shares.owner(x.last_place) - (int)blockIdx.x + 1;
+    // the first part is the tail of its block's share, the others lie at the head of theirs; rows behind
+    // the last are the first over again
+    auto place = [&](int i, int j) {
+        const int row = row0 + j * next;
+        return ((int64_t)(blockIdx.x + i) * 2 + (i == 0)) * p.max_rows + (row < x.rows ? row : row0);
+    };
     constexpr int E = DP / 32;  // elements per lane
-    auto load = [&](int i, float *v) {
-        const float *o = p.part_o + place(i) * DP + lane * E;
+    auto load = [&](int i, int j, float *v) {
+        const float *o = p.part_o + place(i, j) * DP + lane * E;
         if (E == 4) {
             const float4 y = *reinterpret_cast<const float4 *>(o);
             v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
@@ -1330,77 +1329,110 @@ __global__ void __launch_bounds__(256) join_kernel(CacheView c, AttentionParams 
             v[0] = y.x, v[1] = y.y;
         }
     };
-    // most row blocks are in two parts: these are on their way before the weights are known
-    float early[2][4] = {};
-    if (W == 1 && parts >= 2) {
-        load(0, early[0]);
-        load(1, early[1]);
-    }
-    constexpr int kMost = (kMaxGrid + 31) / 32;
-    float2 ml[kMost];
-    float top = -INFINITY;
+    float top[J], l[J], acc[J][4];
 #pragma unroll
-    for (int j = 0; j < kMost; ++j) {
-        const int i = j * 32 + lane;
-        ml[j] = i < parts ? p.part_ml[place(i)] : make_float2(-INFINITY, 0);
-        top = fmaxf(top, ml[j].x);
+    for (int j = 0; j < J; ++j) {
+        top[j] = -INFINITY;
+        l[j] = 0;
+        acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0;
     }
-    top = warp_max(top);
-    float l = 0;
+    // 32 parts in a turn, nearly always all
+#pragma unroll 1
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+        const int some = min(32, parts - i0);
+        float2 ml[J];
+        // two parts on their way before the weights are known
+        const int a = mine, b = mine + W;
+        float va[J][4], vb[J][4];
 #pragma unroll
-    for (int j = 0; j < kMost; ++j) {
-        ml[j].x = ml[j].x == -INFINITY ? 0.0f : ex2(ml[j].x - top);
-        l += ml[j].x * ml[j].y;
-    }
-    l = warp_sum(l);
-    float acc[4] = {};
-    auto add = [&](float f, const float *v) {
+        for (int j = 0; j < J; ++j) {
+            ml[j] = lane < some ? p.part_ml[place(i0 + lane, j)] : make_float2(-INFINITY, 0);
+            load(i0 + min(a, some - 1), j, va[j]);
+            load(i0 + min(b, some - 1), j, vb[j]);
+        }
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            acc[e] = fmaf(f, v[e], acc[e]);
-    };
-    if (W == 1 && parts >= 2) {
-        add(__shfl_sync(kFull, ml[0].x, 0), early[0]);
-        add(__shfl_sync(kFull, ml[0].x, 1), early[1]);
-    }
+        for (int j = 0; j < J; ++j) {
+            const float now = fmaxf(top[j], warp_max(ml[j].x)), f = top[j] == -INFINITY ? 0.0f : ex2(top[j] - now);
+            top[j] = now;
+            ml[j].x = ml[j].x == -INFINITY ? 0.0f : ex2(ml[j].x - now);
+            l[j] = l[j] * f + warp_sum(ml[j].x * ml[j].y);
+            const float fa = __shfl_sync(kFull, ml[j].x, a), fb = __shfl_sync(kFull, ml[j].x, b);
 #pragma unroll
-    for (int j = 0; j < kMost; ++j) {
-        const int some = min(32, parts - j * 32);
-#pragma unroll 8
-        for (int i = W == 1 && j == 0 && parts >= 2 ? 2 : mine; i < some; i += W) {
-            const float f = __shfl_sync(kFull, ml[j].x, i);
-            float v[4];
-            load(j * 32 + i, v);
-            add(f, v);
+            for (int e = 0; e < E; ++e) {
+                if (i0 > 0)
+                    acc[j][e] *= f;
+                if (a < some)
+                    acc[j][e] = fmaf(fa, va[j][e], acc[j][e]);
+                if (b < some)
+                    acc[j][e] = fmaf(fb, vb[j][e], acc[j][e]);
+            }
+        }
+#pragma unroll(8 / J)
+        for (int i = mine + 2 * W; i < some; i += W) {
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                float v[4];
+                load(i0 + i, j, v);
+                const float f = __shfl_sync(kFull, ml[j].x, i);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    acc[j][e] = fmaf(f, v[e], acc[j][e]);
+            }
         }
     }
     if (W > 1) {
-        sums[warp][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-        __syncthreads();
+        sums[warp][lane] = make_float4(acc[0][0], acc[0][1], acc[0][2], acc[0][3]);
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / W), "n"(32 * W) : "memory");
         if (mine > 0)
             return;
 #pragma unroll
         for (int i = 1; i < W; ++i) {
             const float4 y = sums[warp + i][lane];
-            acc[0] += y.x, acc[1] += y.y, acc[2] += y.z, acc[3] += y.w;
+            acc[0][0] += y.x, acc[0][1] += y.y, acc[0][2] += y.z, acc[0][3] += y.w;
         }
     }
-    if (row >= x.rows)
-        return;
-    const int m = x.b * kBlockRows + row;
-    const int token = by_group(p, m), head = x.h * p.group + m - token * p.group;
-    const int64_t t = (int64_t)p.cu[x.r] + token;
-    const float by = 1.0f / l;
-    if (lane * E < c.dim) {
-        char *out = p.out + 2 * (t * p.out_token + head * p.out_head + lane * E);
-        const uint32_t low = from_float2<DT>(acc[0] * by, acc[1] * by);
-        if (E == 4)
-            *reinterpret_cast<uint2 *>(out) = make_uint2(low, from_float2<DT>(acc[2] * by, acc[3] * by));
-        else
-            *reinterpret_cast<uint32_t *>(out) = low;
+    const int first = p.cu[x.r];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const int row = row0 + j * next;
+        if (row >= x.rows)
+            return;
+        const int m = x.b * kBlockRows + row;
+        const int token = by_group(p, m), head = x.h * p.group + m - token * p.group;
+        const int64_t t = (int64_t)first + token;
+        const float by = 1.0f / l[j];
+        if (lane * E < c.dim) {
+            char *out = p.out + 2 * (t * p.out_token + head * p.out_head + lane * E);
+            const uint32_t low = from_float2<DT>(acc[j][0] * by, acc[j][1] * by);
+            if (E == 4)
+                *reinterpret_cast<uint2 *>(out) = make_uint2(low, from_float2<DT>(acc[j][2] * by, acc[j][3] * by));
+            else
+                *reinterpret_cast<uint32_t *>(out) = low;
+        }
+        if (lane == 0 && p.lse)
+            p.lse[t * p.heads + head] = (top[j] + log2f(l[j])) * 0.69314718055994531f;
     }
-    if (lane == 0 && p.lse)
-        p.lse[t * p.heads + head] = (top + log2f(l)) * 0.69314718055994531f;
+}
+
+// Row blocks of many rows are cut into few parts (a warp for up to kJoinRows rows; prompt chunks with 1, 2
+// and 4 rows per warp: 314, 312 and 316 us), those of few rows into as many as there are SMs (four warps per
+// row: 38 parts of 48 rows took 79 us in all with one, 62 with four).
+constexpr int kJoinRows = 2;
+
+template <int DT, int DP, int W>
+__global__ void __launch_bounds__(256) join_kernel(CacheView c, AttentionParams p)
+{
+    __shared__ float4 sums[W > 1 ? 8 : 1][32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row0 = blockIdx.y * (8 / W) + warp / W;
+    const Partial x = p.partial[blockIdx.x];
+    if (row0 >= x.rows)
+        return;
+    if (W > 1 || row0 + gridDim.y * 8 >= x.rows)
+        join<DT, DP, W, 1>(c, p, x, sums, row0, lane, warp);
+    else
+        join<DT, DP, W, kJoinRows>(c, p, x, sums, row0, lane, warp);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -1540,7 +1572,8 @@ cudaError_t launch_attention(const CUtensorMap &kmap, const CUtensorMap &vmap, c
         return e;
     cfg.numAttrs = 1;  // the join starts as the blocks end, and waits for the last of them itself
     const int warps = p.max_rows <= 64 ? 4 : 1;  // per row
-    cfg.gridDim = dim3(grid, (p.max_rows * warps + 7) / 8);
+    const int rows = warps == 4 ? 2 : 8 * kJoinRows;  // per block
+    cfg.gridDim = dim3(grid, (p.max_rows + rows - 1) / rows);
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     return warps == 4 ? cudaLaunchKernelEx(&cfg, join_kernel<DT, DP, 4>, c, p)

@@ -533,3 +533,11 @@ def test_values_that_are_not_finite_reach_only_the_rows_that_see_them(dtype, gro
     np.testing.assert_array_equal(out.float().cpu().numpy(), want)
     np.testing.assert_array_equal(lse.cpu().numpy(), want_lse)
     assert cache.last_error(c.c) == (0, 0, -1)
+
+
+@pytest.mark.parametrize("dtype,dim", [("bf16", 128), ("f16", 64), ("bf16", 40)])
+@pytest.mark.parametrize("n,group", [(70, 1), (9, 4), (33, 4), (1, 1), (250, 1)])
+def test_row_blocks_cut_into_more_parts_than_a_warp_has_lanes(dtype, dim, n, group):
+    """One row block over 120 tiles, behind another request's (its first part lies within a share)."""
+    c = Case([1, n], [300, 15000], heads=1, group=group, dim=dim, page=64, dtype=dtype, seed=n + dim, poison=False)
+    c.check(*c.run())
