@@ -379,3 +379,41 @@ def test_binding_refusals():
     with pytest.raises(ValueError):
         cache.PagedCache(c.k, c.v.transpose(2, 3).contiguous().transpose(2, 3), page_table=c.page_table, lens=c.lens,
                          held=c.held, ref_counts=c.ref_counts, free_pages=c.free_pages, num_free=c.num_free)
+
+
+def test_offsets_past_32_bits():
+    """The same steps in a cache of few pages and in the last pages of one of 5 GB of keys: bit for bit alike."""
+    import torch
+    heads, dim, page = 8, 128, 64
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    caches = [cache.make_cache(2, pages, page, heads, dim, 4, 16) for pages in (48, 20000)]
+    assert caches[1].k.numel() * 2 > 2 ** 32
+    ints = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+
+    def step(n, parent=None):
+        cu = torch.tensor(np.concatenate([[0], np.cumsum(n)]), dtype=torch.int32, device="cuda")
+        N = sum(n)
+        rows = [[torch.randn((N, h, dim), generator=gen, device="cuda").bfloat16() for h in (heads, heads, 2 * heads)]
+                for _ in range(2)]
+        outs = []
+        for c in caches:
+            cache.reserve(c, cu)
+            for layer, (k, v, q) in enumerate(rows):
+                cache.append(c, layer, k, v, cu)
+                outs.append(cache.attention(c, layer, q, cu, parent=parent))
+            assert cache.last_error(c) == (0, 0, -1)
+        assert outs[0].isfinite().all() and torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[3])
+        return cu
+
+    cu = step([300, 129, 65, 0])
+    for c in caches:
+        cache.commit(c, cu, ints(299, 128, 64, -1))
+        cache.fork(c, ints(0), ints(3))
+    parent = ints(*[-1, 0, 0, 1, 2, 4] * 4)
+    cu = step([6] * 4, parent)  # requests 0 and 3 share their last page
+    for c in caches:
+        cache.commit(c, cu, ints(2, 3, 1, 0), parent=parent, last_node=ints(3, 5, 2, 0))
+    step([1, 1, 1, 1])
+    a, b = caches
+    assert a.lens.tolist() == b.lens.tolist() == [303, 133, 67, 301]
+    assert (torch.where(a.page_table >= 0, a.page_table + 20000 - 48, -1) == b.page_table).all()
