@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(kBookThreads) reserve_kernel(CacheView c, cons
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the copies wait for the whole of this
     __shared__ int32_t held_of[kBookThreads], copies_of[kBookThreads], shared_of[kBookThreads];
+    __shared__ int32_t free_of[kBookThreads];  // the top of the stack, read before it is known what is asked for
     __shared__ int64_t base_of[kBookThreads + 1];
     __shared__ int first_short, ncopy;
     const int r = threadIdx.x;
@@ -153,7 +154,8 @@ __global__ void __launch_bounds__(kBookThreads) reserve_kernel(CacheView c, cons
         }
         return;
     }
-    int need = 0, shared = -1;
+    free_of[r] = have <= c.num_pages && r < have ? c.free_pages[have - 1 - r] : -1;
+    int need = 0, shared = -1, refs = 0;
     if (next > here) {
         const int n = next - here;
         if (len < 0 || held < 0 || held > c.max_pages || len > (int64_t)held * c.page_size ||
@@ -163,7 +165,7 @@ __global__ void __launch_bounds__(kBookThreads) reserve_kernel(CacheView c, cons
             need = pages_of((int64_t)len + n, c.page_size);
             if (len % c.page_size) {
                 const int page = c.table[r * c.table_stride + len / c.page_size];
-                const int refs = page >= 0 && page < c.num_pages ? c.ref[page] : 0;
+                refs = page >= 0 && page < c.num_pages ? c.ref[page] : 0;
                 if (refs < 1) {
                     cache_error(c.error, SPEC_DEVERR_PAGE, r);
                     need = 0;
@@ -180,7 +182,7 @@ __global__ void __launch_bounds__(kBookThreads) reserve_kernel(CacheView c, cons
 #pragma unroll 8
         for (int j = 0; j < r; ++j)
             before += shared_of[j] == shared;
-        copies = c.ref[shared] - before > 1;
+        copies = refs - before > 1;
     }
     const int fresh = (need > held ? need - held : 0) + copies;
     int64_t used;
@@ -207,7 +209,7 @@ __global__ void __launch_bounds__(kBookThreads) reserve_kernel(CacheView c, cons
             else
                 hi = mid;
         }
-        const int page = c.free_pages[have - 1 - k];
+        const int page = k < kBookThreads ? free_of[k] : c.free_pages[have - 1 - k];
         const int i = (int)(k - base_of[lo]) - copies_of[lo];  // -1: the copy of its last page
         if (page < 0 || page >= c.num_pages)
             cache_error(c.error, SPEC_DEVERR_PAGE, lo);
@@ -217,7 +219,7 @@ __global__ void __launch_bounds__(kBookThreads) reserve_kernel(CacheView c, cons
             c.table[lo * c.table_stride + held_of[lo] + i] = page;
     }
     if (copies) {
-        const int page = c.free_pages[have - 1 - at];
+        const int page = at < kBookThreads ? free_of[at] : c.free_pages[have - 1 - at];
         c.table[r * c.table_stride + len / c.page_size] = page;
         atomicSub(&c.ref[shared], 1);
         if (page >= 0 && page < c.num_pages)
@@ -580,18 +582,25 @@ __global__ void __launch_bounds__(kCopyThreads) fork_kernel(CacheView c, const i
     const int f = blockIdx.x, tid = threadIdx.x;
     const int s = src[f], d = dst[f];
     bool bad = s < 0 || s >= c.num_requests || d < 0 || d >= c.num_requests || s == d;
+    // (what the checks need is asked for at once: the kernel is a chain of loads)
+    int len = 0, held = 0, taken = 0, mine = -1;
+    if (!bad) {
+        len = c.lens[s];
+        held = c.held[s];
+        taken = c.held[d];
+        if (tid < c.max_pages)
+            mine = c.table[s * c.table_stride + tid];
+    }
     for (int g = tid; g < F; g += kCopyThreads)
         bad |= (g != f && dst[g] == d) || dst[g] == s || src[g] == d;
-    if (!bad)
-        bad = c.held[d] != 0;
+    bad |= taken != 0;
     if (__syncthreads_or(bad)) {
         if (tid == 0)
             cache_error(c.error, SPEC_DEVERR_FORK, d >= 0 && d < c.num_requests ? d : -1);
         return;
     }
-    const int64_t len = c.lens[s];
     const int count = len < 0 ? -1 : pages_of(len, c.page_size);
-    if (count < 0 || count > c.held[s] || count > c.max_pages) {
+    if (count < 0 || count > held || count > c.max_pages) {
         if (tid == 0)
             cache_error(c.error, SPEC_DEVERR_LENGTH, d);
         return;
@@ -599,20 +608,22 @@ __global__ void __launch_bounds__(kCopyThreads) fork_kernel(CacheView c, const i
     const int32_t *from = c.table + s * c.table_stride;
     int32_t *to = c.table + d * c.table_stride;
     bool lost = false;
-    for (int i = tid; i < count; i += kCopyThreads)
-        lost |= from[i] < 0 || from[i] >= c.num_pages || c.ref[from[i]] < 1;
+    for (int i = tid; i < count; i += kCopyThreads) {
+        const int page = i == tid ? mine : from[i];
+        lost |= page < 0 || page >= c.num_pages || c.ref[page] < 1;
+    }
     if (__syncthreads_or(lost)) {
         if (tid == 0)
             cache_error(c.error, SPEC_DEVERR_PAGE, d);
         return;
     }
     for (int i = tid; i < count; i += kCopyThreads) {
-        const int page = from[i];
+        const int page = i == tid ? mine : from[i];
         to[i] = page;
         atomicAdd(&c.ref[page], 1);
     }
     if (tid == 0) {
-        c.lens[d] = (int32_t)len;
+        c.lens[d] = len;
         c.held[d] = count;
     }
 }
