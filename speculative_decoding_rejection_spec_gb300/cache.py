@@ -303,9 +303,11 @@ def attention(c: PagedCache, layer: int, q, cu_new, parent=None, scale=None, out
     out, like q.
 
     ``parent`` (int32 [N]) makes the new tokens draft trees, otherwise they are chains; ``scale``
-    defaults to head_dim ** -0.5; ``lse`` (float32 [N, q_heads], given) receives the log of each
-    row's softmax sum; ``workspace`` (uint8) may be given, calls that can run at the same time need
-    one each (without one, the cache keeps one per stream, and a captured graph has its own).  Rows behind ``cu_new[B]`` are left as they were in ``out``.
+    defaults to head_dim ** -0.5; ``out`` may be given (one made for a call on another ``stream`` is
+    memory of that stream, kept for the current one); ``lse`` (float32 [N, q_heads], given) receives
+    the log of each row's softmax sum; ``workspace`` (uint8) may be given, calls that can run at the
+    same time need one each (without one, the cache keeps one per stream, and a captured graph has its
+    own).  Rows behind ``cu_new[B]`` are left as they were in ``out``.
     """
     B = _cu(c, cu_new)
     qt, qh = _rows(c, q, None, "q")
@@ -313,9 +315,14 @@ def attention(c: PagedCache, layer: int, q, cu_new, parent=None, scale=None, out
     if parent is not None:
         _int32(parent, (N,), "parent", c.device)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if stream is not None:
-            out.record_stream(stream)
+        if stream is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        else:
+            # memory of the stream that writes it: the current one's may have been freed with work queued
+            # there that still uses it.  Recorded for the current one, which will read it.
+            with torch.cuda.stream(stream):
+                out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            out.record_stream(torch.cuda.current_stream(c.device))
         ot, oh = H * c.dim, c.dim
     elif out.shape != q.shape:
         raise ValueError("out must have the shape of q")
