@@ -170,16 +170,21 @@ def _call(c, name, stream, *args):
 
 def make_cache(num_layers: int, num_pages: int, page_size: int, num_kv_heads: int, head_dim: int, num_requests: int,
                max_pages: int, dtype=None, device="cuda", stream=None) -> PagedCache:
-    """An empty cache: every page free.  Keys and values are zero."""
+    """An empty cache: every page free.  Keys and values are zero.  With ``stream`` it is made there and its
+    tensors are memory of that stream: calls on it may follow at once, other streams wait for it."""
     dev = torch.device(device)
     if dev.type == "cuda" and dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return make_cache(num_layers, num_pages, page_size, num_kv_heads, head_dim, num_requests, max_pages, dtype,
+                              dev)
     ints = lambda *shape: torch.empty(shape, dtype=torch.int32, device=dev)  # noqa: E731
     kv = torch.zeros((2, num_layers, num_pages, page_size, num_kv_heads, head_dim),
                      dtype=torch.bfloat16 if dtype is None else dtype, device=dev)
     c = PagedCache(kv[0], kv[1], page_table=ints(num_requests, max_pages), lens=ints(num_requests),
                    held=ints(num_requests), ref_counts=ints(num_pages), free_pages=ints(num_pages), num_free=ints(1))
-    _call(c, "spec_cache_init", stream)
+    _call(c, "spec_cache_init", None)
     return c
 
 

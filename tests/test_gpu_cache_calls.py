@@ -45,3 +45,49 @@ def test_an_output_made_for_another_stream_lives_until_the_current_one_has_read_
     other = cache.attention(c.c, 0, half, cu, stream=s)
     torch.cuda.synchronize()
     assert torch.equal(copy, want) and not torch.equal(other, want)
+
+
+def small_cache(stream=None, pages=256):
+    return cache.make_cache(2, pages, 16, 8, 128, 4, 16, stream=stream)
+
+
+def test_a_cache_made_on_a_stream_is_ready_there():
+    """The current stream is busy; the cache's own goes on at once."""
+    import torch
+    s = torch.cuda.Stream()
+    rows = torch.randn((50, 8, 128), device="cuda").bfloat16()
+    cu = dev([0, 20, 50, 50, 50])
+    torch.cuda.synchronize()
+    torch.cuda._sleep(BUSY)
+    c = small_cache(s)
+    cache.reserve(c, cu, stream=s)
+    cache.append(c, 1, rows, -rows, cu, stream=s)
+    assert cache.last_error(c, stream=s) == (0, 0, -1)
+    torch.cuda.synchronize()
+    assert cache.last_error(c) == (0, 0, -1)
+    table = c.page_table.tolist()
+    for r, (a, b) in enumerate(((0, 20), (20, 50))):
+        for t in range(b - a):
+            at = table[r][t // 16], t % 16
+            assert torch.equal(c.k[1][at], rows[a + t]) and torch.equal(c.v[1][at], -rows[a + t])
+    assert not c.k[0].any() and not c.v[0].any()
+    assert c.held.tolist() == [2, 2, 0, 0] and c.num_free.tolist() == [252]
+
+
+def test_a_cache_made_on_a_stream_is_that_stream_s_memory():
+    """A cache that is dropped while its stream still writes to it does not go to the current stream."""
+    import torch
+    s = torch.cuda.Stream()
+    rows = torch.ones((50, 8, 128), device="cuda").bfloat16()
+    cu = dev([0, 20, 50, 50, 50])
+    torch.cuda.synchronize()
+    c = small_cache(s)
+    size = 2 * c.k.numel()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(BUSY)
+    cache.reserve(c, cu, stream=s)
+    cache.append(c, 1, rows, rows, cu, stream=s)
+    del c
+    mine = torch.full((size,), 2.0, dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    assert (mine == 2).all()
