@@ -31,8 +31,9 @@
  *   - The device that owns the cache's memory is current.
  *   - Calls that change a cache (reserve, append, commit, fork, release) are ordered by the
  *     caller: they run on one stream, or behind one another by events.  Attention only reads; calls
- *     may run at the same time on several streams, each with a workspace of its own.  Appends of
- *     different layers may run at the same time.
+ *     may run at the same time on several streams, each with a workspace of its own; host threads that
+ *     call it on one stream share a workspace only behind a lock (a call launches two kernels).
+ *     Appends of different layers may run at the same time.
  *   - Every call can be captured into a CUDA graph.  All device data (tables, lengths, cu_new) are
  *     read when the graph runs; sizes, pointers and strides are those of the capture.  Two graphs
  *     that can run at the same time need attention workspaces of their own.

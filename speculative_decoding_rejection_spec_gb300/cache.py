@@ -18,6 +18,7 @@ request r.  Chains of k_r drafts are k_r + 1 new tokens: ``cu_new = cu_num_draft
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import threading
 from dataclasses import dataclass, field
@@ -29,6 +30,7 @@ from .binding import SpecRejectError, load as _load_library
 F16, BF16 = 2, 1
 MAX_TREE = 128
 ATTENTION_MAX_HEAD_DIM = 128
+KEPT_WORKSPACES = 8  # of attention, per cache: those of the streams first seen last
 DEVERR_PAGE, DEVERR_CAPACITY, DEVERR_LENGTH, DEVERR_FORK = 32, 64, 128, 256
 
 EXPORTED = [
@@ -137,7 +139,9 @@ class PagedCache:
         # what every call needs, looked up once: the tensors of a cache do not change
         self.ref, self.device, self.index = ctypes.byref(self.struct), dev, dev.index
         self.dtype, self.heads, self.dim = k.dtype, H, D
-        self.workspaces = {}  # attention's, by stream
+        # attention's, by stream: (rows, workspace); the lock is held from the look to the launches, as a call's
+        # two kernels and their workspace belong together whichever host threads call
+        self.workspaces, self.lock = {}, threading.Lock()
 
 
 def _code(t) -> int:
@@ -280,12 +284,11 @@ def attention_workspace_size(c: PagedCache, num_q_heads: int, B: int, N: int) ->
 
 
 def _workspace(c, H, B, N, stream):
-    """A workspace for one call: that of the stream and the host thread, kept with the cache (their calls
-    run one after the other); under capture a new one from the graph's memory, as graphs may run at the
-    same time."""
+    """A workspace for one call: that of the stream, kept with the cache (its calls run one after the
+    other), for KEPT_WORKSPACES streams; under capture a new one from the graph's memory, as graphs may run
+    at the same time.  The caller holds the cache's lock until it has launched the call."""
     rows = min(256, N * (H // c.heads))  # its size grows with these
-    handle = (torch._C._cuda_getCurrentRawStream(c.index) if stream is None else stream.cuda_stream,
-              threading.get_ident())
+    handle = torch._C._cuda_getCurrentRawStream(c.index) if stream is None else stream.cuda_stream
     kept = c.workspaces.get(handle)
     if kept is not None and kept[0] >= rows and not torch._C._cuda_isCurrentStreamCapturing():
         return kept[1]
@@ -298,8 +301,14 @@ def _workspace(c, H, B, N, stream):
             if torch._C._cuda_isCurrentStreamCapturing():
                 return workspace
     if size and not torch._C._cuda_isCurrentStreamCapturing():
+        c.workspaces.pop(handle, None)
+        while len(c.workspaces) >= KEPT_WORKSPACES:  # (memory of its own stream: what runs there goes on)
+            del c.workspaces[next(iter(c.workspaces))]
         c.workspaces[handle] = (rows, workspace)
     return workspace
+
+
+_no_lock = contextlib.nullcontext()
 
 
 def attention(c: PagedCache, layer: int, q, cu_new, parent=None, scale=None, out=None, lse=None, workspace=None,
@@ -311,8 +320,8 @@ def attention(c: PagedCache, layer: int, q, cu_new, parent=None, scale=None, out
     defaults to head_dim ** -0.5; ``out`` may be given (one made for a call on another ``stream`` is
     memory of that stream, kept for the current one); ``lse`` (float32 [N, q_heads], given) receives
     the log of each row's softmax sum; ``workspace`` (uint8) may be given, calls that can run at the
-    same time need one each (without one, the cache keeps one per stream, and a captured graph has its
-    own).  Rows behind ``cu_new[B]`` are left as they were in ``out``.
+    same time and calls of several host threads need one each (without one, the cache keeps one per
+    stream, for KEPT_WORKSPACES streams, and a captured graph has its own).  Rows behind ``cu_new[B]`` are left as they were in ``out``.
     """
     B = _cu(c, cu_new)
     qt, qh = _rows(c, q, None, "q")
@@ -336,11 +345,13 @@ def attention(c: PagedCache, layer: int, q, cu_new, parent=None, scale=None, out
     if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (N, H) or not lse.is_contiguous() or
                             lse.device != c.device):
         raise TypeError(f"lse must be a contiguous float32 tensor of shape {(N, H)} on {c.device}")
-    if workspace is None:
-        workspace = _workspace(c, H, B, N, stream)
-    elif workspace.dtype is not torch.uint8 or workspace.device != c.device or not workspace.is_contiguous():
+    if workspace is not None and (workspace.dtype is not torch.uint8 or workspace.device != c.device or
+                                  not workspace.is_contiguous()):
         raise TypeError(f"workspace must be a contiguous uint8 tensor on {c.device}")
-    _call(c, "spec_attention", stream, layer, q.data_ptr(), qt, qh, H, cu_new.data_ptr(), B, N, _ptr(parent),
-          c.dim ** -0.5 if scale is None else scale, out.data_ptr(), ot, oh, _ptr(lse), workspace.data_ptr(),
-          workspace.numel())
+    with c.lock if workspace is None else _no_lock:
+        if workspace is None:
+            workspace = _workspace(c, H, B, N, stream)
+        _call(c, "spec_attention", stream, layer, q.data_ptr(), qt, qh, H, cu_new.data_ptr(), B, N, _ptr(parent),
+              c.dim ** -0.5 if scale is None else scale, out.data_ptr(), ot, oh, _ptr(lse), workspace.data_ptr(),
+              workspace.numel())
     return out

@@ -1,4 +1,7 @@
 """How the cache's calls treat streams, host threads, captures and the memory that they allocate."""
+import threading
+
+import numpy as np
 import pytest
 
 from speculative_decoding_rejection_spec_gb300 import cache
@@ -91,3 +94,39 @@ def test_a_cache_made_on_a_stream_is_that_stream_s_memory():
     mine = torch.full((size,), 2.0, dtype=torch.bfloat16, device="cuda")
     torch.cuda.synchronize()
     assert (mine == 2).all()
+
+
+def test_host_threads_of_one_stream_share_its_workspace():
+    """Threads that come and go leave nothing behind, and calls of several at once are right."""
+    import torch
+    c = Case([9] * 12, np.random.default_rng(0).integers(0, 3000, 12), page=32, seed=1, poison=False)
+    q, cu = c.q.cuda(), dev(c.cu)
+    want = cache.attention(c.c, 0, q, cu)
+    results, threads = [], []
+
+    def work():
+        torch.cuda.set_device(0)
+        results.extend([cache.attention(c.c, 0, q, cu) for _ in range(20)])
+
+    for _ in range(2):
+        threads = [threading.Thread(target=work) for _ in range(5)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    torch.cuda.synchronize()
+    assert len(results) == 200 and all(torch.equal(x, want) for x in results)
+    assert len(c.c.workspaces) == 1
+
+
+def test_workspaces_of_few_streams_are_kept():
+    import torch
+    c = Case([9] * 12, np.random.default_rng(0).integers(0, 3000, 12), page=32, seed=1, poison=False)
+    q, cu = c.q.cuda(), dev(c.cu)
+    want = cache.attention(c.c, 0, q, cu)
+    streams = [torch.cuda.Stream() for _ in range(20)]
+    torch.cuda.synchronize()
+    results = [cache.attention(c.c, 0, q, cu, stream=s) for s in streams * 3]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want) for x in results)
+    assert 0 < len(c.c.workspaces) <= cache.KEPT_WORKSPACES
