@@ -283,24 +283,20 @@ def attention_workspace_size(c: PagedCache, num_q_heads: int, B: int, N: int) ->
     return int(n)
 
 
-def _workspace(c, H, B, N, stream):
-    """A workspace for one call: that of the stream, kept with the cache (its calls run one after the
-    other), for KEPT_WORKSPACES streams; under capture a new one from the graph's memory, as graphs may run
-    at the same time.  The caller holds the cache's lock until it has launched the call."""
+def _workspace(c, H, B, N):
+    """A workspace for one call on the current stream (of the cache's device, the current one): that of the
+    stream, kept with the cache (its calls run one after the other), for KEPT_WORKSPACES streams; under
+    capture a new one from the graph's memory, as graphs may run at the same time.  The caller holds the
+    cache's lock until it has launched the call."""
     rows = min(256, N * (H // c.heads))  # its size grows with these
-    handle = torch._C._cuda_getCurrentRawStream(c.index) if stream is None else stream.cuda_stream
-    kept = c.workspaces.get(handle)
-    if kept is not None and kept[0] >= rows and not torch._C._cuda_isCurrentStreamCapturing():
+    handle = torch._C._cuda_getCurrentRawStream(c.index)
+    capturing = torch._C._cuda_isCurrentStreamCapturing()
+    kept = None if capturing else c.workspaces.get(handle)
+    if kept is not None and kept[0] >= rows:
         return kept[1]
     size = _lib.spec_attention_workspace_size(c.ref, H, B, N)
-    if stream is None:
-        workspace = torch.empty(size, dtype=torch.uint8, device=c.device)
-    else:
-        with torch.cuda.stream(stream):
-            workspace = torch.empty(size, dtype=torch.uint8, device=c.device)
-            if torch._C._cuda_isCurrentStreamCapturing():
-                return workspace
-    if size and not torch._C._cuda_isCurrentStreamCapturing():
+    workspace = torch.empty(size, dtype=torch.uint8, device=c.device)
+    if size and not capturing:
         c.workspaces.pop(handle, None)
         while len(c.workspaces) >= KEPT_WORKSPACES:  # (memory of its own stream: what runs there goes on)
             del c.workspaces[next(iter(c.workspaces))]
@@ -321,22 +317,28 @@ def attention(c: PagedCache, layer: int, q, cu_new, parent=None, scale=None, out
     memory of that stream, kept for the current one); ``lse`` (float32 [N, q_heads], given) receives
     the log of each row's softmax sum; ``workspace`` (uint8) may be given, calls that can run at the
     same time and calls of several host threads need one each (without one, the cache keeps one per
-    stream, for KEPT_WORKSPACES streams, and a captured graph has its own).  Rows behind ``cu_new[B]`` are left as they were in ``out``.
+    stream, for KEPT_WORKSPACES streams, and a captured graph has its own).  Rows behind
+    ``cu_new[B]`` are left as they were in ``out``.
     """
+    if stream is not None:
+        # all of the call on that stream: what it allocates is memory of the stream that writes it (the current
+        # one's may have been freed with work queued there that still uses it), and of its graph under capture
+        before = torch.cuda.current_stream(c.device)
+        with torch.cuda.stream(stream):
+            result = attention(c, layer, q, cu_new, parent, scale, out, lse, workspace)
+        if out is None:
+            result.record_stream(before)  # which will read it
+        return result
+    if torch._C._cuda_getDevice() != c.index:
+        with torch.cuda.device(c.index):
+            return attention(c, layer, q, cu_new, parent, scale, out, lse, workspace)
     B = _cu(c, cu_new)
     qt, qh = _rows(c, q, None, "q")
     N, H, _ = q.shape
     if parent is not None:
         _int32(parent, (N,), "parent", c.device)
     if out is None:
-        if stream is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        else:
-            # memory of the stream that writes it: the current one's may have been freed with work queued
-            # there that still uses it.  Recorded for the current one, which will read it.
-            with torch.cuda.stream(stream):
-                out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            out.record_stream(torch.cuda.current_stream(c.device))
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         ot, oh = H * c.dim, c.dim
     elif out.shape != q.shape:
         raise ValueError("out must have the shape of q")
@@ -350,8 +352,8 @@ def attention(c: PagedCache, layer: int, q, cu_new, parent=None, scale=None, out
         raise TypeError(f"workspace must be a contiguous uint8 tensor on {c.device}")
     with c.lock if workspace is None else _no_lock:
         if workspace is None:
-            workspace = _workspace(c, H, B, N, stream)
-        _call(c, "spec_attention", stream, layer, q.data_ptr(), qt, qh, H, cu_new.data_ptr(), B, N, _ptr(parent),
+            workspace = _workspace(c, H, B, N)
+        _call(c, "spec_attention", None, layer, q.data_ptr(), qt, qh, H, cu_new.data_ptr(), B, N, _ptr(parent),
               c.dim ** -0.5 if scale is None else scale, out.data_ptr(), ot, oh, _ptr(lse), workspace.data_ptr(),
               workspace.numel())
     return out

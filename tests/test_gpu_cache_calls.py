@@ -130,3 +130,28 @@ def test_workspaces_of_few_streams_are_kept():
     torch.cuda.synchronize()
     assert all(torch.equal(x, want) for x in results)
     assert 0 < len(c.c.workspaces) <= cache.KEPT_WORKSPACES
+
+
+def test_a_capture_on_the_given_stream_has_a_workspace_of_its_own():
+    """Only ``stream=`` is capturing, not the current stream: the graph does not touch the kept workspace."""
+    import torch
+    c = Case([9, 3], [5000, 700], page=32, seed=1, poison=False)
+    q, cu, s = c.q.cuda(), dev(c.cu), torch.cuda.Stream()
+    out = torch.zeros_like(q)
+    torch.cuda.synchronize()
+    want = cache.attention(c.c, 0, q, cu, stream=s)
+    torch.cuda.synchronize()
+    kept = [w[-1] for w in c.c.workspaces.values()]
+    assert kept and all(w.any() for w in kept)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s):
+        graph.capture_begin(capture_error_mode="relaxed")
+    cache.attention(c.c, 0, q, cu, out=out, stream=s)
+    with torch.cuda.stream(s):
+        graph.capture_end()
+    for w in kept:
+        w.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    assert not any(w.any() for w in kept)
