@@ -159,10 +159,18 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _of_device(stream, index):
+    """Refuses a stream of another device than the cache's: a launch there would fail in the driver."""
+    if stream.device_index != index:
+        raise ValueError(f"stream must be one of cuda:{index}")
+
+
 def _call(c, name, stream, *args):
     """Calls a library function on the cache's device and a stream (the device's current one, by its raw
     handle, unless one is given)."""
     index = c.index
+    if stream is not None:
+        _of_device(stream, index)
     if torch._C._cuda_getDevice() != index:
         with torch.cuda.device(index):
             return _call(c, name, stream, *args)
@@ -180,6 +188,7 @@ def make_cache(num_layers: int, num_pages: int, page_size: int, num_kv_heads: in
     if dev.type == "cuda" and dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
     if stream is not None:
+        _of_device(stream, dev.index)
         with torch.cuda.stream(stream):
             return make_cache(num_layers, num_pages, page_size, num_kv_heads, head_dim, num_requests, max_pages, dtype,
                               dev)
@@ -194,6 +203,8 @@ def make_cache(num_layers: int, num_pages: int, page_size: int, num_kv_heads: in
 
 def last_error(c: PagedCache, stream=None):
     """(status, error_bits, first_bad_request) since the last call, and clears them (synchronises)."""
+    if stream is not None:
+        _of_device(stream, c.index)
     bits, first = ctypes.c_int32(0), ctypes.c_int32(0)
     with torch.cuda.device(c.device):
         s = torch.cuda.current_stream() if stream is None else stream
@@ -323,6 +334,7 @@ def attention(c: PagedCache, layer: int, q, cu_new, parent=None, scale=None, out
     if stream is not None:
         # all of the call on that stream: what it allocates is memory of the stream that writes it (the current
         # one's may have been freed with work queued there that still uses it), and of its graph under capture
+        _of_device(stream, c.index)
         before = torch.cuda.current_stream(c.device)
         with torch.cuda.stream(stream):
             result = attention(c, layer, q, cu_new, parent, scale, out, lse, workspace)

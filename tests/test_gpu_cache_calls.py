@@ -1,5 +1,6 @@
 """How the cache's calls treat streams, host threads, captures and the memory that they allocate."""
 import threading
+import types
 
 import numpy as np
 import pytest
@@ -155,3 +156,18 @@ def test_a_capture_on_the_given_stream_has_a_workspace_of_its_own():
     torch.cuda.synchronize()
     assert torch.equal(out, want)
     assert not any(w.any() for w in kept)
+
+
+def test_streams_of_other_devices_are_refused():
+    c = Case([9, 3], [50, 7], seed=1)
+    cu = dev(c.cu)
+    other = types.SimpleNamespace(cuda_stream=0, device_index=1)
+    with pytest.raises(ValueError):
+        cache.attention(c.c, 0, c.q.cuda(), cu, stream=other)
+    with pytest.raises(ValueError):
+        cache.reserve(c.c, cu, stream=other)
+    with pytest.raises(ValueError):
+        cache.last_error(c.c, stream=other)
+    with pytest.raises(ValueError):
+        small_cache(other)
+    c.check(*c.run())
