@@ -111,7 +111,7 @@ struct AttentionParams {
     float scale_log2;
     // workspace
     Partial *partial;   // [grid]
-    float2 *part_ml;    // [grid * 2 * max_rows] M, l
+    float2 *part_ml;    // [grid * 2 * max_rows] M, l (0, -1: a row of a refused request, whose part_o is not written)
     float *part_o;      // [grid * 2 * max_rows * DP]
     int32_t max_rows;
 };
@@ -1031,25 +1031,31 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const int turns = wide ? nt : (nt - g + 1) / 2;  // this group's tiles
 
             uint32_t bits[kMaxTree / 32] = {};
-            if (p.parent && turns > 0 && !dry) {
+            bool refused = false;  // the request's tree is malformed: every row block of it is left out
+            if (p.parent && !dry) {
                 int32_t *par = S.group[g].parent;  // every warp of the group writes the same there
-                for (int i = lane; i < item.n; i += 32)
-                    par[i] = p.parent[item.first + i];
+                bool bad = false;
+                for (int i = lane; i < item.n; i += 32) {
+                    const int up = p.parent[item.first + i];
+                    bad |= i == 0 ? up != -1 : up < 0 || up >= i;
+                    if (turns > 0)  // a group without tiles does not wait for its warps before it writes ml[] there
+                        par[i] = up;
+                }
+                refused = __any_sync(kFull, bad);
                 __syncwarp();
-                if (on)
-                    for (int at = token; at >= 0;) {
+                if (refused) {
+                    if (lane == 0)
+                        cache_error(c.error, SPEC_DEVERR_TREE, item.r);
+                } else if (on && turns > 0) {
+                    for (int at = token; at >= 0; at = par[at]) {
 #pragma unroll
                         for (int j = 0; j < kMaxTree / 32; ++j)
                             bits[j] |= at / 32 == j ? 1u << (at & 31) : 0u;
-                        const int up = par[at];
-                        if (at == 0 ? up != -1 : up < 0 || up >= at) {
-                            cache_error(c.error, SPEC_DEVERR_TREE, item.r);
-                            break;
-                        }
-                        at = up;
                     }
+                }
                 __syncwarp();
             }
+            const bool kept = on && !refused;  // the row has a result
             // keys that every row of this warp sees
             const int all_see = p.parent ? item.len
                                          : item.len + by_group(p, item.b * kBlockRows + m0 + sub * 32) + 1;
@@ -1192,7 +1198,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const int64_t place = ((int64_t)blockIdx.x * 2 + (item.t0 == 0)) * p.max_rows + m0 + row;
             char *out = p.out + 2 * ((int64_t)(item.first + token) * p.out_token + head * p.out_head);
             auto store = [&](const float *o, int col, float by) {  // 32 columns
-                if (!on)
+                if (!kept)
                     return;
                 if (whole) {
 #pragma unroll
@@ -1214,14 +1220,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (!on)
                     return;
                 if (!whole)
-                    p.part_ml[place] = make_float2(M, l);
-                else if (p.lse)
+                    p.part_ml[place] = refused ? make_float2(0, -1) : make_float2(M, l);
+                else if (p.lse && kept)
                     p.lse[(int64_t)(item.first + token) * p.heads + head] = (M + log2f(l)) * 0.69314718055994531f;
             };
             // (The groups are less than two row blocks apart, by their meetings or, of wide ones, by the order
             // of the products: nobody writes spoilt[] for the next but one before all have read it here.)
             auto spoilt = [&]() {
-                if (cut_block && on && S.spoilt[cuts & 1] == cuts)
+                if (cut_block && kept && S.spoilt[cuts & 1] == cuts)
                     add_spoilt<DT>(c, p, item.r, item.h, max(common, item.t0 * kTile), last, item.len, token,
                                    make_uint4(bits[0], bits[1], bits[2], bits[3]),
                                    whole ? out : reinterpret_cast<char *>(p.part_o + place * DP), !whole);
@@ -1397,6 +1403,8 @@ __device__ __forceinline__ void join(const CacheView &c, const AttentionParams &
         const int row = row0 + j * next;
         if (row >= x.rows)
             return;
+        if (l[j] < 0)
+            continue;  // of a refused request: its parts have sums of -1
         const int m = x.b * kBlockRows + row;
         const int token = by_group(p, m), head = x.h * p.group + m - token * p.group;
         const int64_t t = (int64_t)first + token;
