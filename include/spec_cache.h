@@ -58,9 +58,9 @@ extern "C" {
 #define SPEC_DEVERR_PAGE 32     /* a page id outside [0, num_pages), a page written that is not the
                                    request's alone, a page released more often than it is held */
 #define SPEC_DEVERR_CAPACITY 64 /* reserve: the free pages do not suffice */
-#define SPEC_DEVERR_LENGTH 128  /* a negative length, more tokens than max_pages pages (or, where
-                                   they are shared, the pages held) contain, an accepted count
-                                   outside [-1, n_r) */
+#define SPEC_DEVERR_LENGTH 128  /* a negative length; more tokens than max_pages pages (reserve, append)
+                                   or the pages held (attention, commit, fork) contain, so also a step
+                                   whose reserve found no room; an accepted count outside [-1, n_r) */
 #define SPEC_DEVERR_FORK 256    /* a fork's source or destination out of range, a destination that
                                    holds pages, is named twice or is also a source */
 
@@ -121,6 +121,9 @@ spec_status spec_cache_error(const spec_cache *cache, void *stream, int32_t *err
  * When the free pages do not suffice nothing is changed (SPEC_DEVERR_CAPACITY, with the first
  * request that finds none); a request that would pass max_pages is skipped
  * (SPEC_DEVERR_LENGTH).  Pages reserved and not used (rejected drafts) stay with the request.
+ * A step that goes on without its room: append skips the rows (SPEC_DEVERR_PAGE), attention and commit
+ * the requests whose pages do not contain the new tokens (SPEC_DEVERR_LENGTH).  Where all that was
+ * missing is the copy of a shared page, commit cannot tell: its num_accepted must be -1.
  */
 spec_status spec_cache_reserve(const spec_cache *cache, const int32_t *cu_new, int32_t B, void *stream);
 
@@ -138,8 +141,9 @@ spec_status spec_cache_append(const spec_cache *cache, int32_t layer, const void
 
 /*
  * The step's outcome: lens[r] advances by num_accepted[r] + 1 where n_r > 0 and num_accepted[r] >=
- * 0 (-1, a request reported invalid, commits nothing).  With a tree, the accepted path from the
- * root to last_node[r] (num_accepted[r] + 1 nodes) is moved, in every layer, to positions
+ * 0 (-1, a request reported invalid, commits nothing), and where the pages held contain the step's
+ * tokens (SPEC_DEVERR_LENGTH otherwise, and the length stays).  With a tree, the accepted path from
+ * the root to last_node[r] (num_accepted[r] + 1 nodes) is moved, in every layer, to positions
  * lens[r] + depth; rows that already lie there stay.
  *   parent, last_node  device int32 [N] and [B], as spec_tree_verify_greedy() takes and returns
  *                      them; both NULL for chains
@@ -185,9 +189,10 @@ spec_status spec_cache_release(const spec_cache *cache, const int32_t *keep_lens
  *   workspace     spec_attention_workspace_size() bytes; contents need no initialisation
  * page_size is a multiple of 8, head_dim at most SPEC_ATTENTION_MAX_HEAD_DIM and N * num_q_heads
  * below 2^30 (SPEC_ERR_UNSUPPORTED otherwise).  The keys and values of all lens[r] + n_r tokens are
- * read, rows behind them are not used whatever they hold.  A key or value that is not finite reaches
- * the rows that see it and no others.  A page id out of range reads as zeros (SPEC_DEVERR_PAGE); the
- * rows of other requests with errors are not written.
+ * read, from the pages held (SPEC_DEVERR_LENGTH where those contain fewer); rows behind them are not
+ * used whatever they hold.  A key or value that is not finite reaches the rows that see it and no
+ * others.  A page id out of range reads as zeros (SPEC_DEVERR_PAGE); the rows of other requests with
+ * errors are not written.
  */
 size_t spec_attention_workspace_size(const spec_cache *cache, int32_t num_q_heads, int32_t B, int64_t N);
 spec_status spec_attention(const spec_cache *cache, int32_t layer, const void *q, int64_t q_token_stride,

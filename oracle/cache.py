@@ -99,7 +99,8 @@ class Book:
             if m == 0 or a == -1:
                 continue
             length = int(self.lens[r])
-            if a < -1 or a >= m or length < 0 or length + m > self.MP * self.P:
+            held = int(self.held[r])
+            if a < -1 or a >= m or length < 0 or not 0 <= held <= self.MP or length + m > held * self.P:
                 self._error(LENGTH, r)
                 continue
             if parents is not None:

@@ -341,7 +341,7 @@ __device__ __forceinline__ int block_tiles(const AttentionParams &p, const Reque
 
 // The request's sizes; cost = 0 when there is nothing to do, or an error, which is recorded on demand.
 __device__ __forceinline__ Request request_of(const CacheView &c, const AttentionParams &p, int r, int n, int len,
-                                              bool report)
+                                              int held, bool report)
 {
     Request q;
     q.n = n;
@@ -351,7 +351,7 @@ __device__ __forceinline__ Request request_of(const CacheView &c, const Attentio
     if (n <= 0)
         return q;
     const int64_t blocks = (q.rows + kBlockRows - 1) / kBlockRows;
-    if (len < 0 || (int64_t)len + n > (int64_t)c.max_pages * c.page_size || (p.parent && n > kMaxTree) ||
+    if (!holds(c, held, len, n) || (p.parent && n > kMaxTree) ||
         blocks * (kBlockCost + 1 + ((int64_t)len + n) / kTile) > INT32_MAX) {
         if (report)
             cache_error(c.error, p.parent && n > kMaxTree ? SPEC_DEVERR_TREE : SPEC_DEVERR_LENGTH, r);
@@ -365,7 +365,7 @@ __device__ __forceinline__ Request request_of(const CacheView &c, const Attentio
 
 __device__ __forceinline__ Request request_of(const CacheView &c, const AttentionParams &p, int r, bool report)
 {
-    return request_of(c, p, r, p.cu[r + 1] - p.cu[r], c.lens[r], report);
+    return request_of(c, p, r, p.cu[r + 1] - p.cu[r], c.lens[r], c.held[r], report);
 }
 
 // Walks a block's share, one (request, head, row block) at a time; a whole warp.  A row block takes
@@ -558,11 +558,12 @@ __device__ __forceinline__ bool find_share(const CacheView &c, const AttentionPa
         for (int r0 = 0; r0 < p.B; r0 += 32) {
             const int r = r0 + lane;
             if (pass == 0 || p.B > 32) {
-                const int32_t here = p.cu[min(r, p.B)], next = p.cu[min(r + 1, p.B)], len = c.lens[min(r, p.B - 1)];
+                const int32_t here = p.cu[min(r, p.B)], next = p.cu[min(r + 1, p.B)], len = c.lens[min(r, p.B - 1)],
+                              held = c.held[min(r, p.B - 1)];
                 bad |= here > next || next > p.N || here < 0 || (r == 0 && here != 0);
                 q.cost = 0;
                 if (r < p.B && !bad) {
-                    q = request_of(c, p, r, next - here, len, false);
+                    q = request_of(c, p, r, next - here, len, held, false);
                     wrong |= q.cost == 0 && q.n > 0;
                 }
                 work = (int64_t)q.cost * c.heads;

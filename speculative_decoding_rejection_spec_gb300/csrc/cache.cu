@@ -452,11 +452,11 @@ __global__ void __launch_bounds__(kCopyThreads) append_kernel(CacheView c, NewRo
 __device__ __forceinline__ int64_t commit_length(const CacheView &c, const int32_t *cu, const int32_t *accepted,
                                                  int r, bool report)
 {
-    const int n = cu[r + 1] - cu[r], a = accepted[r];
+    const int n = cu[r + 1] - cu[r], a = accepted[r], held = c.held[r];
     const int64_t len = c.lens[r];
     if (n == 0 || a == -1)
         return len;
-    if (a < -1 || a >= n || len < 0 || len + n > (int64_t)c.max_pages * c.page_size) {
+    if (a < -1 || a >= n || !holds(c, held, (int)len, n)) {
         if (report)
             cache_error(c.error, SPEC_DEVERR_LENGTH, r);
         return -1;

@@ -128,6 +128,12 @@ __device__ __forceinline__ int pages_of(int64_t tokens, int page_size)
     return (int)((tokens + page_size - 1) / page_size);
 }
 
+// Whether the pages that a request holds contain its len committed tokens and n new ones.
+__device__ __forceinline__ bool holds(const CacheView &c, int held, int len, int n)
+{
+    return len >= 0 && held >= 0 && held <= c.max_pages && (int64_t)len + n <= (int64_t)held * c.page_size;
+}
+
 // The request of row t by a 32-way search of the warp over cu[0 .. B]: the largest r with cu[r] <=
 // t, and with it cu[r + 1] > t when cu does not decrease (requests of no rows are passed over).
 // -1 when t lies outside [cu[0], cu[B]).

@@ -199,3 +199,18 @@ def test_pages_past_32_bits_are_refused(lib):
     assert lib.spec_cache_reserve(ctypes.byref(s), ctypes.c_void_p(FAKE), 1, None) == 2
     s.page_size = 2 ** 23 - 8
     assert lib.spec_attention_workspace_size(ctypes.byref(s), 16, 1, 4) > 0
+
+
+def test_oracle_commits_only_what_the_pages_hold():
+    """A step whose reserve found no room leaves the length as it was, and finds its room later."""
+    b = oracle_cache.Book(2, 4, 3, 16)
+    b.reserve([30, 10])
+    b.commit([30, 10], [29, 9])
+    b.reserve([5, 5])
+    assert b.take_error() == (oracle_cache.CAPACITY, 0)
+    b.commit([5, 5], [4, 4])
+    assert b.take_error() == (oracle_cache.LENGTH, 0) and b.lens.tolist() == [30, 15]
+    b.release([30, 0])
+    b.reserve([5, 0])
+    b.commit([5, 0], [4, 0])
+    assert b.take_error() == (0, -1) and b.lens.tolist() == [35, 0]
