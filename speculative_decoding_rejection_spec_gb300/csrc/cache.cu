@@ -92,7 +92,7 @@ struct Ask {
     int need, shared;
 };
 
-__device__ __forceinline__ Ask reserve_ask(const CacheView &c, const int32_t *cu, int r, bool report)
+__device__ __forceinline__ Ask reserve_ask(const CacheView &c, const int32_t *cu, int r)
 {
     Ask a{0, -1};
     const int n = cu[r + 1] - cu[r];
@@ -102,15 +102,13 @@ __device__ __forceinline__ Ask reserve_ask(const CacheView &c, const int32_t *cu
     const int held = c.held[r];
     if (len < 0 || held < 0 || held > c.max_pages || len > (int64_t)held * c.page_size ||
         len + n > (int64_t)c.max_pages * c.page_size) {
-        if (report)
-            cache_error(c.error, SPEC_DEVERR_LENGTH, r);
+        cache_error(c.error, SPEC_DEVERR_LENGTH, r);
         return a;
     }
     if (len % c.page_size) {
         const int page = c.table[r * c.table_stride + len / c.page_size];
         if (page < 0 || page >= c.num_pages || c.ref[page] < 1) {
-            if (report)
-                cache_error(c.error, SPEC_DEVERR_PAGE, r);
+            cache_error(c.error, SPEC_DEVERR_PAGE, r);
             return a;
         }
         if (c.ref[page] > 1)
@@ -252,8 +250,8 @@ __global__ void __launch_bounds__(kBookThreads) reserve_many_kernel(CacheView c,
         const int r = r0 + tid;
         Ask a{0, -1};
         if (r < B) {
-            a = reserve_ask(c, cu, r, true);
-            c.flags[r] = 0;
+            a = reserve_ask(c, cu, r);
+            c.flags[r] = a.need > 0 ? 0 : -1;  // -1: gets nothing, whatever the counts become
         }
         const int64_t at = nwriters + block_scan<kBookThreads>(a.shared >= 0, &total);
         if (a.shared >= 0)
@@ -278,9 +276,10 @@ __global__ void __launch_bounds__(kBookThreads) reserve_many_kernel(CacheView c,
     for (int r0 = 0; r0 < B; r0 += kBookThreads) {
         const int r = r0 + tid;
         int64_t fresh = 0;
-        if (r < B) {
-            const Ask a = reserve_ask(c, cu, r, false);
-            fresh = (a.need > c.held[r] ? a.need - c.held[r] : 0) + (a.need > 0 ? c.flags[r] : 0);
+        const int copies = r < B ? c.flags[r] : -1;
+        if (copies >= 0) {
+            const int need = pages_of((int64_t)c.lens[r] + (cu[r + 1] - cu[r]), c.page_size), held = c.held[r];
+            fresh = (need > held ? need - held : 0) + copies;
         }
         const int64_t at = used + block_scan<kBookThreads>(fresh, &total);
         if (r < B) {
@@ -296,24 +295,16 @@ __global__ void __launch_bounds__(kBookThreads) reserve_many_kernel(CacheView c,
             cache_error(c.error, SPEC_DEVERR_CAPACITY, first_short);
         return;
     }
-    // Hand out: a warp per request, as pages per request may be many.  Lane 0 decides from the
-    // state before any write to this request's own entries; counts of shared pages only go down
-    // here, by the requests that copy, which was settled above.
+    // Hand out: a warp per request, as pages per request may be many.  Who gets pages and who copies was
+    // settled above: counts change from here on.
     for (int r = w; r < B; r += kBookThreads / 32) {
+        if (c.flags[r] < 0)
+            continue;
         const int n = cu[r + 1] - cu[r];
         const int64_t len = c.lens[r];
         const int held = c.held[r];
-        const bool fits = n > 0 && len >= 0 && held >= 0 && held <= c.max_pages &&
-                          len <= (int64_t)held * c.page_size && len + n <= (int64_t)c.max_pages * c.page_size;
-        if (!fits)
-            continue;
         int32_t *row = c.table + r * c.table_stride;
         const bool copies = c.flags[r] != 0;
-        if (!copies && len % c.page_size) {
-            const int page = row[len / c.page_size];
-            if (page < 0 || page >= c.num_pages || c.ref[page] < 1)
-                continue;
-        }
         const int need = pages_of(len + n, c.page_size);
         const int64_t top = have - 1 - c.base[r];
         for (int i = held + lane; i < need; i += 32) {

@@ -86,3 +86,21 @@ def test_a_step_without_room_commits_nothing(tree):
     p.append(n)
     p.commit(n, [4, 2, 0])
     p.check()
+
+
+@pytest.mark.parametrize("requests", [900, 1500])
+def test_a_skipped_request_among_many_gets_nothing(requests):
+    """A table that names a free page, which the same call hands to another request: the request is skipped and
+    no page goes to two requests."""
+    p = Pair(requests, 4, 8000, 8, layers=1, heads=1, dim=8)
+    n, bad = [5] * requests, requests - 100
+    p.reserve(n)
+    p.append(n)
+    p.commit(n, [4] * requests)
+    p.check()
+    p.book.table[bad, 0] = p.book.free[p.book.num_free - 1]  # goes to request 0
+    p.c.page_table.copy_(dev(p.book.table))
+    p.reserve([8] * requests)
+    p.check((cache.DEVERR_PAGE, bad))
+    pages = p.book.table[:, :2][np.arange(requests) != bad]
+    assert len(np.unique(pages)) == pages.size
