@@ -43,6 +43,7 @@
 #include <cuda_fp16.h>
 
 #include "cache.cuh"
+#include "drain.cuh"
 
 namespace specrej {
 namespace {
@@ -290,13 +291,15 @@ template <int SLOTS> struct alignas(16) AttnShared {
     uint64_t ready, merge, done;
     uint64_t known[2];  // group 0 of a wide row block has looked at its last values (by turns)
     uint32_t tmem;
+    uint32_t arrivals[SLOTS + 2];  // made on full[] and q_full[] in all, added up as the loading roles end
     volatile int32_t gave_up;
     volatile int32_t spoilt[2];  // the number of a row block among those with unseen keys, by its last bit
 };
 
 // Waits for a barrier's phase, a bounded number of polls.  When one wait gives up, all do: no row block
-// is begun and no copy started any more, what has begun runs through without waiting (its indices are
-// those of an announced row block), and the roles leave together.  A wait of try_wait is suspended and
+// is begun, no copy started and no slot given back any more; the softmax of what has begun runs through
+// without waiting (its indices are those of an announced row block); the roles leave together, and the
+// copies in flight are waited for before the block does.  A wait of try_wait is suspended and
 // woken late; the thread that issues the products polls instead (SPIN): prompt chunks 0.356 -> 0.330 ms.
 // The others do not, for the sake of the schedulers they share.
 template <bool SPIN>
@@ -647,6 +650,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         mbar_init(&S.done, 1);
         mbar_init(&S.known[0], 4);
         mbar_init(&S.known[1], 4);
+        for (int i = 0; i < SLOTS + 2; ++i)
+            S.arrivals[i] = 0;
         S.gave_up = 0;
         S.spoilt[0] = S.spoilt[1] = 0;
         mbar_fence_init();
@@ -686,6 +691,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             struct Pieces {
                 int page, token;
             };
+            uint32_t arrivals = 0;  // lane i: on full[i]
             for (uint32_t k = 0;; ++k) {
                 if (!announced(k))
                     break;
@@ -725,9 +731,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     const int count = __popc(__ballot_sync(kFull, now.token >= 0) >> from & low_bits(pieces));
                     if (turn > 0)
                         wait(&S.empty[slot], (turn & 1) ^ 1);
-                    __syncwarp();
-                    if (S.gave_up)
-                        continue;
+                    if (__any_sync(kFull, S.gave_up))
+                        break;
+                    arrivals += lane == slot;
                     const uint32_t dst = smem_addr(ring) + slot * Z::kSlotBytes;
                     uint64_t *bar = &S.full[slot];
                     constexpr int kChunks = DP / 64;
@@ -745,6 +751,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     __syncwarp();
                 }
             }
+            if (lane < SLOTS)
+                atomicAdd(&S.arrivals[lane], arrivals);
         } else if (warp == kMmaWarp) {
             if (elect_one()) {
                 const uint64_t q_desc = smem_desc(smem_addr(qtile), 16), k_desc = smem_desc(smem_addr(ring), 16),
@@ -754,13 +762,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 // barriers of the next step are looked at together, beside the commits of this one, and
                 // waited for only if they were not through then.
                 uint32_t slot = 0, turn = 0, p_turn = 0;  // p_turn: a bit per group
+                bool lost = false;                        // a wait gave up: no slot is given back any more
                 auto full_here = [&](uint32_t i) {        // slot i from the next
                     const uint32_t s = slot + i;
                     return s < SLOTS ? mbar_test_wait(&S.full[s], turn) : mbar_test_wait(&S.full[s - SLOTS], turn ^ 1);
                 };
                 auto take = [&](bool here) {  // the next slot, landed
                     if (!here)
-                        spin(&S.full[slot], turn);
+                        lost |= !spin(&S.full[slot], turn);
                     const uint32_t s = slot;
                     if (++slot == SLOTS) {
                         slot = 0;
@@ -786,12 +795,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 auto p_here = [&](int g) { return mbar_test_wait(&S.p_full[g], p_turn >> g & 1); };
                 auto p_ready = [&](int g, bool here) {
                     if (!here)
-                        spin(&S.p_full[g], p_turn >> g & 1);
+                        lost |= !spin(&S.p_full[g], p_turn >> g & 1);
                     p_turn ^= 1u << g;
                     tmem_fence_after();
                 };
-                wait(&S.ready, 0);
-                for (uint32_t k = 0;; ++k) {
+                lost = !wait(&S.ready, 0);
+                for (uint32_t k = 0; !lost; ++k) {
                     if (!announced(k))
                         break;
                     const Item &item = S.item[k % kItems];
@@ -801,7 +810,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     if (nt == 0)
                         break;
                     for (int g = 0; g <= (int)wide; ++g)
-                        wait(&S.q_full[(q_use + g) & 1], (q_use + g) >> 1 & 1);
+                        lost |= !wait(&S.q_full[(q_use + g) & 1], (q_use + g) >> 1 & 1);
                     // step t: scores of tile t, outputs of tile t - 1
                     bool k_in = false, v_in = false, p_in = false;
                     if (!wide) {
@@ -820,6 +829,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                 if (t + 1 >= nt)
                                     mma_commit(&S.o_full[g]);
                             }
+                            if (lost)
+                                break;
                             if (t < nt) {
                                 const bool more = t + 1 < nt;
                                 k_in = more && full_here(0);
@@ -849,6 +860,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                     scores(g, kslot, (q_use + g) & 1);
                                 mma_commit(t < nt ? &S.s_full[g] : &S.o_full[g]);
                             }
+                            if (lost)
+                                break;
                             if (t < nt) {
                                 const bool more = t + 1 < nt;
                                 k_in = more && full_here(0);
@@ -876,7 +889,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             Shares shares;
             const int part = warp == kWalkWarp ? 0 : warp - 7;
             int q_use = 0;
-            uint32_t slots = 0;
+            uint32_t slots = 0, arrivals = 0;  // arrivals: lane i: on q_full[i]
             bool more = false;
             if (warp == kWalkWarp) {
                 if (lane == 0)
@@ -935,13 +948,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     const int use = item.q_use + g;
                     if (use >= 2)
                         wait(&S.q_empty[use & 1], (use >> 1 & 1) ^ 1);
+                    if (__any_sync(kFull, S.gave_up))
+                        break;
+                    arrivals += lane == (use & 1);
                     const int at = part * 32 + lane, vec = at % kVecs;
                     const uint32_t dst = smem_addr(qtile) + (use & 1) * Z::kSlotBytes + vec / 8 * Z::kChunk;
                     const int m0 = item.b * kBlockRows + g * kTile, rows = min(kTile, item.rows - g * kTile);
                     if (count == 2 && p.q_tokens) {
                         // a wide row block's: one copy for each 64 elements (rows behind the last are not
                         // looked at); row by row they took 7 us, with the products waiting
-                        if (warp == kWalkWarp && !S.gave_up) {
+                        if (warp == kWalkWarp) {
                             if (elect_one()) {
                                 mbar_arrive_expect_tx(&S.q_full[use & 1], Z::kSlotBytes);
 #pragma unroll
@@ -984,6 +1000,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (warp == kWalkWarp)
                     more = w.next(c, p);
             }
+            if (lane < 2)
+                atomicAdd(&S.arrivals[SLOTS + lane], arrivals);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -1293,12 +1311,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         tmem_fence_before();
     }
     __syncthreads();
-    if (warp == 10 && S.gave_up) {
-        // copies that nobody waited for; a slot that none was started into waits in vain, for a while
-        for (int i = 0; i < SLOTS + 2; ++i) {
-            uint64_t *bar = i < SLOTS ? &S.full[i] : &S.q_full[i - SLOTS];
-            for (uint32_t n = 0; n < 4096 && !(mbar_try_wait(bar, 0) && mbar_try_wait(bar, 1)); ++n) {
-            }
+    if (warp == 10 && S.gave_up && lane < SLOTS + 2) {
+        // copies that nobody waited for: a lane per barrier
+        uint64_t *bar = lane < SLOTS ? &S.full[lane] : &S.q_full[lane - SLOTS];
+        const Drain d = drain_of(S.arrivals[lane], lane < SLOTS ? 2 : kQueryWarps);
+        for (uint32_t i = 0; i < d.missing; ++i)
+            mbar_arrive(bar);
+        for (uint32_t i = 0; d.begun && i < kWaitLimit && !mbar_try_wait(bar, d.parity); ++i) {
         }
     }
     __syncthreads();
