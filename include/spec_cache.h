@@ -180,7 +180,8 @@ spec_status spec_cache_release(const spec_cache *cache, const int32_t *keep_lens
  *   lse = log sum_t exp(scale * (q . k_t))
  * Products of the cache's 16-bit values are summed in fp32; the maximum, the sum and the output's
  * accumulator are fp32; p is rounded to the cache's type once before its product with v (its sum
- * is not), the output once at the end.
+ * is not; fp16 holds p / p_max * 2^7 or more: in full from 2^-21 of the largest on, in multiples of
+ * 2^-31 of it below), the output once at the end.
  *   q, out        device, [N, num_q_heads, head_dim] of the cache's type, strides as for
  *                 spec_cache_append; num_q_heads a multiple of num_kv_heads, at most 128 times
  *   parent        device int32 [N] (spec_tree_verify_greedy's), or NULL

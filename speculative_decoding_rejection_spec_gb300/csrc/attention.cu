@@ -8,8 +8,9 @@
 // One block per SM, warps by role:
 //   warps 0-3, 4-7  two softmax groups, a thread per row: S from tensor memory to registers, mask,
 //                   maximum, exponentials, P back over S.  M only moves when a row's maximum has
-//                   grown by more than 2^8 since (P stays below 2^8, exact in its sum's fp32), so
-//                   the accumulator in tensor memory is rarely rescaled.
+//                   grown by more than 2^8 since, so the accumulator in tensor memory is rarely
+//                   rescaled.  The largest P is 1 when M moves, and stays below 2^8; of fp16, whose
+//                   numbers below 2^-14 lose bits and end at 2^-24, 2^7 and 2^15.
 //   warps 10, 11 / 14, 15  load tiles of K / V, page by page, through TMA into a ring of slots; two
 //                   warps share a tile's copies: one warp cannot issue those of small pages fast enough
 //                   (a streaming loop over 16-token pages reached 3.6 TB/s with one warp issuing, 6.0
@@ -63,6 +64,10 @@ constexpr int kMaxGrid = 160;       // blocks a call may use (SMs of the device,
 constexpr int kBlockCost = 3;
 constexpr int kMinShare = 2;        // least places of a block's share (2 / 4 / 8: one token 17 / 20 / 23 us)
 constexpr float kLazy = 8.0f;       // log2 of the growth that moves a row's maximum (4 is no faster)
+// log2 of the largest weight when a row's maximum moves.  fp16: far below the maximum, where a long context
+// may have a good part of its weight, the product with V keeps 2^-21 of it in full and 2^-32 at all (with
+// weights of at most 1 to 2^8 as in bf16: 2^-14 and 2^-25).
+template <int DT> constexpr float kHead = DT == SPEC_F16 ? 7.0f : 0.0f;
 constexpr int kTmemColumns = 512;   // two groups: 128 of S (P over it), up to 128 of O
 
 // A block's share of the list: [begin(x), begin(x + 1)), in tiles of cost.
@@ -1127,10 +1132,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         mx = max3(fmaxf(top[0], top[1]), top[2], top[3]);
                     }
                     mx *= p.scale_log2;
-                    const bool grown = mx > M + kLazy;  // also from -inf
-                    const float f = grown ? ex2(M - mx) : 1.0f;
+                    const bool grown = mx > M + (kHead<DT> + kLazy);  // also from -inf
+                    const float f = grown ? ex2(M - (mx - kHead<DT>)) : 1.0f;
                     if (grown) {
-                        M = mx;
+                        M = mx - kHead<DT>;
                         l *= f;
                     }
                     if (any && __any_sync(kFull, grown)) {

@@ -1,0 +1,44 @@
+"""Small softmax weights next to a large one, over contexts that no other block shares."""
+import numpy as np
+import pytest
+
+from speculative_decoding_rejection_spec_gb300 import cache
+from test_gpu_attention import Case, built, dev  # noqa: F401 (built: the module's fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("n", [1, 150])
+def test_small_weights_of_a_long_context_count(dtype, n):
+    """One key takes nearly all of the weight, each of 65535 others e^-16.266 = 1.448 * 2^-24 of it, 0.56% together.
+    A weight is rounded once, by half a step u of its type; fp16 holds it as 2^7 or more times its ratio to the
+    largest, 1.448 * 2^-17, which is below its smallest normal: half of 2^-24 there, 2^-32 of the largest."""
+    import torch
+    L, score = 65536, -1041 / 64  # exact in both types
+    R = 400 if n == 1 else 8  # more rows than blocks: most are whole in one
+    c = Case([n], [L - n], heads=1, group=1, dim=64, page=64, dtype=dtype, seed=2, poison=False)
+    c.kv.zero_()
+    c.kv[0][..., 0] = score
+    c.kv[1][...] = 1.0
+    first = int(c.table[0, 0])
+    c.kv[0][first, 0, 0, 0] = 0.0
+    c.kv[1][first, 0] = 0.0
+    many = cache.PagedCache(c.kv[:1].cuda(), c.kv[1:].cuda(), page_table=dev(np.repeat(c.table, R, 0)),
+                            lens=dev([L - n] * R), held=dev([L // 64] * R), ref_counts=c.c.ref_counts,
+                            free_pages=c.c.free_pages, num_free=c.c.num_free)  # every request reads the same pages
+    q = torch.zeros((R * n, 1, 64), dtype=c.q.dtype, device="cuda")
+    q[:, :, 0] = 1.0
+    lse = torch.zeros((R * n, 1), device="cuda")
+    out = cache.attention(many, 0, q, dev(np.arange(R + 1) * n), scale=1.0, lse=lse).double().cpu().numpy()
+    assert cache.last_error(many) == (0, 0, -1)
+    p = np.exp(score)
+    keys = np.tile(np.arange(L - n, L), R)  # others that each row sees
+    want = (keys * p / (1 + keys * p))[:, None, None]
+    u = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -11
+    # scores, exponentials and sums in fp32 as in test_gpu_attention
+    es = (64 + 8) * 2.0 ** -23 * -score
+    tol = want * (2 * u + 2 * es + 2 * L * 2.0 ** -23 + 2.0 ** -20) + (L * 2.0 ** -32 if dtype == "f16" else 0)
+    assert (np.abs(out - want) <= tol).all(), (np.abs(out - want).max(), tol.min(), want.min())
+    z = np.log1p(keys * p)[:, None]
+    assert (np.abs(lse.double().cpu().numpy() - z) <= es + L * 2.0 ** -23 + 2.0 ** -20).all()
