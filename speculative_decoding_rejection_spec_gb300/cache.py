@@ -331,19 +331,22 @@ def attention(c: PagedCache, layer: int, q, cu_new, parent=None, scale=None, out
     stream, for KEPT_WORKSPACES streams, and a captured graph has its own).  Rows behind
     ``cu_new[B]`` are left as they were in ``out``.
     """
+    if torch._C._cuda_getDevice() != c.index:
+        with torch.cuda.device(c.index):
+            return attention(c, layer, q, cu_new, parent, scale, out, lse, workspace, stream)
     if stream is not None:
         # all of the call on that stream: what it allocates is memory of the stream that writes it (the current
         # one's may have been freed with work queued there that still uses it), and of its graph under capture
         _of_device(stream, c.index)
-        before = torch.cuda.current_stream(c.device)
-        with torch.cuda.stream(stream):
+        before = dict(zip(("stream_id", "device_index", "device_type"), torch._C._cuda_getCurrentStream(c.index)))
+        torch.cuda.set_stream(stream)
+        try:
             result = attention(c, layer, q, cu_new, parent, scale, out, lse, workspace)
+        finally:
+            torch._C._cuda_setStream(**before)
         if out is None:
-            result.record_stream(before)  # which will read it
+            result.record_stream(torch.cuda.Stream(**before))  # which will read it
         return result
-    if torch._C._cuda_getDevice() != c.index:
-        with torch.cuda.device(c.index):
-            return attention(c, layer, q, cu_new, parent, scale, out, lse, workspace)
     B = _cu(c, cu_new)
     qt, qh = _rows(c, q, None, "q")
     N, H, _ = q.shape

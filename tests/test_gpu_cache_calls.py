@@ -171,3 +171,42 @@ def test_streams_of_other_devices_are_refused():
     with pytest.raises(ValueError):
         small_cache(other)
     c.check(*c.run())
+
+
+def test_the_current_stream_stays_current():
+    """Behind a call on another stream, behind a refused one too."""
+    import torch
+    c = Case([9, 3], [50, 7], seed=1)
+    q, cu, s, mine = c.q.cuda(), dev(c.cu), torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(mine):
+        cache.attention(c.c, 0, q, cu, stream=s)
+        assert torch.cuda.current_stream() == mine
+        with pytest.raises(TypeError):
+            cache.attention(c.c, 0, q.half(), cu, stream=s)
+        assert torch.cuda.current_stream() == mine
+    torch.cuda.synchronize()
+
+
+def test_a_captured_call_on_the_given_stream_makes_its_output_there():
+    """The output of a call that only ``stream=`` captures lies in the graph's memory and follows the replays."""
+    import torch
+    c = Case([9, 3], [5000, 700], page=32, seed=1, poison=False)
+    q, cu, s = c.q.cuda(), dev(c.cu), torch.cuda.Stream()
+    want = cache.attention(c.c, 0, q, cu)
+    half = cache.attention(c.c, 0, q * 0.5, cu)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s):
+        graph.capture_begin(capture_error_mode="relaxed")
+    out = cache.attention(c.c, 0, q, cu, stream=s)
+    with torch.cuda.stream(s):
+        graph.capture_end()
+    keep = [torch.zeros_like(out) for _ in range(4)]  # what the current stream hands out is other memory
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and not any(x.any() for x in keep)
+    q.mul_(0.5)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, half)
