@@ -1,8 +1,9 @@
 """The paged key/value cache around the verify step (``include/spec_cache.h``), over torch tensors.
 
 Argument marshalling only, as in ``binding``: every operation runs in the library's CUDA kernels,
-asynchronously on a stream of the cache's device.  Errors the host can see raise; errors in device
-data are collected in the cache's error word (``last_error``).
+asynchronously on a stream of the cache's device: the current one, or ``stream=``, which then has to be
+behind the work that makes the tensors given, and they have to live until it has run.  Errors the host can
+see raise; errors in device data are collected in the cache's error word (``last_error``).
 
 One step of a serving loop:
 

@@ -34,9 +34,11 @@
 //
 // What bounds it (GB300; measured rates 6779 GB/s, 1948.5 TFLOP/s): decoding and verifying long
 // contexts, HBM (64 requests of 1 to 8191 keys, 1.03 GB: 168 us, 6.1 TB/s, nothing read twice); short
-// ones, the start of a block (the search for its share, the tables, the first tile: 10 us) and the
-// join; prompt chunks, the thread that issues the products (3200 cycles per wide tile, whose products
-// take 2120: 1.28 PFLOP/s, the tensor pipe 55% active).
+// ones, the start of a block (the search for its share and the tables: the first key is asked for after
+// 4 us of one request, 6 of 64, 8 of 128, 40 of 1024) and the join; prompt chunks, the chain of a group:
+// softmax, product with V, product with the next K, as P lies over S (1700 cycles of softmax; the issuing
+// thread waits 950 of some 3500 cycles per wide tile for P; the products alone take 2120: 1.27 PFLOP/s in
+// the kernel, the tensor pipe 55% active).
 #include <algorithm>
 
 #include <cuda.h>
