@@ -142,7 +142,7 @@ class PagedCache:
         self.dtype, self.heads, self.dim = k.dtype, H, D
         # attention's, by stream: (rows, workspace); the lock is held from the look to the launches, as a call's
         # two kernels and their workspace belong together whichever host threads call
-        self.workspaces, self.lock = {}, threading.Lock()
+        self.workspaces, self.lock = {}, threading.RLock()
 
 
 def _code(t) -> int:

@@ -1073,7 +1073,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     if (lane == 0)
                         cache_error(c.error, SPEC_DEVERR_TREE, item.r);
                 } else if (on && turns > 0) {
-                    for (int at = token; at >= 0; at = par[at]) {
+                    // (ends whatever stands in par[]: the array may be written while other warps read it)
+                    for (int at = token; at >= 0; at = min(par[at], at - 1)) {
 #pragma unroll
                         for (int j = 0; j < kMaxTree / 32; ++j)
                             bits[j] |= at / 32 == j ? 1u << (at & 31) : 0u;
@@ -1134,7 +1135,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         mx = max3(fmaxf(top[0], top[1]), top[2], top[3]);
                     }
                     mx *= p.scale_log2;
-                    const bool grown = mx > M + (kHead<DT> + kLazy);  // also from -inf
+                    // also from -inf; of the difference, which is exact: of scores from 2^23 on a sum may round up
+                    // to twice the limit, and fp16's weights end at 2^16
+                    const bool grown = mx - M > kHead<DT> + kLazy;
                     const float f = grown ? ex2(M - (mx - kHead<DT>)) : 1.0f;
                     if (grown) {
                         M = mx - kHead<DT>;

@@ -42,3 +42,47 @@ def test_small_weights_of_a_long_context_count(dtype, n):
     assert (np.abs(out - want) <= tol).all(), (np.abs(out - want).max(), tol.min(), want.min())
     z = np.log1p(keys * p)[:, None]
     assert (np.abs(lse.double().cpu().numpy() - z) <= es + L * 2.0 ** -23 + 2.0 ** -20).all()
+
+
+def shared(c, requests, **kw):
+    """Attention of `requests` requests of the case's one, over the same pages: more rows than the device has
+    blocks, so that most rows are whole in one."""
+    import torch
+    pages = int(c.c.held[0])
+    many = cache.PagedCache(c.kv[:1].cuda(), c.kv[1:].cuda(), page_table=dev(np.repeat(c.table, requests, 0)),
+                            lens=dev(c.ctx * requests), held=dev([pages] * requests), ref_counts=c.c.ref_counts,
+                            free_pages=c.c.free_pages, num_free=c.c.num_free)
+    n = c.n[0]
+    q = c.q.cuda().repeat(requests, 1, 1)
+    lse = torch.zeros(q.shape[:2], device="cuda")
+    out = cache.attention(many, 0, q, dev(np.arange(requests + 1) * n), lse=lse, **kw)
+    assert cache.last_error(many) == (0, 0, -1)
+    return out, lse
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("base", [1024, 1536, 2560, 4096, 5120, 7168, 12288])
+@pytest.mark.parametrize("step", [1, 2, 4, 8])
+def test_scores_whose_steps_are_whole_exponents(dtype, base, step):
+    """Scores of 2^23 to 2^27, whose steps in fp32 are 1 to 8: sums, differences and the limits that they are held
+    against round to those, and no weight may leave its type's range.  Outputs are averages of the values."""
+    import torch
+    L = 4096
+    c = Case([1], [L - 1], heads=1, group=4, dim=64, page=64, dtype=dtype, seed=3, poison=False)
+    rows = torch.zeros((L // 64, 64, 64))
+    rows[..., 0] = float(base)
+    rows[..., 1] = (torch.arange(L) // 128 * step).float().view(L // 64, 64)  # every tile's maximum rises a little
+    pages = torch.from_numpy(c.table[0, :L // 64].astype(np.int64))
+    c.kv.zero_()
+    c.kv[0][pages, :, 0] = rows.to(c.kv.dtype)
+    c.kv[1][...] = 1 + torch.rand(c.kv[1].shape, generator=torch.Generator().manual_seed(base)).to(c.kv.dtype)
+    c.q.zero_()
+    c.q[:, :, 0] = 8192.0
+    c.q[:, :, 1] = torch.arange(4) + 1.0
+    out, lse = shared(c, 400, scale=1.0)
+    # a weight and its rounded one differ by half a step u, so do the output and its rounded one; sums in fp32
+    u = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -11
+    off = 2 * u + 2 * L * 2.0 ** -23
+    out = out.double().cpu().numpy()
+    assert (out >= 1 - 2 * off).all() and (out <= 2 + 4 * off).all(), (out.min(), out.max())
+    assert lse.isfinite().all()
