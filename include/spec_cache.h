@@ -188,6 +188,8 @@ spec_status spec_cache_release(const spec_cache *cache, const int32_t *keep_lens
  *   scale         finite, > 0
  *   lse           device fp32 [N, num_q_heads], or NULL
  *   workspace     spec_attention_workspace_size() bytes; contents need no initialisation
+ * Scores scale * (q . k_t) are held in fp32; finite results are certain for scores below 1.8e8 (fp16)
+ * and 1.4e9 (bf16) in size, where a step of fp32 is a factor of 2^16 and 2^128 between weights.
  * page_size is a multiple of 8, head_dim at most SPEC_ATTENTION_MAX_HEAD_DIM and N * num_q_heads
  * below 2^30 (SPEC_ERR_UNSUPPORTED otherwise).  The keys and values of all lens[r] + n_r tokens are
  * read, from the pages held (SPEC_DEVERR_LENGTH where those contain fewer); rows behind them are not

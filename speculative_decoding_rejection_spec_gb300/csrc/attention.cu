@@ -1135,8 +1135,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         mx = max3(fmaxf(top[0], top[1]), top[2], top[3]);
                     }
                     mx *= p.scale_log2;
-                    // also from -inf; of the difference, which is exact: of scores from 2^23 on a sum may round up
-                    // to twice the limit, and fp16's weights end at 2^16
+                    // Also from -inf; of the difference, which is exact: of scores from 2^23 on a sum may round up
+                    // to twice the limit, and fp16's weights end at 2^16.  (The exponents below are of products
+                    // rounded once, with M taken off, so up to half a step of mx off: with the limit, which the
+                    // difference then keeps by as much, 15.5 at most for products below 2^28.)
                     const bool grown = mx - M > kHead<DT> + kLazy;
                     const float f = grown ? ex2(M - (mx - kHead<DT>)) : 1.0f;
                     if (grown) {

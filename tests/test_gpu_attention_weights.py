@@ -86,3 +86,32 @@ def test_scores_whose_steps_are_whole_exponents(dtype, base, step):
     out = out.double().cpu().numpy()
     assert (out >= 1 - 2 * off).all() and (out <= 2 + 4 * off).all(), (out.min(), out.max())
     assert lse.isfinite().all()
+
+
+@pytest.mark.parametrize("dtype,q,k", [("f16", 8192, 14000), ("f16", 8192, 20000), ("f16", -8192, 18000),
+                                       ("f16", 4096, 43000), ("bf16", 2 ** 12, 3 * 2 ** 15), ("bf16", 2 ** 14, 5 * 2 ** 14),
+                                       ("bf16", -2 ** 14, 5 * 2 ** 13)])
+def test_scores_whose_steps_are_many_exponents(dtype, q, k):
+    """Scores up to the largest that the header names, 2^28 (fp16) and 2^31 (bf16) over log2 e: their steps are 16
+    and 128 exponents.  Keys of one score share the weight, whatever it is."""
+    import torch
+    L = 1536
+    c = Case([1], [L - 1], heads=1, group=4, dim=64, page=64, dtype=dtype, seed=3, poison=False)
+    scale = torch.ones(L)
+    scale[L // 3:2 * L // 3] = 0.75 if q > 0 else 1.25  # the lower scores, behind the first: weights of zero
+    pages = torch.from_numpy(c.table[0, :L // 64].astype(np.int64))
+    c.kv.zero_()
+    c.kv[0][pages, :, 0, 0] = (k * scale).view(L // 64, 64).to(c.kv.dtype)
+    v = torch.randn((L, 64), generator=torch.Generator().manual_seed(7)).to(c.kv.dtype)
+    c.kv[1][pages, :, 0] = v.view(L // 64, 64, 64)
+    c.q.zero_()
+    c.q[:, :, 0] = float(q)
+    out, lse = shared(c, 400, scale=1.0)
+    top = v[scale == 1].double()
+    want, mass = top.mean(0).numpy(), top.abs().mean(0).numpy()
+    u = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -11
+    tol = u * np.abs(want) + mass * (u + 2 * L * 2.0 ** -23 + 2.0 ** -20)
+    out = out.double().cpu().numpy()
+    assert (np.abs(out - want) <= tol).all(), np.abs(out - want).max()
+    score = float(c.q[0, 0, 0]) * float((k * scale[:1]).to(c.kv.dtype)[0])
+    assert (np.abs(lse.double().cpu().numpy() - score) <= 2.0 ** -21 * abs(score)).all()
