@@ -1135,11 +1135,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         mx = max3(fmaxf(top[0], top[1]), top[2], top[3]);
                     }
                     mx *= p.scale_log2;
-                    // Also from -inf; of the difference, which is exact: of scores from 2^23 on a sum may round up
-                    // to twice the limit, and fp16's weights end at 2^16.  (The exponents below are of products
-                    // rounded once, with M taken off, so up to half a step of mx off: with the limit, which the
-                    // difference then keeps by as much, 15.5 at most for products below 2^28.)
-                    const bool grown = mx - M > kHead<DT> + kLazy;
+                    // Also from -inf.  fp16, whose weights end at 2^16: of the difference, which is exact, as a sum
+                    // may round up to twice the limit from 2^23 on.  (The exponents below are of products rounded
+                    // once, with M taken off, so up to half a step of mx off: with the limit, which the difference
+                    // then keeps by as much, 15.5 at most for products below 2^28.)  bf16 has the range for the
+                    // sum (prompt chunks 326.2 us, 328.3 by the difference).
+                    const bool grown = DT == SPEC_F16 ? mx - M > kHead<DT> + kLazy : mx > M + kLazy;
                     const float f = grown ? ex2(M - (mx - kHead<DT>)) : 1.0f;
                     if (grown) {
                         M = mx - kHead<DT>;
