@@ -12,7 +12,10 @@
  *   spec_cache_commit    the accepted tokens stay: the length advances by accepted + 1; a tree's
  *                        accepted path, scattered over the step's rows, is moved together
  *   spec_cache_release   (when wanted) pages behind the committed tokens, or of finished requests
- * and spec_cache_fork makes a request that shares another's committed tokens.
+ * and spec_cache_fork makes a request that shares another's committed tokens.  In place of the two calls per layer:
+ * spec_cache_append_rotated turns keys and queries by their positions on the way; spec_attention_window sees the last
+ * positions and the first ones only; spec_attention_shared reads the pages that several requests share once for all
+ * (spec_cache_share finds them).
  *
  * The rollback of rejected drafts ("第12章 投机解码：以小博大" §12.3.4: the next step starts
  * accepted + 1 positions further) is the commit: rows of rejected tokens lie behind the committed
@@ -66,8 +69,10 @@ extern "C" {
 
 /* Largest draft tree (nodes of one request, the root included). */
 #define SPEC_CACHE_MAX_TREE 128
-/* Largest head dimension of spec_attention(). */
+/* Largest head dimension of spec_attention(), spec_attention_window() and spec_attention_shared(). */
 #define SPEC_ATTENTION_MAX_HEAD_DIM 128
+/* Largest head dimension of spec_cache_append_rotated(). */
+#define SPEC_ROTATION_MAX_HEAD_DIM 256
 
 /*
  * A cache.  Keys and values are num_layers x num_pages pages of page_size tokens of num_kv_heads
@@ -140,6 +145,41 @@ spec_status spec_cache_append(const spec_cache *cache, int32_t layer, const void
                               int64_t v_head_stride, const int32_t *cu_new, int32_t B, int64_t N, void *stream);
 
 /*
+ * The rotation of positions: the first `dim` elements of a head form dim / 2 pairs, elements i and dim / 2 + i
+ * (neighbours == 0) or 2 i and 2 i + 1; at position p a pair (a, b) becomes
+ *   (a cos - b sin, b cos + a sin),  cos = table[p * row_stride + i], sin = table[p * row_stride + dim / 2 + i]
+ * and the elements behind stay as they are.
+ *   table       device fp32, 16-byte aligned, `positions` rows row_stride elements apart (>= dim and a multiple of
+ *               4; not looked at for one row)
+ *   dim         even, at most head_dim; a multiple of 16, or of 8 with neighbours (SPEC_ERR_UNSUPPORTED otherwise)
+ */
+typedef struct spec_rotation {
+    const float *table;
+    int64_t row_stride;
+    int32_t positions, dim, neighbours;
+} spec_rotation;
+
+/*
+ * spec_cache_append() with the keys turned by their positions on the way, and the queries of the same tokens: new
+ * token i of request r stands at position lens[r] + i (parent == NULL) or, as node i of a tree (parent given,
+ * spec_tree_verify_greedy's), at lens[r] + its depth, where a commit moves it.  Its key and value are written to
+ * place lens[r] + i.  Computed in fp32, rounded to the cache's type once.
+ *   q, q_out  device, [N, num_q_heads, head_dim] of the cache's type, strides as for spec_cache_append(); q_out may
+ *             be q (with its strides); num_q_heads == 0: keys and values alone
+ * The positions lens[r] .. lens[r] + n_r - 1 lie in the table (SPEC_DEVERR_LENGTH otherwise, and the request is
+ * skipped, as it is with a malformed tree or one of more than SPEC_CACHE_MAX_TREE nodes, SPEC_DEVERR_TREE).  A row that
+ * spec_cache_append() would skip is skipped in q_out too.  head_dim is at most SPEC_ROTATION_MAX_HEAD_DIM
+ * (SPEC_ERR_UNSUPPORTED otherwise).  `rotation` is read during the call only.
+ */
+spec_status spec_cache_append_rotated(const spec_cache *cache, int32_t layer, const void *k_new,
+                                      int64_t k_token_stride, int64_t k_head_stride, const void *v_new,
+                                      int64_t v_token_stride, int64_t v_head_stride, const void *q,
+                                      int64_t q_token_stride, int64_t q_head_stride, int32_t num_q_heads, void *q_out,
+                                      int64_t out_token_stride, int64_t out_head_stride, const int32_t *cu_new,
+                                      int32_t B, int64_t N, const int32_t *parent, const spec_rotation *rotation,
+                                      void *stream);
+
+/*
  * The step's outcome: lens[r] advances by num_accepted[r] + 1 where n_r > 0 and num_accepted[r] >=
  * 0 (-1, a request reported invalid, commits nothing), and where the pages held contain the step's
  * tokens (SPEC_DEVERR_LENGTH otherwise, and the length stays).  With a tree, the accepted path from
@@ -203,6 +243,49 @@ spec_status spec_attention(const spec_cache *cache, int32_t layer, const void *q
                            const int32_t *parent, float scale, void *out, int64_t out_token_stride,
                            int64_t out_head_stride, float *lse, void *workspace, size_t workspace_bytes,
                            void *stream);
+
+/*
+ * spec_attention() of which a row at position p sees only the keys at positions above p - window (its own among
+ * them) and those of the first `sinks` positions.  New token i of a chain stands at position lens[r] + i, node i of
+ * a tree at lens[r] + its depth.  Keys that no row of a request sees are not read, nor are their table entries.
+ *   window  >= 1;  sinks  >= 0
+ * Everything else, the workspace too, is as for spec_attention(): all lens[r] + n_r tokens lie in the pages held.
+ */
+spec_status spec_attention_window(const spec_cache *cache, int32_t layer, const void *q, int64_t q_token_stride,
+                                  int64_t q_head_stride, int32_t num_q_heads, const int32_t *cu_new, int32_t B,
+                                  int64_t N, const int32_t *parent, float scale, int32_t window, int32_t sinks,
+                                  void *out, int64_t out_token_stride, int64_t out_head_stride, float *lse,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The plan of spec_attention_shared(): for each of the requests 0 .. B-1 four numbers, the first request of its group
+ * and the end (one more than the last), the tokens that all of the group share, and 0.  Two neighbouring requests
+ * are linked when their committed tokens begin with the same pages, whole ones, of min_tokens tokens or more (>= 0,
+ * and at least one page); a group is a run of links, and shares the tokens of its shortest link.  A request of no link
+ * is a group of its own that shares 0 tokens, and so is, with SPEC_DEVERR_LENGTH, one whose pages held do not contain
+ * its tokens.
+ *   shared  device int32 [B, 4], 16-byte aligned
+ * The plan holds for the steps that follow, in every layer, as long as the requests keep their first pages: committed
+ * tokens may be added, and a request is planned anew when it was released or truncated.  It may also be written by the
+ * caller: `tokens` a multiple of page_size, the same three numbers for every request of a group.
+ * Uses the cache's scratch: ordered by the caller like the calls that change a cache.
+ */
+spec_status spec_cache_share(const spec_cache *cache, int32_t B, int32_t min_tokens, int32_t *shared, void *stream);
+
+/*
+ * spec_attention() that reads the tokens which the requests of a group share once for all of them, from the pages of
+ * its first request: same results, but for the order of sums.  Entries of the plan that the requests do not fit (a
+ * group out of range or of one request, fewer committed tokens than it shares, another entry for its first request)
+ * count as no group; whether the pages are in fact the same is not looked at.
+ *   shared     device int32 [B, 4], 16-byte aligned, as spec_cache_share() writes it
+ *   workspace  spec_attention_shared_workspace_size() bytes; contents need no initialisation
+ */
+size_t spec_attention_shared_workspace_size(const spec_cache *cache, int32_t num_q_heads, int32_t B, int64_t N);
+spec_status spec_attention_shared(const spec_cache *cache, int32_t layer, const void *q, int64_t q_token_stride,
+                                  int64_t q_head_stride, int32_t num_q_heads, const int32_t *cu_new, int32_t B,
+                                  int64_t N, const int32_t *parent, float scale, const int32_t *shared, void *out,
+                                  int64_t out_token_stride, int64_t out_head_stride, float *lse, void *workspace,
+                                  size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

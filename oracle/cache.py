@@ -186,3 +186,53 @@ def attention(q, k, v, seen, scale):
     reach = np.where(seen[:, None, :], np.einsum("igd,td->igt", np.abs(q), np.abs(k)) * scale, 0).max(-1)
     return (np.einsum("igt,td->igd", p, v), (top + np.log(total))[..., 0],
             np.einsum("igt,td->igd", p, np.abs(v)), reach)
+
+
+def depths(parent):
+    """Depth of every node of a tree."""
+    d = np.zeros(len(parent), np.int64)
+    for i in range(1, len(parent)):
+        d[i] = d[parent[i]] + 1
+    return d
+
+
+def visible_window(n, ctx, window, sinks, parent=None):
+    """[n, ctx + n] which keys each new token sees whose position is among the last `window` up to its own, or one of
+    the first `sinks`; a tree's nodes stand at ctx + their depth."""
+    new = np.arange(n) if parent is None else depths(parent)
+    place = np.concatenate([np.arange(ctx), ctx + new])
+    return visible(n, ctx, parent) & ((place[None, :] > (ctx + new)[:, None] - window) | (place < sinks)[None, :])
+
+
+def share_plan(table, lens, held, page_size, min_tokens):
+    """Per request (first, end, tokens, 0) of its group, one request after the other; and the requests with errors."""
+    R, MP = len(lens), max((len(row) for row in table), default=0)
+    good = [0 <= held[r] <= MP and 0 <= lens[r] <= held[r] * page_size for r in range(R)]
+    plan, first = [], 0
+    link = [0] * R
+    for r in range(1, R):
+        full = min(lens[r], lens[r - 1]) // page_size if good[r] and good[r - 1] else 0
+        while link[r] < full and table[r][link[r]] == table[r - 1][link[r]]:
+            link[r] += 1
+        link[r] *= page_size
+        if link[r] < max(min_tokens, 1):
+            link[r] = 0
+    while first < R:
+        end = first + 1
+        while end < R and link[end]:
+            end += 1
+        plan += [(first, end, min(link[first + 1:end], default=0), 0)] * (end - first)
+        first = end
+    return np.array(plan, np.int32).reshape(R, 4), [r for r in range(R) if not good[r]]
+
+
+def rotate(x, table, positions, interleaved):
+    """x [N, heads, D] turned by the table's rows at `positions` [N], in float64."""
+    x = np.array(x, np.float64)
+    row = np.asarray(table, np.float64)[np.asarray(positions, np.int64)]
+    half = row.shape[1] // 2
+    c, s = row[:, None, :half], row[:, None, half:]
+    a, b = (slice(0, 2 * half, 2), slice(1, 2 * half, 2)) if interleaved else (slice(0, half), slice(half, 2 * half))
+    p, q = x[..., a].copy(), x[..., b].copy()
+    x[..., a], x[..., b] = p * c - q * s, q * c + p * s
+    return x

@@ -14,6 +14,10 @@ One step of a serving loop:
     tokens, accepted = binding.sample(logits, ...)                  # or binding.tree_verify_greedy
     cache.commit(c, cu_new, accepted)                               # trees: parent=, last_node=
 
+In place of ``append``, ``append_rotated`` turns keys and queries by their positions on the way; attention over the
+last positions alone takes ``window=`` and ``sinks=``, and requests that share a prefix (forked ones) have it read
+once for all with ``shared=cache.share(c)``.
+
 ``cu_new`` is a device int32 [B + 1]; row ``cu_new[r] + i`` of a step's tensors is new token i of
 request r.  Chains of k_r drafts are k_r + 1 new tokens: ``cu_new = cu_num_draft + arange(B + 1)``.
 """
@@ -31,12 +35,15 @@ from .binding import SpecRejectError, load as _load_library
 F16, BF16 = 2, 1
 MAX_TREE = 128
 ATTENTION_MAX_HEAD_DIM = 128
+ROTATION_MAX_HEAD_DIM = 256
 KEPT_WORKSPACES = 8  # of attention, per cache: those of the streams first seen last
 DEVERR_PAGE, DEVERR_CAPACITY, DEVERR_LENGTH, DEVERR_FORK = 32, 64, 128, 256
 
 EXPORTED = [
     "spec_cache_scratch_size", "spec_cache_init", "spec_cache_error", "spec_cache_reserve", "spec_cache_append",
     "spec_cache_commit", "spec_cache_fork", "spec_cache_release", "spec_attention_workspace_size", "spec_attention",
+    "spec_cache_append_rotated", "spec_attention_window", "spec_cache_share", "spec_attention_shared_workspace_size",
+    "spec_attention_shared",
 ]
 
 _P, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
@@ -49,6 +56,11 @@ class SpecCache(ctypes.Structure):
                 ("page_stride", _i64), ("token_stride", _i64), ("head_stride", _i64), ("page_table", _P),
                 ("table_stride", _i64), ("num_requests", _i32), ("max_pages", _i32), ("lens", _P), ("held", _P),
                 ("ref_counts", _P), ("free_pages", _P), ("num_free", _P), ("error", _P), ("scratch", _P)]
+
+
+class Rotation(ctypes.Structure):
+    """spec_rotation."""
+    _fields_ = [("table", _P), ("row_stride", _i64), ("positions", _i32), ("dim", _i32), ("neighbours", _i32)]
 
 
 _lib = None
@@ -71,7 +83,16 @@ def load():
             ("spec_cache_release", ctypes.c_int, [C, _P, _i32, _P]),
             ("spec_attention_workspace_size", _sz, [C, _i32, _i32, _i64]),
             ("spec_attention", ctypes.c_int, [C, _i32, _P, _i64, _i64, _i32, _P, _i32, _i64, _P, ctypes.c_float, _P,
-                                              _i64, _i64, _P, _P, _sz, _P])):
+                                              _i64, _i64, _P, _P, _sz, _P]),
+            ("spec_cache_append_rotated", ctypes.c_int, [C, _i32, _P, _i64, _i64, _P, _i64, _i64, _P, _i64, _i64, _i32,
+                                                         _P, _i64, _i64, _P, _i32, _i64, _P,
+                                                         ctypes.POINTER(Rotation), _P]),
+            ("spec_attention_window", ctypes.c_int, [C, _i32, _P, _i64, _i64, _i32, _P, _i32, _i64, _P, ctypes.c_float,
+                                                     _i32, _i32, _P, _i64, _i64, _P, _P, _sz, _P]),
+            ("spec_cache_share", ctypes.c_int, [C, _i32, _i32, _P, _P]),
+            ("spec_attention_shared_workspace_size", _sz, [C, _i32, _i32, _i64]),
+            ("spec_attention_shared", ctypes.c_int, [C, _i32, _P, _i64, _i64, _i32, _P, _i32, _i64, _P, ctypes.c_float,
+                                                     _P, _P, _i64, _i64, _P, _P, _sz, _P])):
         f = getattr(lib, name)
         f.restype, f.argtypes = result, args
     _lib = lib
@@ -154,6 +175,11 @@ def _int32(t, shape, name, device, contiguous=True):
         raise TypeError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
+
+
+def _clamped(x):
+    """An integer as the library takes it: what lies outside of int32 is as good as its ends, or refused as -1 is."""
+    return max(-1, min(x, 2 ** 31 - 1))
 
 
 def _ptr(t):
@@ -252,6 +278,80 @@ def append(c: PagedCache, layer: int, k_new, v_new, cu_new, stream=None):
           cu_new.data_ptr(), B, N)
 
 
+def rotation_table(positions: int, dim: int, base: float = 10000.0, device="cuda"):
+    """The table of ``append_rotated`` for positions 0 .. positions - 1: pair i turns by p * base ** (-2 i / dim)
+    radians at position p.  float32 [positions, dim], cosines before sines, computed in 64 bits.  Scaled or otherwise
+    spaced rotations are tables of the caller's making."""
+    half = dim // 2
+    speed = base ** (-torch.arange(half, dtype=torch.float64, device=device) / half)
+    angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * speed
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+def append_rotated(c: PagedCache, layer: int, q, k_new, v_new, cu_new, rotation, parent=None, interleaved=False,
+                   out=None, stream=None):
+    """``append`` with the keys turned by their positions on the way; returns the queries q [N, q_heads, head_dim] of
+    the same tokens, turned alike (spec_cache_append_rotated).
+
+    ``rotation`` (float32 [positions, dim], ``rotation_table``) holds dim / 2 cosines and as many sines per position;
+    it turns the first ``dim`` elements of each head, pairs of elements i and dim / 2 + i, or of neighbours with
+    ``interleaved``.  Chains stand at positions lens + i, with ``parent`` (int32 [N]) the nodes of draft trees at
+    lens + depth.  ``out`` may be q itself; rows of requests with errors, and behind ``cu_new[B]``, are left as they
+    were in it.  ``q`` may be None.  A result made for a call on another ``stream`` is memory of that stream, kept for
+    the current one.
+    """
+    if stream is not None:
+        return _on_stream(c, stream, out is None and q is not None, append_rotated, c, layer, q, k_new, v_new, cu_new,
+                          rotation, parent, interleaved, out)
+    B = _cu(c, cu_new)
+    kt, kh = _rows(c, k_new, c.heads, "k_new")
+    vt, vh = _rows(c, v_new, c.heads, "v_new")
+    N = k_new.shape[0]
+    if v_new.shape[0] != N or (q is not None and q.shape[0] != N):
+        raise ValueError("q, k_new and v_new must have the same rows")
+    if rotation.dtype is not torch.float32 or rotation.dim() != 2 or (rotation.stride(1) != 1 and rotation.numel()):
+        raise TypeError("rotation must be a float32 tensor [positions, dim] with unit stride inside")
+    if rotation.device != c.device:
+        raise ValueError(f"rotation must be on {c.device}")
+    if parent is not None:
+        _int32(parent, (N,), "parent", c.device)
+    H = qt = qh = ot = oh = 0
+    if q is not None:
+        qt, qh = _rows(c, q, None, "q")
+        H = q.shape[1]
+        if out is None:
+            with torch.cuda.device(c.index):
+                out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            ot, oh = H * c.dim, c.dim
+        elif out.shape != q.shape:
+            raise ValueError("out must have the shape of q")
+        else:
+            ot, oh = _rows(c, out, H, "out")
+    elif out is not None:
+        raise ValueError("out needs q")
+    turn = Rotation(table=rotation.data_ptr(), row_stride=rotation.stride(0), positions=rotation.shape[0],
+                    dim=rotation.shape[1], neighbours=int(interleaved))
+    _call(c, "spec_cache_append_rotated", None, layer, k_new.data_ptr(), kt, kh, v_new.data_ptr(), vt, vh, _ptr(q),
+          qt, qh, H, _ptr(out), ot, oh, cu_new.data_ptr(), B, N, _ptr(parent), ctypes.byref(turn))
+    return out
+
+
+def share(c: PagedCache, min_tokens: int = 256, B: int | None = None, out=None, stream=None):
+    """Which of the requests 0 .. B-1 (None: all) share the pages of a prefix of ``min_tokens`` tokens or more with
+    their neighbours (spec_cache_share): int32 [B, 4], per request the first of its group, the end, the tokens that the
+    group shares, 0.  The plan of ``attention(shared=...)`` for all layers and steps in which the requests keep these
+    pages; ordered like the calls that change the cache."""
+    if stream is not None:
+        return _on_stream(c, stream, out is None, share, c, min_tokens, B, out)
+    B = int(c.lens.shape[0]) if B is None else int(B)
+    if out is None:
+        with torch.cuda.device(c.index):
+            out = torch.empty((max(B, 0), 4), dtype=torch.int32, device=c.device)
+    _int32(out, (B, 4), "out", c.device)
+    _call(c, "spec_cache_share", None, B, _clamped(min_tokens), out.data_ptr())
+    return out
+
+
 def commit(c: PagedCache, cu_new, num_accepted, parent=None, last_node=None, out_lens=None, stream=None):
     """Advances lengths by num_accepted + 1; with a tree (``parent`` and ``last_node``) moves the
     accepted path's rows together (spec_cache_commit)."""
@@ -295,7 +395,26 @@ def attention_workspace_size(c: PagedCache, num_q_heads: int, B: int, N: int) ->
     return int(n)
 
 
-def _workspace(c, H, B, N):
+def _on_stream(c, stream, made, function, *args):
+    """A call with ``stream`` current: what it allocates is memory of the stream that writes it (the current one's may
+    have been freed with work queued there that still uses it), and of its graph under capture.  ``made``: the result
+    is new, and the stream that was current will read it."""
+    if torch._C._cuda_getDevice() != c.index:
+        with torch.cuda.device(c.index):
+            return _on_stream(c, stream, made, function, *args)
+    _of_device(stream, c.index)
+    before = dict(zip(("stream_id", "device_index", "device_type"), torch._C._cuda_getCurrentStream(c.index)))
+    torch.cuda.set_stream(stream)
+    try:
+        result = function(*args)
+    finally:
+        torch._C._cuda_setStream(**before)
+    if made:
+        result.record_stream(torch.cuda.Stream(**before))
+    return result
+
+
+def _workspace(c, H, B, N, shared=False):
     """A workspace for one call on the current stream (of the cache's device, the current one): that of the
     stream, kept with the cache (its calls run one after the other), for KEPT_WORKSPACES streams; under
     capture a new one from the graph's memory, as graphs may run at the same time.  The caller holds the
@@ -304,9 +423,16 @@ def _workspace(c, H, B, N):
     handle = torch._C._cuda_getCurrentRawStream(c.index)
     capturing = torch._C._cuda_isCurrentStreamCapturing()
     kept = None if capturing else c.workspaces.get(handle)
-    if kept is not None and kept[0] >= rows:
-        return kept[1]
-    size = _lib.spec_attention_workspace_size(c.ref, H, B, N)
+    if shared:  # its size grows with N * H, too
+        size = _lib.spec_attention_shared_workspace_size(c.ref, H, B, N)
+        if kept is not None and kept[1].numel() >= size:
+            return kept[1]
+    else:
+        if kept is not None and kept[0] >= rows:
+            return kept[1]
+        size = _lib.spec_attention_workspace_size(c.ref, H, B, N)
+    if kept is not None:
+        rows, size = max(rows, kept[0]), max(size, kept[1].numel())
     workspace = torch.empty(size, dtype=torch.uint8, device=c.device)
     if size and not capturing:
         c.workspaces.pop(handle, None)
@@ -320,7 +446,7 @@ _no_lock = contextlib.nullcontext()
 
 
 def attention(c: PagedCache, layer: int, q, cu_new, parent=None, scale=None, out=None, lse=None, workspace=None,
-              stream=None):
+              stream=None, window=None, sinks=0, shared=None):
     """Attention of the new tokens q [N, q_heads, head_dim] over the cache (spec_attention); returns
     out, like q.
 
@@ -331,23 +457,18 @@ def attention(c: PagedCache, layer: int, q, cu_new, parent=None, scale=None, out
     same time and calls of several host threads need one each (without one, the cache keeps one per
     stream, for KEPT_WORKSPACES streams, and a captured graph has its own).  Rows behind
     ``cu_new[B]`` are left as they were in ``out``.
+
+    ``window`` (>= 1): a row sees the last ``window`` positions, its own among them, and the first ``sinks`` ones
+    (spec_attention_window; positions of a tree's nodes are by depth).  ``shared`` (int32 [B, 4], ``share``): requests
+    whose prefix lies in the same pages have it read once for all (spec_attention_shared).  Not both: what lies behind
+    a window is read by few requests, if any.
     """
     if torch._C._cuda_getDevice() != c.index:
         with torch.cuda.device(c.index):
-            return attention(c, layer, q, cu_new, parent, scale, out, lse, workspace, stream)
+            return attention(c, layer, q, cu_new, parent, scale, out, lse, workspace, stream, window, sinks, shared)
     if stream is not None:
-        # all of the call on that stream: what it allocates is memory of the stream that writes it (the current
-        # one's may have been freed with work queued there that still uses it), and of its graph under capture
-        _of_device(stream, c.index)
-        before = dict(zip(("stream_id", "device_index", "device_type"), torch._C._cuda_getCurrentStream(c.index)))
-        torch.cuda.set_stream(stream)
-        try:
-            result = attention(c, layer, q, cu_new, parent, scale, out, lse, workspace)
-        finally:
-            torch._C._cuda_setStream(**before)
-        if out is None:
-            result.record_stream(torch.cuda.Stream(**before))  # which will read it
-        return result
+        return _on_stream(c, stream, out is None, attention, c, layer, q, cu_new, parent, scale, out, lse, workspace,
+                          None, window, sinks, shared)
     B = _cu(c, cu_new)
     qt, qh = _rows(c, q, None, "q")
     N, H, _ = q.shape
@@ -366,10 +487,20 @@ def attention(c: PagedCache, layer: int, q, cu_new, parent=None, scale=None, out
     if workspace is not None and (workspace.dtype is not torch.uint8 or workspace.device != c.device or
                                   not workspace.is_contiguous()):
         raise TypeError(f"workspace must be a contiguous uint8 tensor on {c.device}")
+    name, more = "spec_attention", ()
+    if window is not None:
+        if shared is not None:
+            raise ValueError("attention takes a window or a plan of shared prefixes, not both")
+        name, more = "spec_attention_window", (_clamped(window), _clamped(sinks))
+    elif sinks:
+        raise ValueError("sinks need a window")
+    elif shared is not None:
+        _int32(shared, (B, 4), "shared", c.device)
+        name, more = "spec_attention_shared", (shared.data_ptr(),)
     with c.lock if workspace is None else _no_lock:
         if workspace is None:
-            workspace = _workspace(c, H, B, N)
-        _call(c, "spec_attention", None, layer, q.data_ptr(), qt, qh, H, cu_new.data_ptr(), B, N, _ptr(parent),
-              c.dim ** -0.5 if scale is None else scale, out.data_ptr(), ot, oh, _ptr(lse), workspace.data_ptr(),
-              workspace.numel())
+            workspace = _workspace(c, H, B, N, shared is not None)
+        _call(c, name, None, layer, q.data_ptr(), qt, qh, H, cu_new.data_ptr(), B, N, _ptr(parent),
+              c.dim ** -0.5 if scale is None else scale, *more, out.data_ptr(), ot, oh, _ptr(lse),
+              workspace.data_ptr(), workspace.numel())
     return out

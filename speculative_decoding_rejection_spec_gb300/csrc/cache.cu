@@ -12,19 +12,6 @@ namespace specrej {
 namespace {
 
 constexpr int kBookThreads = 1024;  // the one block of reserve
-constexpr int kCopyThreads = 256;
-
-// Whether cu[0 .. B] starts at 0, does not decrease and ends within N rows; the whole block.
-__device__ __forceinline__ bool block_layout_ok(const int32_t *cu, int B, int64_t N)
-{
-    bool bad = false;
-    for (int r = threadIdx.x; r <= B; r += blockDim.x) {
-        const int32_t c = cu[r];
-        bad |= r == 0 ? c != 0 : cu[r - 1] > c;
-        bad |= c > N;
-    }
-    return !__syncthreads_or(bad);
-}
 
 // Exclusive prefix sum over the block; *total is the block's sum.
 template <int THREADS> __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t *total)
@@ -49,22 +36,6 @@ template <int THREADS> __device__ __forceinline__ int64_t block_scan(int64_t x, 
     }
     *total = all;
     return before + incl - x;
-}
-
-// Whether this block is the last of `blocks` to come here; what the others wrote is then visible.
-__device__ __forceinline__ bool last_block(int32_t *ticket, int blocks)
-{
-    __shared__ bool last;
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        last = atomicAdd(ticket, 1) == blocks - 1;
-        if (last)
-            *ticket = 0;
-    }
-    __syncthreads();
-    __threadfence();
-    return last;
 }
 
 __global__ void __launch_bounds__(kCopyThreads) init_kernel(CacheView c)
@@ -688,49 +659,6 @@ __global__ void __launch_bounds__(kReleaseThreads) release_kernel(CacheView c, c
             cache_error(c.error, SPEC_DEVERR_PAGE, -1);
     }
 }
-
-constexpr int kMaxDevices = 64;
-
-// SMs of the current device.
-cudaError_t current_sms(int *sms)
-{
-    static int cached[kMaxDevices];  // written with the same value by every thread that finds it 0
-    int dev;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e)
-        return e;
-    if (dev < 0 || dev >= kMaxDevices)
-        return cudaErrorInvalidDevice;
-    int n = __atomic_load_n(&cached[dev], __ATOMIC_RELAXED);
-    if (n == 0) {
-        e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-        if (e)
-            return e;
-        __atomic_store_n(&cached[dev], n, __ATOMIC_RELAXED);
-    }
-    *sms = n;
-    return cudaSuccess;
-}
-
-// `follows`: as a programmatic dependent of the call's kernel before it, which it waits for itself.  The
-// first kernel of a call is launched plainly: what other calls launched before it, some as dependents of
-// one another, has all ended then.
-template <class... Params, class... Args>
-spec_status launch(bool follows, void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t st, Args... args)
-{
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = follows ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
-}
-
-bool pending() { return cudaPeekAtLastError() != cudaSuccess; }
 
 }  // namespace
 }  // namespace specrej

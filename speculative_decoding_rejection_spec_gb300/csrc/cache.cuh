@@ -115,6 +115,8 @@ inline spec_status view_cache(const spec_cache *c, CacheView *out)
 
 namespace {
 
+constexpr int kCopyThreads = 256;
+
 // Records an error in the cache's word.
 __device__ __forceinline__ void cache_error(int32_t *error, int32_t bits, int32_t request)
 {
@@ -153,6 +155,77 @@ __device__ __forceinline__ int warp_find_request(const int32_t *cu, int B, int64
     }
     return lo;
 }
+
+// Whether cu[0 .. B] starts at 0, does not decrease and ends within N rows; the whole block.
+__device__ __forceinline__ bool block_layout_ok(const int32_t *cu, int B, int64_t N)
+{
+    bool bad = false;
+    for (int r = threadIdx.x; r <= B; r += blockDim.x) {
+        const int32_t c = cu[r];
+        bad |= r == 0 ? c != 0 : cu[r - 1] > c;
+        bad |= c > N;
+    }
+    return !__syncthreads_or(bad);
+}
+
+// Whether this block is the last of `blocks` to come here; what the others wrote is then visible.
+__device__ __forceinline__ bool last_block(int32_t *ticket, int blocks)
+{
+    __shared__ bool last;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        last = atomicAdd(ticket, 1) == blocks - 1;
+        if (last)
+            *ticket = 0;
+    }
+    __syncthreads();
+    __threadfence();
+    return last;
+}
+
+constexpr int kMaxDevices = 64;
+
+// SMs of the current device.
+inline cudaError_t current_sms(int *sms)
+{
+    static int cached[kMaxDevices];  // written with the same value by every thread that finds it 0
+    int dev;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e)
+        return e;
+    if (dev < 0 || dev >= kMaxDevices)
+        return cudaErrorInvalidDevice;
+    int n = __atomic_load_n(&cached[dev], __ATOMIC_RELAXED);
+    if (n == 0) {
+        e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        if (e)
+            return e;
+        __atomic_store_n(&cached[dev], n, __ATOMIC_RELAXED);
+    }
+    *sms = n;
+    return cudaSuccess;
+}
+
+// `follows`: as a programmatic dependent of the call's kernel before it, which it waits for itself.  The
+// first kernel of a call is launched plainly: what other calls launched before it, some as dependents of
+// one another, has all ended then.
+template <class... Params, class... Args>
+spec_status launch(bool follows, void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t st, Args... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = follows ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+inline bool pending() { return cudaPeekAtLastError() != cudaSuccess; }
 
 }  // namespace
 }  // namespace specrej
