@@ -1220,6 +1220,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             // keys of the share that lie below the window of some rows, or of all
             const int some_from = max(p.sinks, item.t0 * kTile), some = min(high, last);
             const bool cut_block = (last > common || (MODE == kWindow && some > some_from)) && !dry;
+            cuts += cut_block;
             float M = -INFINITY, l = 0;
             bool any = false;  // the accumulator holds something
             for (int t = wide ? 0 : g; t < nt; t += wide ? 1 : 2) {
