@@ -67,6 +67,10 @@ constexpr int kMaxGrid = 160;       // blocks a call may use (SMs of the device,
 // late (0 / 2 / 4 / 6: decoding 200 / 178 / 176 / 180 us, verifying 234 / 205 / 205 / 206).
 constexpr int kBlockCost = 3;
 constexpr int kMinShare = 2;        // least places of a block's share (2 / 4 / 8: one token 17 / 20 / 23 us)
+// Windows and shared prefixes, whose calls mix row blocks of both kinds and many of few tiles, weigh them in thirds
+// of a narrow tile.  (Measured in the blocks: narrow tile 1.05-1.3 us, wide 1.7-1.8, between two row blocks 3.5 and
+// 5.2 us.)
+constexpr int kNarrowTile = 3, kWideTile = 5, kNarrowBlock = 10, kWideBlock = 14, kMinWeighed = 10;
 constexpr float kLazy = 8.0f;       // log2 of the growth that moves a row's maximum (4 is no faster)
 // log2 of the largest weight when a row's maximum moves.  fp16: far below the maximum, where a long context
 // may have a good part of its weight, the product with V keeps 2^-21 of it in full and 2^-32 at all (with
@@ -81,10 +85,10 @@ constexpr int kTmemColumns = 512;   // two groups: 128 of S (P over it), up to 1
 struct Shares {
     int64_t each;  // the first `more` shares have one more than each
     int32_t blocks, more;
-    __device__ __forceinline__ void cut(int64_t cost, int most)
+    template <int LEAST> __device__ __forceinline__ void cut(int64_t cost, int most)
     {
         if (cost < INT32_MAX) {  // nearly always: a 64-bit division takes some hundred cycles
-            blocks = max(1, min(most, ((int)cost + kMinShare - 1) / kMinShare));
+            blocks = max(1, min(most, (int)((uint32_t)cost + LEAST - 1) / LEAST));
             each = (uint32_t)cost / (uint32_t)blocks;
         } else {
             blocks = most;
@@ -105,7 +109,6 @@ struct Shares {
 
 struct Partial {  // of the row block that starts in a block's share and goes on behind it
     int32_t r, h, b, rows;  // rows 0: none
-    int32_t kind;           // as Item's
     int64_t last_place;     // of its last tile in the list
     Shares shares;
 };
@@ -134,6 +137,8 @@ struct AttentionParams {
     const int4 *shared;  // [B] first request, end, tokens of the request's group
     float2 *row_ml;      // [2][N * heads] M, l of a row over its group's tokens, over its own (as part_ml)
     float *row_o;        // [2][N * heads * DP]
+    int2 *row_parts;     // [2][N * heads] of a row block, at its first row: the block it begins in, and the parts
+                         // that it was cut into (0: none, the rows' sums are in row_o, or their results in out)
     int32_t *begun;      // [1] whether there is work at all (a malformed cu: none)
 };
 
@@ -273,7 +278,8 @@ struct alignas(16) Item {
     uint32_t slots;        // K / V slots used before
     int32_t near, gap;     // as Range's; keys and len are without those left out
     int32_t kind;          // 0: the result goes to out; 1: it is that over a group's shared tokens (the rows are
-                           // those of all its requests); 2: that over the other tokens of a request of a group
+                           // those of all its requests); 2: that over the other tokens of a request of a group;
+                           // 4 more: twins, the same of head h + 1 with it, a group each
 };
 
 __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap *map, int x, int head, int token, uint64_t *bar)
@@ -316,7 +322,8 @@ template <int SLOTS> struct alignas(16) AttnShared {
     uint32_t tmem;
     uint32_t arrivals[SLOTS + 2];  // made on full[] and q_full[] in all, added up as the loading roles end
     volatile int32_t gave_up;
-    volatile int32_t spoilt[2];  // the number of a row block among those with unseen keys, by its last bit
+    // the number of a row block among those with unseen keys, by its last bit (of twins, by group)
+    volatile int32_t spoilt[2][2];
 };
 
 // Waits for a barrier's phase, a bounded number of polls.  When one wait gives up, all do: no row block
@@ -364,6 +371,25 @@ struct Range {
     __device__ __forceinline__ int tiles() const { return (keys + kTile - 1) / kTile; }
 };
 
+// The places of a row block in the list: `begin`, then `tile` for each tile, done by the block whose share has the
+// first of them.
+struct Cost {
+    int begin, tile;
+    __device__ __forceinline__ int of(int tiles) const { return begin + tile * tiles; }
+    // the first tile whose first place is `at` or behind it
+    __device__ __forceinline__ int first(int at) const
+    {
+        return at <= begin ? 0 : (uint32_t)(at - begin + tile - 1) / (uint32_t)tile;
+    }
+};
+
+template <int MODE> __device__ __forceinline__ Cost cost_of(int rows)
+{
+    if (MODE == kWhole)
+        return Cost{kBlockCost, 1};
+    return rows > kTile ? Cost{kWideBlock, kWideTile} : Cost{kNarrowBlock, kNarrowTile};
+}
+
 // Of row block b: up to the last row's own key.  What is left out begins and ends with a copy of `box` keys: before
 // the window of the block's first row (the root of a tree: the others are deeper), behind the sinks; or the tokens of
 // the group.
@@ -398,7 +424,7 @@ __device__ __forceinline__ int group_tokens(const CacheView &c, const AttentionP
     const int64_t all = ((int64_t)p.cu[g.y] - p.cu[g.x]) * p.group;
     if (first.x != g.x || first.y != g.y || first.z != g.z || c.lens[g.x] < g.z ||
         !holds(c, c.held[g.x], c.lens[g.x], 0) || all <= 0 || all > p.N * p.group ||
-        (all + kBlockRows - 1) / kBlockRows * (kBlockCost + 1 + (int64_t)g.z / kTile) > INT32_MAX)
+        (all + kBlockRows - 1) / kBlockRows * (kWideBlock + kWideTile * (1 + (int64_t)g.z / kTile)) > INT32_MAX / 2)
         return 0;
     *rows = g.x == r ? (int)all : 0;
     return g.z;
@@ -416,22 +442,25 @@ __device__ __forceinline__ Request request_of(const CacheView &c, const Attentio
     q.cost = q.tokens = q.group_rows = q.group_cost = 0;
     if (MODE == kShared) {
         q.tokens = group_tokens(c, p, r, len, g, &q.group_rows);
-        if (q.group_rows > 0)
-            q.group_cost = (q.group_rows + kBlockRows - 1) / kBlockRows *
-                           (kBlockCost + block_range<MODE>(p, q, true, 0).tiles());
+        if (q.group_rows > 0) {
+            const int tiles = block_range<MODE>(p, q, true, 0).tiles(), last = q.group_rows % kBlockRows;
+            q.group_cost = q.group_rows / kBlockRows * cost_of<MODE>(kBlockRows).of(tiles) +
+                           (last > 0 ? cost_of<MODE>(last).of(tiles) : 0);
+        }
     }
     if (n <= 0)
         return q;
     const int64_t blocks = (q.rows + kBlockRows - 1) / kBlockRows;
     if (!holds(c, held, len, n) || (p.parent && n > kMaxTree) ||
-        blocks * (kBlockCost + 1 + (MODE == kWindow) + ((int64_t)len + n) / kTile) > INT32_MAX) {
+        blocks * cost_of<MODE>(kBlockRows).of(1) + blocks * (((int64_t)len + n) / kTile) * cost_of<MODE>(kBlockRows).tile >
+            (MODE == kWhole ? INT32_MAX : INT32_MAX / 2)) {
         if (report)
             cache_error(c.error, p.parent && n > kMaxTree ? SPEC_DEVERR_TREE : SPEC_DEVERR_LENGTH, r);
         return q;
     }
 #pragma unroll 1
     for (int b = 0; b * kBlockRows < q.rows; ++b)
-        q.cost += kBlockCost + block_range<MODE>(p, q, false, b).tiles();
+        q.cost += cost_of<MODE>(min(kBlockRows, q.rows - b * kBlockRows)).of(block_range<MODE>(p, q, false, b).tiles());
     return q;
 }
 
@@ -443,8 +472,9 @@ __device__ __forceinline__ Request request_of(const CacheView &c, const Attentio
 }
 
 // Walks a block's share, one (request or group, head, row block) at a time; a whole warp.  A row block takes
-// kBlockCost places of the list before those of its tiles; a share that ends within them leaves the
-// row block to the next.
+// some places of the list before those of its tiles; a share that ends within them leaves the row block to the next.
+// (Every share but a call's last is longer than a tile's places: a row block that is cut has a part in each block from
+// its first to its last.)
 template <int MODE> struct Walk {
     Request q;
     int r, h, b;
@@ -452,7 +482,9 @@ template <int MODE> struct Walk {
     Range range;      // of this row block
     int tiles;        // of this row block
     int t0, t1;       // those in the share; t1 > t0 but for a share of no tile
-    int64_t pos, end; // place of the row block's part in the list
+    bool twins;       // with the same of the next head
+    int64_t pos, end; // place in the list behind the row block's part
+    int64_t last;     // place of the row block's last tile
 
     // r and q are the request in which the share begins, after `base` places; false when it holds no tile
     __device__ __forceinline__ bool start(const CacheView &c, const AttentionParams &p, const Shares &s, int64_t base)
@@ -466,23 +498,34 @@ template <int MODE> struct Walk {
         const int cost = of_group ? q.group_cost : q.cost;
         for (h = 0; at >= cost; ++h)
             at -= cost;
-        for (b = 0; at >= kBlockCost + block_range<MODE>(p, q, of_group, b).tiles(); ++b)
-            at -= kBlockCost + block_range<MODE>(p, q, of_group, b).tiles();
-        return here(p, (int)at);
+        for (b = 0;; ++b) {
+            const int all = cost_of<MODE>(rows()).of(block_range<MODE>(p, q, of_group, b).tiles());
+            if (at < all)
+                break;
+            at -= all;
+        }
+        return here(c, p, (int)at);
     }
     // the part of the row block from its place `from` on
-    __device__ __forceinline__ bool here(const AttentionParams &p, int from)
+    __device__ __forceinline__ bool here(const CacheView &c, const AttentionParams &p, int from)
     {
         range = block_range<MODE>(p, q, of_group, b);
         tiles = range.tiles();
-        const int to = (int)min((int64_t)(kBlockCost + tiles), from + (end - pos));
-        t0 = max(from - kBlockCost, 0);
-        t1 = max(to - kBlockCost, 0);
+        const Cost cost = cost_of<MODE>(rows());
+        const int all = cost.of(tiles), to = (int)min((int64_t)all, from + (end - pos));
+        t0 = cost.first(from);
+        t1 = cost.first(to);
+        last = pos - from + cost.of(tiles - 1);
         pos += to - from;
+        // Two heads of few rows, both whole: a softmax group takes each, nothing is to be merged, and the one's first
+        // and last steps run beside the other's.
+        twins = MODE != kWhole && t0 == 0 && to == all && all_rows() <= kTile && h + 1 < c.heads && end - pos >= all;
+        if (twins) {
+            pos += all;
+            ++h;
+        }
         return t1 > t0;
     }
-    // place of the row block's last tile
-    __device__ __forceinline__ int64_t last_place() const { return pos + (tiles - t1) - 1; }
     // to the next row block; false at the share's end
     __device__ __forceinline__ bool next(const CacheView &c, const AttentionParams &p)
     {
@@ -494,7 +537,7 @@ template <int MODE> struct Walk {
                 h = 0;
                 if (MODE == kShared && of_group && q.cost > 0) {
                     of_group = false;
-                    return here(p, 0);
+                    return here(c, p, 0);
                 }
                 const int lane = threadIdx.x & 31;
                 for (++r;; r += 32) {
@@ -515,11 +558,12 @@ template <int MODE> struct Walk {
                 of_group = MODE == kShared && q.group_cost > 0;
             }
         }
-        return here(p, 0);
+        return here(c, p, 0);
     }
     __device__ __forceinline__ int all_rows() const { return of_group ? q.group_rows : q.rows; }
     __device__ __forceinline__ int rows() const { return min(kBlockRows, all_rows() - b * kBlockRows); }
     __device__ __forceinline__ int kind() const { return MODE != kShared || !q.tokens ? 0 : of_group ? 1 : 2; }
+    __device__ __forceinline__ int first_head() const { return h - (MODE != kWhole && twins); }
 };
 
 // ---------------------------------------------------------------------------------------
@@ -705,12 +749,21 @@ __device__ __forceinline__ bool find_share(const CacheView &c, const AttentionPa
             if (blockIdx.x == 0 && __any_sync(kFull, wrong))
                 for (int r = lane; r < p.B; r += 32)
                     request_of<MODE>(c, p, r, true);
-            shares->cut(before, gridDim.x);
+            shares->template cut<MODE == kWhole ? kMinShare : kMinWeighed>(before, gridDim.x);
             if (before == 0 || blockIdx.x >= shares->blocks)
                 return false;
         }
     }
     return false;  // cannot be: every place belongs to a request
+}
+
+// The order of a row block's tiles in the ring, as the products use them: K of tile 0, then K of tile t + 1 and V of
+// tile t.  Twins: of both in every step.
+__device__ __forceinline__ uint32_t slot_of(bool is_v, bool twins, int g, int t, int nt)
+{
+    if (twins)
+        return is_v ? (t + 1 < nt ? 4 * t + 3 + 2 * g : 4 * nt - 2 + g) : (t > 0 ? 4 * t - 2 + 2 * g : g);
+    return is_v ? min(2 * t + 2, 2 * nt - 1) : max(2 * t - 1, 0);
 }
 
 template <int DT, int DP, int MODE>
@@ -755,7 +808,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         for (int i = 0; i < SLOTS + 2; ++i)
             S.arrivals[i] = 0;
         S.gave_up = 0;
-        S.spoilt[0] = S.spoilt[1] = 0;
+        S.spoilt[0][0] = S.spoilt[0][1] = S.spoilt[1][0] = S.spoilt[1][1] = 0;
         mbar_fence_init();
     }
     if (warp == kMmaWarp) {
@@ -784,7 +837,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (warp >= kSoftmaxWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp & 2) {
-            // Slot order: K of tile 0, then K of tile t + 1 and V of tile t, as the products use them.
             const bool is_v = warp >= 14;
             const int half = warp & 1;  // copies (piece, chunk) of every second number
             const CUtensorMap *map = is_v ? &vmap : &kmap;
@@ -794,13 +846,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 int page, token;
             };
             uint32_t arrivals = 0;  // lane i: on full[i]
+            bool lost = false;
             for (uint32_t k = 0;; ++k) {
                 if (!announced(k))
                     break;
                 const Item &item = S.item[k % kItems];
                 const int r = item.r, h = item.h, keys = item.keys, t0 = item.t0, nt = item.nt;
                 const uint32_t slots = item.slots;
-                const int near = item.near, gap = item.gap;
+                const int near = item.near, gap = item.gap, heads = MODE != kWhole && item.kind & 4 ? 2 : 1;
                 done_with(k);
                 if (nt == 0)
                     break;
@@ -831,29 +884,35 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             now.page = c.num_pages;  // outside the tensor: reads as zeros
                         }
                     }
-                    const uint32_t use = slots + (is_v ? min(2 * t + 2, 2 * nt - 1) : max(2 * t - 1, 0));
-                    const uint32_t slot = use % SLOTS, turn = use / SLOTS;
-                    const int count = __popc(__ballot_sync(kFull, now.token >= 0) >> from & low_bits(pieces));
-                    if (turn > 0)
-                        wait(&S.empty[slot], (turn & 1) ^ 1);
-                    if (__any_sync(kFull, S.gave_up))
-                        break;
-                    arrivals += lane == slot;
-                    const uint32_t dst = smem_addr(ring) + slot * Z::kSlotBytes;
-                    uint64_t *bar = &S.full[slot];
-                    constexpr int kChunks = DP / 64;
-                    const int mine = kChunks == 2 ? count : (count + 1 - half) / 2;
-                    if (elect_one())
-                        mbar_arrive_expect_tx(bar, mine * p.box * 128);
-                    for (int i = 0; i < mine; ++i) {
-                        const int piece = kChunks == 2 ? i : 2 * i + half, chunk = kChunks == 2 ? half : 0;
-                        const int page = __shfl_sync(kFull, now.page, from + piece);
-                        const int token = __shfl_sync(kFull, now.token, from + piece);
+                    for (int g = 0; g < heads; ++g) {
+                        const uint32_t use = slots + slot_of(is_v, heads == 2, g, t, nt);
+                        const uint32_t slot = use % SLOTS, turn = use / SLOTS;
+                        const int count = __popc(__ballot_sync(kFull, now.token >= 0) >> from & low_bits(pieces));
+                        if (turn > 0)
+                            wait(&S.empty[slot], (turn & 1) ^ 1);
+                        if (__any_sync(kFull, S.gave_up)) {
+                            lost = true;
+                            break;
+                        }
+                        arrivals += lane == slot;
+                        const uint32_t dst = smem_addr(ring) + slot * Z::kSlotBytes;
+                        uint64_t *bar = &S.full[slot];
+                        constexpr int kChunks = DP / 64;
+                        const int mine = kChunks == 2 ? count : (count + 1 - half) / 2;
                         if (elect_one())
-                            tma_box(dst + piece * p.box * 128 + chunk * Z::kChunk, map, chunk * 64, token, h, page,
-                                    bar);
+                            mbar_arrive_expect_tx(bar, mine * p.box * 128);
+                        for (int i = 0; i < mine; ++i) {
+                            const int piece = kChunks == 2 ? i : 2 * i + half, chunk = kChunks == 2 ? half : 0;
+                            const int page = __shfl_sync(kFull, now.page, from + piece);
+                            const int token = __shfl_sync(kFull, now.token, from + piece);
+                            if (elect_one())
+                                tma_box(dst + piece * p.box * 128 + chunk * Z::kChunk, map, chunk * 64, token, h + g, page,
+                                        bar);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
+                    if (lost)
+                        break;
                 }
             }
             if (lane < SLOTS)
@@ -910,15 +969,46 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         break;
                     const Item &item = S.item[k % kItems];
                     const int nt = item.nt, q_use = item.q_use;
-                    const bool wide = item.rows > kTile;
+                    const bool wide = item.rows > kTile, twins = MODE != kWhole && item.kind & 4;
                     mbar_arrive(&S.item_empty[k % kItems]);
                     if (nt == 0)
                         break;
-                    for (int g = 0; g <= (int)wide; ++g)
+                    for (int g = 0; g <= (int)(wide || twins); ++g)
                         lost |= !wait(&S.q_full[(q_use + g) & 1], (q_use + g) >> 1 & 1);
                     // step t: scores of tile t, outputs of tile t - 1
                     bool k_in = false, v_in = false, p_in = false;
-                    if (!wide) {
+                    if (MODE != kWhole && twins) {
+                        for (int t = 0; t <= nt && !lost; ++t) {
+#pragma unroll 1
+                            for (int g = 0; g < 2; ++g) {
+                                uint32_t kslot = 0, vslot = 0;
+                                if (t < nt)
+                                    kslot = take(k_in);
+                                if (t > 0) {
+                                    vslot = take(v_in);
+                                    p_ready(g, p_in);
+                                    outputs(g, vslot, t > 1);
+                                }
+                                if (t < nt)
+                                    scores(g, kslot, (q_use + g) & 1);
+                                mma_commit(t < nt ? &S.s_full[g] : &S.o_full[g]);
+                                if (lost)
+                                    break;
+                                // the next half step's: K where there is one, V behind it, and the group's weights
+                                const int nextt = t + g;
+                                k_in = nextt < nt && full_here(0);
+                                v_in = nextt > 0 && nextt <= nt && full_here(nextt < nt);
+                                p_in = nextt > 0 && nextt <= nt && p_here(g ^ 1);
+                                if (t < nt) {
+                                    mma_commit(&S.empty[kslot]);
+                                    if (t + 1 == nt)
+                                        mma_commit(&S.q_empty[(q_use + g) & 1]);
+                                }
+                                if (t > 0)
+                                    mma_commit(&S.empty[vslot]);
+                            }
+                        }
+                    } else if (!wide) {
                         for (int t = 0; t <= nt; ++t) {
                             const int g = (t - 1) & 1;  // the group of tile t - 1
                             uint32_t kslot = 0, vslot = 0;
@@ -1014,7 +1104,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         Item x{};
                         if (more) {
                             x.r = w.r;
-                            x.h = w.h;
+                            x.h = w.first_head();
                             x.b = w.b;
                             x.rows = w.rows();
                             x.nt = w.t1 - w.t0;
@@ -1023,7 +1113,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             x.keys = w.range.keys;
                             x.near = w.range.near;
                             x.gap = w.range.gap;
-                            x.kind = w.kind();
+                            x.kind = w.kind() + (MODE != kWhole && w.twins ? 4 : 0);
                             x.len = MODE == kShared && w.of_group ? w.q.tokens : w.q.len - w.range.gap;
                             x.n = MODE == kShared && w.of_group ? 0 : w.q.n;
                             x.first = p.cu[w.r];
@@ -1035,9 +1125,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                 y.h = w.h;
                                 y.b = w.b;
                                 y.rows = x.rows;
-                                y.kind = x.kind;
-                                y.last_place = w.last_place();
+                                y.last_place = w.last;
                                 y.shares = shares;
+                            }
+                            if (MODE == kShared && w.t0 == 0) {
+                                const int m = w.b * kBlockRows, token = by_group(p, m);
+                                const int64_t at = ((w.kind() == 1 ? 0 : p.N) + x.first + token) * p.heads +
+                                                   x.h * p.group + m - token * p.group;
+                                const int2 y = make_int2(blockIdx.x, w.t1 < w.tiles ? shares.owner(w.last) - (int)blockIdx.x + 1
+                                                                                   : 0);
+                                p.row_parts[at] = y;
+                                if (w.twins)
+                                    p.row_parts[at + p.group] = y;
                             }
                         }
                         *mine = x;
@@ -1052,9 +1151,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     done_with(k);
                 if (item.nt == 0)
                     break;
-                const int count = item.rows > kTile ? 2 : 1;
+                const bool twins = MODE != kWhole && item.kind & 4;
+                const int count = item.rows > kTile || twins ? 2 : 1;
                 q_use = item.q_use + count;
-                slots = item.slots + 2 * item.nt;
+                slots = item.slots + (twins ? 4 : 2) * item.nt;
                 constexpr int kVecs = DP / 8, kStep = 32 * kQueryWarps / kVecs;  // 16-byte units of a row, rows of a turn
                 for (int g = 0; g < count; ++g) {
                     const int use = item.q_use + g;
@@ -1065,8 +1165,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     arrivals += lane == (use & 1);
                     const int at = part * 32 + lane, vec = at % kVecs;
                     const uint32_t dst = smem_addr(qtile) + (use & 1) * Z::kSlotBytes + vec / 8 * Z::kChunk;
-                    const int m0 = item.b * kBlockRows + g * kTile, rows = min(kTile, item.rows - g * kTile);
-                    if (count == 2 && p.q_tokens) {
+                    const int more_rows = twins ? 0 : g * kTile, h = item.h + (twins ? g : 0);
+                    const int m0 = item.b * kBlockRows + more_rows, rows = min(kTile, item.rows - more_rows);
+                    if (count == 2 && !twins && p.q_tokens) {
                         // a wide row block's: one copy for each 64 elements (rows behind the last are not
                         // looked at); row by row they took 7 us, with the products waiting
                         if (warp == kWalkWarp) {
@@ -1087,7 +1188,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     int x = at / kVecs, token = by_group(p, m0 + x), head = (m0 + x) - token * p.group;
                     const int more_tokens = by_group(p, kStep), more_heads = kStep - more_tokens * p.group;
                     const char *src = p.q + 2 * ((int64_t)item.first * p.q_token +
-                                                 (int64_t)(item.h * p.group) * p.q_head + vec * 8);
+                                                 (int64_t)(h * p.group) * p.q_head + vec * 8);
                     if (vec * 8 < c.dim) {
                         for (; x < rows; x += kStep) {
                             copy16(dst + x * 128 + ((vec % 8) ^ (x % 8)) * 16,
@@ -1152,19 +1253,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const int nt = item.nt;
             if (nt == 0)
                 break;
-            const bool wide = item.rows > kTile;
-            const int m0 = wide ? g * kTile : 0;             // the group's first row in the block
+            // wide: both groups take every tile (twins: of a head each)
+            const bool twins = MODE != kWhole && item.kind & 4, wide = item.rows > kTile || twins;
+            const int m0 = wide && !twins ? g * kTile : 0;   // the group's first row in the block
             const int mine = min(kTile, item.rows - m0);     // its rows
             const bool warp_on = sub * 32 < mine, on = row < mine;
             const int m = item.b * kBlockRows + m0 + row;    // row of the request
-            const int token = by_group(p, m), q_head = item.h * p.group + m - token * p.group;
+            const int token = by_group(p, m), kv_head = item.h + (twins ? g : 0);
+            const int q_head = kv_head * p.group + m - token * p.group;
 
             const int turns = wide ? nt : (nt - g + 1) / 2;  // this group's tiles
 
             uint32_t bits[kMaxTree / 32] = {};
             int depth = 0;  // windows: of the row's node
             bool refused = false;  // the request's tree is malformed: every row block of it is left out
-            if (p.parent && !dry && !(MODE == kShared && item.kind == 1)) {
+            if (p.parent && !dry && !(MODE == kShared && (item.kind & 3) == 1)) {
                 int32_t *par = S.group[g].parent;  // every warp of the group writes the same there
                 bool bad = false;
                 for (int i = lane; i < item.n; i += 32) {
@@ -1202,7 +1305,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             int common = p.parent ? item.len + (MODE != kWindow) : item.len + by_group(p, item.b * kBlockRows) + 1;
             // keys of the chain that this row sees end here
             int limit = item.len + token + 1;
-            if (MODE == kShared && item.kind == 1)
+            if (MODE == kShared && (item.kind & 3) == 1)
                 all_see = common = limit = item.keys;
             const int last = min(item.keys, (item.t0 + nt) * kTile);
             // Windows: behind the sinks a row sees no key below `low`, at least up to its own; the highest of the row
@@ -1323,8 +1426,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 // windows: keys from w0 to w1 are below the window of some rows or all
                 const int w0 = MODE == kWindow ? min(max(p.sinks - column, 0), kTile) : 0,
                           w1 = MODE == kWindow ? max(min(min(high - column, kTile), unseen), 0) : 0;
-                if ((unseen < kTile || (MODE == kWindow && w0 < w1)) && (!wide || g == 0) && !dry) {
-                    const uint32_t use = item.slots + min(2 * t + 2, 2 * nt - 1);  // the slot of V
+                if ((unseen < kTile || (MODE == kWindow && w0 < w1)) && (!wide || g == 0 || twins) && !dry) {
+                    const uint32_t use = item.slots + slot_of(true, twins, g, t, nt);
                     wait(&S.full[use % SLOTS], use / SLOTS & 1);
                     char *base = ring + use % SLOTS * Z::kSlotBytes;
                     const int i0 = max(unseen, 0) * 8 + row, i1 = min(behind, kTile) * 8;
@@ -1340,7 +1443,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             }
                         if (bad & 0x80008000u) {
                             drop_not_finite<DT, DP>(base, i0, i1);
-                            S.spoilt[cuts & 1] = cuts;
+                            S.spoilt[twins ? g : 0][cuts & 1] = cuts;
                         }
                     };
                     look(i0, i1);
@@ -1370,9 +1473,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const int64_t place = ((int64_t)blockIdx.x * 2 + (item.t0 == 0)) * p.max_rows + m0 + row;
             char *out = p.out + 2 * ((int64_t)(item.first + token) * p.out_token + q_head * p.out_head);
             // of a row of a group: its place over the shared tokens, or over its own
-            const int64_t in_group = ((item.kind - 1) * p.N + item.first + token) * p.heads + q_head;
+            const int64_t in_group = (((item.kind & 3) - 1) * p.N + item.first + token) * p.heads + q_head;
             float *sums = MODE == kShared && whole ? p.row_o + in_group * DP : p.part_o + place * DP;
-            const bool to_out = whole && (MODE != kShared || item.kind == 0);
+            const bool to_out = whole && (MODE != kShared || (item.kind & 3) == 0);
             auto store = [&](const float *o, int col, float by) {  // 32 columns
                 if (!kept)
                     return;
@@ -1404,19 +1507,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             // (The groups are less than two row blocks apart, by their meetings or, of wide ones, by the order
             // of the products: nobody writes spoilt[] for the next but one before all have read it here.)
             auto spoilt = [&]() {
-                if (cut_block && kept && S.spoilt[cuts & 1] == cuts) {
+                if (cut_block && kept && S.spoilt[twins ? g : 0][cuts & 1] == cuts) {
                     const uint4 tree = make_uint4(bits[0], bits[1], bits[2], bits[3]);
                     char *result = to_out ? out : reinterpret_cast<char *>(sums);
                     const int from = max(common, item.t0 * kTile);
-                    add_spoilt<DT, MODE>(c, p, item.r, item.h, from, last, item.near, item.gap, item.len, token, low, tree,
+                    add_spoilt<DT, MODE>(c, p, item.r, kv_head, from, last, item.near, item.gap, item.len, token, low, tree,
                                          result, !to_out);
                     if (MODE == kWindow)
-                        add_spoilt<DT, MODE>(c, p, item.r, item.h, some_from, min(some, from), item.near, item.gap, item.len,
+                        add_spoilt<DT, MODE>(c, p, item.r, kv_head, some_from, min(some, from), item.near, item.gap, item.len,
                                              token, low, tree, result, !to_out);
                 }
             };
             if (wide) {
-                if (cut_block) {
+                if (cut_block && !twins) {
                     if (g == 1)
                         wait(&S.known[wide_cuts & 1], wide_cuts >> 1 & 1);
                     else if (lane == 0)
@@ -1496,7 +1599,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 // every W-th part, J rows per warp at the same time.  Bound by the latency of L2, a chain of three loads
 // (the row block, the weights, the parts): two parts of every row are on their way before the weights
 // are known.
-template <int DT, int DP, int MODE, int W, int J>
+template <int DT, int DP, int W, int J>
 __device__ __forceinline__ void join(const CacheView &c, const AttentionParams &p, const Partial &x, float4 (*sums)[32],
                                      int row0, int lane, int warp)
 {
@@ -1587,22 +1690,11 @@ __device__ __forceinline__ void join(const CacheView &c, const AttentionParams &
         const int row = row0 + j * next;
         if (row >= x.rows)
             return;
-        if (l[j] < 0 && (MODE != kShared || x.kind == 0))
+        if (l[j] < 0)
             continue;  // of a refused request: its parts have sums of -1
         const int m = x.b * kBlockRows + row;
         const int token = by_group(p, m), head = x.h * p.group + m - token * p.group;
         const int64_t t = (int64_t)first + token;
-        if (MODE == kShared && x.kind != 0) {
-            const int64_t at = ((x.kind - 1) * p.N + t) * p.heads + head;
-            float *o = p.row_o + at * DP + lane * E;
-            if (E == 4)
-                *reinterpret_cast<float4 *>(o) = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-            else
-                *reinterpret_cast<float2 *>(o) = make_float2(acc[j][0], acc[j][1]);
-            if (lane == 0)
-                p.row_ml[at] = make_float2(top[j], l[j]);
-            continue;
-        }
         const float by = 1.0f / l[j];
         if (lane * E < c.dim) {
             char *out = p.out + 2 * (t * p.out_token + head * p.out_head + lane * E);
@@ -1622,7 +1714,7 @@ __device__ __forceinline__ void join(const CacheView &c, const AttentionParams &
 // row: 38 parts of 48 rows took 79 us in all with one, 62 with four).
 constexpr int kJoinRows = 2;
 
-template <int DT, int DP, int MODE, int W>
+template <int DT, int DP, int W>
 __global__ void __launch_bounds__(256) join_kernel(CacheView c, AttentionParams p)
 {
     __shared__ float4 sums[W > 1 ? 8 : 1][32];
@@ -1633,53 +1725,111 @@ __global__ void __launch_bounds__(256) join_kernel(CacheView c, AttentionParams 
     if (row0 >= x.rows)
         return;
     if (W > 1 || row0 + gridDim.y * 8 >= x.rows)
-        join<DT, DP, MODE, W, 1>(c, p, x, sums, row0, lane, warp);
+        join<DT, DP, W, 1>(c, p, x, sums, row0, lane, warp);
     else
-        join<DT, DP, MODE, W, kJoinRows>(c, p, x, sums, row0, lane, warp);
+        join<DT, DP, W, kJoinRows>(c, p, x, sums, row0, lane, warp);
 }
 
-// The rows of the requests that are in a group: what they have from the shared tokens and from their own.  Blocks
-// (request, y), a warp per row.
-template <int DT, int DP> __global__ void __launch_bounds__(256) merge_kernel(CacheView c, AttentionParams p)
+// Joins what the rows of a call with shared prefixes have from their group's tokens and from their own, each in one
+// piece or in the parts that it was cut into.  Blocks (request, y), a warp per row; bound by latency as join() is.
+template <int DT, int DP> __global__ void __launch_bounds__(256) join_shared_kernel(CacheView c, AttentionParams p)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int r = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (!*p.begun)
         return;
     const Request q = request_of<kShared>(c, p, r, false);
-    if (q.cost == 0 || q.tokens == 0)
+    if (q.cost == 0)
         return;
-    const int64_t from = (int64_t)p.cu[r] * p.heads, rows = (int64_t)q.n * p.heads;
-    constexpr int E = DP / 32;
-    for (int64_t i = blockIdx.y * 8 + warp; i < rows; i += gridDim.y * 8) {
-        const int64_t at = from + i, also = p.N * p.heads + at;
-        const float2 a = p.row_ml[at], b = p.row_ml[also];
-        float x[4], y[4];
-        if (E == 4) {
-            const float4 u = *reinterpret_cast<const float4 *>(p.row_o + at * DP + lane * E),
-                         v = *reinterpret_cast<const float4 *>(p.row_o + also * DP + lane * E);
-            x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
-            y[0] = v.x, y[1] = v.y, y[2] = v.z, y[3] = v.w;
-        } else {
-            const float2 u = *reinterpret_cast<const float2 *>(p.row_o + at * DP + lane * E),
-                         v = *reinterpret_cast<const float2 *>(p.row_o + also * DP + lane * E);
-            x[0] = u.x, x[1] = u.y;
-            y[0] = v.x, y[1] = v.y;
+    const int first = p.cu[r], group_first = q.tokens ? p.cu[p.shared[r].x] : 0;
+    const int rows = q.n * p.heads;
+    constexpr int E = DP / 32;  // elements per lane
+    for (int i = blockIdx.y * 8 + warp; i < rows; i += gridDim.y * 8) {
+        const int token = i / p.heads, head = i - token * p.heads, kv = by_group(p, head), in_kv = head - kv * p.group;
+        const int64_t at = (int64_t)(first + token) * p.heads + head;
+        // a row's place in the row blocks of the group and of the request, and those blocks' first rows
+        auto parts_of = [&](int from, int64_t side, int *row) {
+            const int m = (first + token - from) * p.group + in_kv, m0 = m & -kBlockRows, t0 = by_group(p, m0);
+            *row = m - m0;
+            return p.row_parts[(side + from + t0) * p.heads + kv * p.group + m0 - t0 * p.group];
+        };
+        int row_a = 0, row_b;
+        const int2 b = parts_of(first, p.N, &row_b);
+        int2 a = make_int2(0, 0);
+        if (q.tokens)
+            a = parts_of(group_first, 0, &row_a);
+        else if (b.y == 0)
+            continue;  // nothing to join: it is in out
+        const int in_a = q.tokens ? max(a.y, 1) : 0, parts = in_a + max(b.y, 1);
+        // where part j's sums are: its place among those of cut row blocks, or below zero the row's
+        auto place = [&](int j) {
+            const bool own = j >= in_a;
+            const int2 x = own ? b : a;
+            const int k = own ? j - in_a : j;
+            return x.y > 0 ? ((int64_t)(x.x + k) * 2 + (k == 0)) * p.max_rows + (own ? row_b : row_a)
+                           : -1 - (at + (own ? p.N * p.heads : 0));
+        };
+        auto load = [&](int j, float *v) {
+            const int64_t x = place(j);
+            const float *o = (x >= 0 ? p.part_o + x * DP : p.row_o + (-1 - x) * DP) + lane * E;
+            if (E == 4) {
+                const float4 y = *reinterpret_cast<const float4 *>(o);
+                v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
+            } else {
+                const float2 y = *reinterpret_cast<const float2 *>(o);
+                v[0] = y.x, v[1] = y.y;
+            }
+        };
+        float top = -INFINITY, l = 0, acc[4] = {};
+        bool refused = false;
+#pragma unroll 1
+        for (int j0 = 0; j0 < parts; j0 += 32) {
+            const int some = min(32, parts - j0);
+            float2 ml = make_float2(-INFINITY, 0);
+            if (lane < some) {
+                const int64_t x = place(j0 + lane);
+                ml = x >= 0 ? p.part_ml[x] : p.row_ml[-1 - x];
+            }
+            constexpr int U = 4;  // parts on their way before the weights are known
+            float v[U][4];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                load(j0 + min(u, some - 1), v[u]);
+            refused |= __any_sync(kFull, ml.y < 0);
+            const float now = fmaxf(top, warp_max(ml.x)), f = top == -INFINITY ? 0.0f : ex2(top - now);
+            top = now;
+            ml.x = ml.x == -INFINITY ? 0.0f : ex2(ml.x - now);
+            l = l * f + warp_sum(ml.x * ml.y);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                acc[e] *= j0 > 0 ? f : 1.0f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float w = __shfl_sync(kFull, ml.x, u);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if (u < some)
+                        acc[e] = fmaf(w, v[u][e], acc[e]);
+            }
+#pragma unroll 4
+            for (int j = U; j < some; ++j) {
+                load(j0 + j, v[0]);
+                const float w = __shfl_sync(kFull, ml.x, j);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    acc[e] = fmaf(w, v[0][e], acc[e]);
+            }
         }
-        if (b.y < 0)
-            continue;  // of a refused request
-        const float top = fmaxf(a.x, b.x);
-        const float fa = ex2(a.x - top), fb = ex2(b.x - top), l = fmaf(a.y, fa, b.y * fb), by = 1.0f / l;
-        const int64_t t = at / p.heads;
-        const int head = (int)(at - t * p.heads);
+        if (refused)
+            continue;  // its parts have sums of -1
+        const float by = 1.0f / l;
         if (lane * E < c.dim) {
-            char *out = p.out + 2 * (t * p.out_token + head * p.out_head + lane * E);
-            auto joined = [&](int e) { return fmaf(x[e], fa, y[e] * fb) * by; };
-            const uint32_t first = from_float2<DT>(joined(0), joined(1));
+            char *out = p.out + 2 * ((first + token) * p.out_token + head * p.out_head + lane * E);
+            const uint32_t low = from_float2<DT>(acc[0] * by, acc[1] * by);
             if (E == 4)
-                *reinterpret_cast<uint2 *>(out) = make_uint2(first, from_float2<DT>(joined(2), joined(3)));
+                *reinterpret_cast<uint2 *>(out) = make_uint2(low, from_float2<DT>(acc[2] * by, acc[3] * by));
             else
-                *reinterpret_cast<uint32_t *>(out) = first;
+                *reinterpret_cast<uint32_t *>(out) = low;
         }
         if (lane == 0 && p.lse)
             p.lse[at] = (top + log2f(l)) * 0.69314718055994531f;
@@ -1692,7 +1842,7 @@ template <int DT, int DP> __global__ void __launch_bounds__(256) merge_kernel(Ca
 
 struct AttentionPlan {
     int dp, max_rows;
-    size_t partial, ml, o, begun, row_ml, row_o, total;
+    size_t partial, ml, o, begun, row_parts, row_ml, row_o, total;
 };
 
 AttentionPlan attention_plan(const CacheView &c, int32_t num_q_heads, int64_t N, bool shared)
@@ -1710,6 +1860,8 @@ AttentionPlan attention_plan(const CacheView &c, int32_t num_q_heads, int64_t N,
     const int64_t rows = shared ? 2 * N * num_q_heads : 0;
     a.begun = o;
     o = align256(o + (shared ? sizeof(int32_t) : 0));
+    a.row_parts = o;
+    o = align256(o + sizeof(int2) * rows);
     a.row_ml = o;
     o = align256(o + sizeof(float2) * rows);
     a.row_o = o;
@@ -1827,21 +1979,18 @@ cudaError_t launch_attention(const CUtensorMap &kmap, const CUtensorMap &vmap, c
     if (e)
         return e;
     cfg.numAttrs = 1;  // the join starts as the blocks end, and waits for the last of them itself
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    if constexpr (MODE == kShared) {
+        const int64_t rows = (p.N * p.heads + p.B - 1) / p.B;  // of a request, on average
+        cfg.gridDim = dim3(p.B, (unsigned)std::min<int64_t>((rows + 7) / 8, 65535));
+        return cudaLaunchKernelEx(&cfg, join_shared_kernel<DT, DP>, c, p);
+    }
     const int warps = p.max_rows <= 64 ? 4 : 1;  // per row
     const int rows = warps == 4 ? 2 : 8 * kJoinRows;  // per block
     cfg.gridDim = dim3(grid, (p.max_rows + rows - 1) / rows);
-    cfg.blockDim = dim3(256);
-    cfg.dynamicSmemBytes = 0;
-    e = warps == 4 ? cudaLaunchKernelEx(&cfg, join_kernel<DT, DP, MODE, 4>, c, p)
-                   : cudaLaunchKernelEx(&cfg, join_kernel<DT, DP, MODE, 1>, c, p);
-    if constexpr (MODE == kShared) {
-        if (e)
-            return e;
-        const int64_t rows = (p.N * p.heads + p.B - 1) / p.B;  // of a request, on average
-        cfg.gridDim = dim3(p.B, (unsigned)std::min<int64_t>((rows + 7) / 8, 65535));
-        e = cudaLaunchKernelEx(&cfg, merge_kernel<DT, DP>, c, p);
-    }
-    return e;
+    return warps == 4 ? cudaLaunchKernelEx(&cfg, join_kernel<DT, DP, 4>, c, p)
+                      : cudaLaunchKernelEx(&cfg, join_kernel<DT, DP, 1>, c, p);
 }
 
 spec_status check_attention(const spec_cache *cache, CacheView *c, int32_t num_q_heads, int32_t B, int64_t N)
@@ -1934,6 +2083,7 @@ template <int MODE> spec_status attend(const spec_cache *cache, const AttentionC
     p.sinks = std::min(a.sinks, INT32_MAX / 2);
     p.shared = reinterpret_cast<const int4 *>(a.shared);
     p.begun = reinterpret_cast<int32_t *>(ws + plan.begun);
+    p.row_parts = reinterpret_cast<int2 *>(ws + plan.row_parts);
     p.row_ml = reinterpret_cast<float2 *>(ws + plan.row_ml);
     p.row_o = reinterpret_cast<float *>(ws + plan.row_o);
     // (only where a row block can have more than 128 rows)

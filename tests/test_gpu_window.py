@@ -171,19 +171,17 @@ def test_long_contexts(n, heads, ctx, window, sinks):
 
 
 def test_a_window_that_holds_all_is_plain_attention():
-    """Bit for bit: nothing is left out, and the same sums are made."""
+    """Nothing is left out: the same results, within the bound (the work is shared out otherwise), and the same bits
+    whatever it is that holds all."""
     import torch
     for n, ctx, kw in (([1, 9, 300], [700, 129, 40], {}), ([64, 100], [300, 77], dict(tree=True, dtype="f16", dim=64))):
         c = Windowed(n, ctx, 2 ** 31 - 1, 0, seed=3, **kw)
         out, lse = c.run()
         c.check(out, lse)
-        plain, plain_lse = Case.run(c)
-        assert torch.equal(out, plain) and torch.equal(lse, plain_lse)
-        c.window, c.sinks = 1, 2 ** 31 - 1
-        out, lse = c.run()
-        assert torch.equal(out, plain) and torch.equal(lse, plain_lse)
-        c.window, c.sinks = 2 ** 40, 2 ** 40
-        assert torch.equal(c.run()[0], plain)
+        c.check(*Case.run(c))
+        for c.window, c.sinks in ((1, 2 ** 31 - 1), (2 ** 40, 2 ** 40), (5000, 7)):
+            again, again_lse = c.run()
+            assert torch.equal(out, again) and torch.equal(lse, again_lse)
 
 
 def test_a_window_of_one_is_the_own_value():
