@@ -420,11 +420,13 @@ __device__ __forceinline__ int group_tokens(const CacheView &c, const AttentionP
 {
     if (g.z <= 0 || g.z > len || g.x < 0 || g.x > r || g.y <= r || g.y > p.B || g.y - g.x < 2 || g.z % c.page_size)
         return 0;
-    const int4 first = g.x == r ? g : p.shared[g.x];
-    const int64_t all = ((int64_t)p.cu[g.y] - p.cu[g.x]) * p.group;
-    if (first.x != g.x || first.y != g.y || first.z != g.z || c.lens[g.x] < g.z ||
-        !holds(c, c.held[g.x], c.lens[g.x], 0) || all <= 0 || all > p.N * p.group ||
-        (all + kBlockRows - 1) / kBlockRows * (kWideBlock + kWideTile * (1 + (int64_t)g.z / kTile)) > INT32_MAX / 2)
+    // (asked for together: this is part of the chain of loads that every block begins with)
+    const int4 first = p.shared[g.x];
+    const int first_len = c.lens[g.x], first_held = c.held[g.x], from = p.cu[g.x], to = p.cu[g.y];
+    const int64_t all = ((int64_t)to - from) * p.group;
+    const bool fits = (first.x == g.x) & (first.y == g.y) & (first.z == g.z) & (first_len >= g.z) &
+                      holds(c, first_held, first_len, 0) & (all > 0) & (all <= p.N * p.group);
+    if (!fits || (all + kBlockRows - 1) / kBlockRows * (kWideBlock + kWideTile * (1 + (int64_t)g.z / kTile)) > INT32_MAX / 2)
         return 0;
     *rows = g.x == r ? (int)all : 0;
     return g.z;
@@ -687,74 +689,92 @@ template <int MODE>
 __device__ __forceinline__ bool find_share(const CacheView &c, const AttentionParams &p, Shares *shares,
                                            Walk<MODE> *w, int64_t *base, int lane)
 {
-    // Twice: the total makes the shares, then the block finds its own.  A batch of one turn keeps its
-    // costs in between.
-    int64_t before = 0, at = 0, work = 0;
+    // Twice: the total makes the shares, then the block looks again at the 32 requests in which its own begins (lane i
+    // keeps what lies before those of turn i; batches of more than 32 turns are gone through again).  The next turn's
+    // loads are on their way while one is added up.
+    struct Loads {
+        int32_t here, next, len, held;
+        int4 g;
+    };
+    auto load = [&](int r0) {
+        const int r = min(r0 + lane, p.B - 1);
+        return Loads{p.cu[min(r0 + lane, p.B)], p.cu[min(r0 + lane + 1, p.B)], c.lens[r], c.held[r],
+                     MODE == kShared ? p.shared[r] : int4{}};
+    };
+    int64_t before = 0, at = 0, work = 0, kept = 0;
     Request q{};
     bool bad = false, wrong = false;
-#pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
-        before = 0;
-#pragma unroll 1
-        for (int r0 = 0; r0 < p.B; r0 += 32) {
-            const int r = r0 + lane;
-            if (pass == 0 || p.B > 32) {
-                const int32_t here = p.cu[min(r, p.B)], next = p.cu[min(r + 1, p.B)], len = c.lens[min(r, p.B - 1)],
-                              held = c.held[min(r, p.B - 1)];
-                const int4 g = MODE == kShared ? p.shared[min(r, p.B - 1)] : int4{};
-                bad |= here > next || next > p.N || here < 0 || (r == 0 && here != 0);
-                q.cost = q.group_cost = 0;
-                if (r < p.B && !bad) {
-                    q = request_of<MODE>(c, p, r, next - here, len, held, g, false);
-                    wrong |= q.cost == 0 && q.n > 0;
-                }
-                work = (int64_t)q.cost * c.heads;
-                if (MODE == kShared)
-                    work += (int64_t)q.group_cost * c.heads;
-                int64_t incl = work;
+    auto add_up = [&](int r0, const Loads &x) {
+        const int r = r0 + lane;
+        bad |= x.here > x.next || x.next > p.N || x.here < 0 || (r == 0 && x.here != 0);
+        q.cost = q.group_cost = 0;
+        if (r < p.B && !bad) {
+            q = request_of<MODE>(c, p, r, x.next - x.here, x.len, x.held, x.g, false);
+            wrong |= q.cost == 0 && q.n > 0;
+        }
+        work = (int64_t)q.cost * c.heads;
+        if (MODE == kShared)
+            work += (int64_t)q.group_cost * c.heads;
+        int64_t incl = work;
 #pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const int64_t y = __shfl_up_sync(kFull, incl, d);
-                    incl += lane >= d ? y : 0;
-                }
-                at = before + incl - work;
-                before += __shfl_sync(kFull, incl, 31);
-            }
-            if (pass == 1) {
-                const int64_t want = shares->begin(blockIdx.x);
-                const unsigned who = __ballot_sync(kFull, at <= want && want < at + work);
-                if (who) {
-                    const int from = __ffs(who) - 1;
-                    w->r = r0 + from;
-                    w->q.n = __shfl_sync(kFull, q.n, from);
-                    w->q.len = __shfl_sync(kFull, q.len, from);
-                    w->q.cost = __shfl_sync(kFull, q.cost, from);
-                    w->q.rows = w->q.n * p.group;
-                    if (MODE == kShared) {
-                        w->q.tokens = __shfl_sync(kFull, q.tokens, from);
-                        w->q.group_rows = __shfl_sync(kFull, q.group_rows, from);
-                        w->q.group_cost = __shfl_sync(kFull, q.group_cost, from);
-                    }
-                    *base = __shfl_sync(kFull, at, from);
-                    return true;
-                }
-            }
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t y = __shfl_up_sync(kFull, incl, d);
+            incl += lane >= d ? y : 0;
         }
-        if (pass == 0) {
-            if (__any_sync(kFull, bad)) {
-                if (blockIdx.x == 0 && lane == 0)
-                    cache_error(c.error, SPEC_DEVERR_LAYOUT, -1);
-                return false;
-            }
-            if (blockIdx.x == 0 && __any_sync(kFull, wrong))
-                for (int r = lane; r < p.B; r += 32)
-                    request_of<MODE>(c, p, r, true);
-            shares->template cut<MODE == kWhole ? kMinShare : kMinWeighed>(before, gridDim.x);
-            if (before == 0 || blockIdx.x >= shares->blocks)
-                return false;
-        }
+        at = before + incl - work;
+        before += __shfl_sync(kFull, incl, 31);
+    };
+    Loads ahead = load(0);
+#pragma unroll 1
+    for (int r0 = 0; r0 < p.B; r0 += 32) {
+        const Loads x = ahead;
+        if (r0 + 32 < p.B)
+            ahead = load(r0 + 32);
+        kept = r0 == 32 * lane ? before : kept;
+        add_up(r0, x);
     }
-    return false;  // cannot be: every place belongs to a request
+    if (__any_sync(kFull, bad)) {
+        if (blockIdx.x == 0 && lane == 0)
+            cache_error(c.error, SPEC_DEVERR_LAYOUT, -1);
+        return false;
+    }
+    if (blockIdx.x == 0 && __any_sync(kFull, wrong))
+        for (int r = lane; r < p.B; r += 32)
+            request_of<MODE>(c, p, r, true);
+    shares->template cut<MODE == kWhole ? kMinShare : kMinWeighed>(before, gridDim.x);
+    if (before == 0 || blockIdx.x >= shares->blocks)
+        return false;
+    const int64_t want = shares->begin(blockIdx.x);
+    int r0 = 0;
+    if (p.B > 32) {
+        const int turn = __popc(__ballot_sync(kFull, 32 * lane < p.B && kept <= want)) - 1;
+        r0 = 32 * turn;
+        before = __shfl_sync(kFull, kept, turn);
+        add_up(r0, load(r0));
+    }
+#pragma unroll 1
+    while (true) {
+        const unsigned who = __ballot_sync(kFull, at <= want && want < at + work);
+        if (who) {
+            const int from = __ffs(who) - 1;
+            w->r = r0 + from;
+            w->q.n = __shfl_sync(kFull, q.n, from);
+            w->q.len = __shfl_sync(kFull, q.len, from);
+            w->q.cost = __shfl_sync(kFull, q.cost, from);
+            w->q.rows = w->q.n * p.group;
+            if (MODE == kShared) {
+                w->q.tokens = __shfl_sync(kFull, q.tokens, from);
+                w->q.group_rows = __shfl_sync(kFull, q.group_rows, from);
+                w->q.group_cost = __shfl_sync(kFull, q.group_cost, from);
+            }
+            *base = __shfl_sync(kFull, at, from);
+            return true;
+        }
+        r0 += 32;
+        if (r0 >= p.B)
+            return false;  // cannot be: every place belongs to a request
+        add_up(r0, load(r0));
+    }
 }
 
 // The order of a row block's tiles in the ring, as the products use them: K of tile 0, then K of tile t + 1 and V of
@@ -1119,7 +1139,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             x.first = p.cu[w.r];
                             x.q_use = q_use;
                             x.slots = slots;
-                            if (w.t0 == 0 && w.t1 < w.tiles) {  // goes on behind the share: for the join
+                        }
+                        *mine = x;
+                        mbar_arrive(&S.item_full[k % kItems]);
+                        if (more) {  // for the joins
+                            if (w.t0 == 0 && w.t1 < w.tiles) {  // goes on behind the share
                                 Partial &y = p.partial[blockIdx.x];
                                 y.r = w.r;
                                 y.h = w.h;
@@ -1139,8 +1163,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                     p.row_parts[at + p.group] = y;
                             }
                         }
-                        *mine = x;
-                        mbar_arrive(&S.item_full[k % kItems]);
                     }
                     __syncwarp();
                 } else if (!announced(k)) {
@@ -1350,6 +1372,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                 uint32_t see = p.parent ? tree_columns(bits, item.len, col) : low_bits(limit - col);
                                 if (MODE == kWindow)
                                     see &= low_bits(p.sinks - col) | ~low_bits(low - col);
+                                if (__all_sync(kFull, see == ~0u))
+                                    continue;
 #pragma unroll
                                 for (int e = 0; e < 32; ++e)
                                     x[i * 32 + e] = see >> e & 1 ? x[i * 32 + e] : -INFINITY;
