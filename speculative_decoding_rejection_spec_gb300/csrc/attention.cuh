@@ -126,6 +126,7 @@ struct AttentionParams {
     int64_t N;
     const int32_t *cu, *parent;
     float scale_log2;
+    int32_t out_by_32;  // every row of out is whole 32-byte sectors
     // workspace
     Partial *partial;   // [grid]
     float2 *part_ml;    // [grid * 2 * max_rows] M, l (0, -1: a row of a refused request, whose part_o is not written)
@@ -226,6 +227,15 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 __device__ __forceinline__ void mma_commit(uint64_t *bar)
 {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
+}
+
+// 32 bytes of one thread: a whole sector.  The rows of the threads of a warp are apart, and a store costs the memory
+// pipe a cycle per row whatever it brings.
+__device__ __forceinline__ void store32(void *dst, const uint32_t *x)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                 "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
                  : "memory");
 }
 
@@ -1270,7 +1280,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             } else {
                 item.rows = kTile;
                 item.nt = 1 + g;
-                item.len = item.keys = 4 * kTile;
+                item.keys = 4 * kTile;  // (and len 0: with masks)
             }
             const int nt = item.nt;
             if (nt == 0)
@@ -1359,26 +1369,33 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     // 64 columns at a time, read once for the maximum and once for the exponentials: the
                     // code of a tile is fetched anew by every block, and runs at a fetch's pace then
                     // (all 128 in registers, unrolled: 2% faster on prompt chunks, first tile 2 us)
-                    const bool cut = column + kTile > all_see ||
-                                     (MODE == kWindow && column + kTile > p.sinks && column < warp_high);
+                    // Keys that some row of the warp does not see: their scores become -inf where they lie, 32 at a
+                    // time, so that neither look below has to ask.  (Asked in both: twice the work and four times the
+                    // code, which every block fetches anew.)
+                    if (column + kTile > all_see ||
+                        (MODE == kWindow && column + kTile > p.sinks && column < warp_high)) {
+#pragma unroll 1
+                        for (int j = 0; j < kTile / 32; ++j) {
+                            const int col = column + j * 32;
+                            uint32_t see = p.parent ? tree_columns(bits, item.len, col) : low_bits(limit - col);
+                            if (MODE == kWindow)
+                                see &= low_bits(p.sinks - col) | ~low_bits(low - col);
+                            if (__all_sync(kFull, see == ~0u))
+                                continue;
+                            float x[32];
+                            tmem_ld32(s_addr + j * 32, x);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                x[e] = see >> e & 1 ? x[e] : -INFINITY;
+                            tmem_st32(s_addr + j * 32, x);
+                        }
+                        tmem_wait_st();
+                    }
                     auto columns = [&](int j, float *x) {
                         tmem_ld32(s_addr + j * 64, x);
                         tmem_ld32(s_addr + j * 64 + 32, x + 32);
                         tmem_wait_ld();
-                        if (cut) {
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const int col = column + j * 64 + i * 32;
-                                uint32_t see = p.parent ? tree_columns(bits, item.len, col) : low_bits(limit - col);
-                                if (MODE == kWindow)
-                                    see &= low_bits(p.sinks - col) | ~low_bits(low - col);
-                                if (__all_sync(kFull, see == ~0u))
-                                    continue;
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    x[i * 32 + e] = see >> e & 1 ? x[i * 32 + e] : -INFINITY;
-                            }
-                        }
                     };
                     float mx = -INFINITY;
 #pragma unroll 1
@@ -1504,19 +1521,27 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (!kept)
                     return;
                 if (to_out) {
+                    uint32_t y[16];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        if (col + e < c.dim)
-                            *reinterpret_cast<uint4 *>(out + 2 * (col + e)) =
-                                make_uint4(from_float2<DT>(o[e] * by, o[e + 1] * by),
-                                           from_float2<DT>(o[e + 2] * by, o[e + 3] * by),
-                                           from_float2<DT>(o[e + 4] * by, o[e + 5] * by),
-                                           from_float2<DT>(o[e + 6] * by, o[e + 7] * by));
+                    for (int e = 0; e < 16; ++e)
+                        y[e] = from_float2<DT>(o[2 * e] * by, o[2 * e + 1] * by);
+#pragma unroll
+                    for (int e = 0; e < 16; e += 8) {
+                        if (p.out_by_32) {
+                            if (col + 2 * e < c.dim)
+                                store32(out + 2 * col + 4 * e, y + e);
+                        } else {
+#pragma unroll
+                            for (int i = e; i < e + 8; i += 4)
+                                if (col + 2 * i < c.dim)
+                                    *reinterpret_cast<uint4 *>(out + 2 * col + 4 * i) =
+                                        make_uint4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+                        }
+                    }
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<float4 *>(sums + col + e) =
-                            make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    for (int e = 0; e < 32; e += 8)
+                        store32(sums + col + e, reinterpret_cast<const uint32_t *>(o + e));
                 }
             };
             auto store_ml = [&]() {
@@ -2098,6 +2123,7 @@ template <int MODE> spec_status attend(const spec_cache *cache, const AttentionC
     p.cu = a.cu_new;
     p.parent = a.parent;
     p.scale_log2 = a.scale * kLog2e;
+    p.out_by_32 = ptr_aligned(a.out, 32) && p.out_token % 16 == 0 && p.out_head % 16 == 0 && c.dim % 16 == 0;
     char *ws = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(a.workspace) + 255) & ~uintptr_t(255));
     p.partial = reinterpret_cast<Partial *>(ws + plan.partial);
     p.part_ml = reinterpret_cast<float2 *>(ws + plan.ml);
