@@ -300,6 +300,9 @@ def append_rotated(c: PagedCache, layer: int, q, k_new, v_new, cu_new, rotation,
     were in it.  ``q`` may be None.  A result made for a call on another ``stream`` is memory of that stream, kept for
     the current one.
     """
+    if torch._C._cuda_getDevice() != c.index:
+        with torch.cuda.device(c.index):
+            return append_rotated(c, layer, q, k_new, v_new, cu_new, rotation, parent, interleaved, out, stream)
     if stream is not None:
         return _on_stream(c, stream, out is None and q is not None, append_rotated, c, layer, q, k_new, v_new, cu_new,
                           rotation, parent, interleaved, out)
@@ -309,7 +312,8 @@ def append_rotated(c: PagedCache, layer: int, q, k_new, v_new, cu_new, rotation,
     N = k_new.shape[0]
     if v_new.shape[0] != N or (q is not None and q.shape[0] != N):
         raise ValueError("q, k_new and v_new must have the same rows")
-    if rotation.dtype is not torch.float32 or rotation.dim() != 2 or (rotation.stride(1) != 1 and rotation.numel()):
+    shape, stride = rotation.shape, rotation.stride()
+    if rotation.dtype is not torch.float32 or len(shape) != 2 or (stride[1] != 1 and rotation.numel()):
         raise TypeError("rotation must be a float32 tensor [positions, dim] with unit stride inside")
     if rotation.device != c.device:
         raise ValueError(f"rotation must be on {c.device}")
@@ -320,8 +324,7 @@ def append_rotated(c: PagedCache, layer: int, q, k_new, v_new, cu_new, rotation,
         qt, qh = _rows(c, q, None, "q")
         H = q.shape[1]
         if out is None:
-            with torch.cuda.device(c.index):
-                out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
             ot, oh = H * c.dim, c.dim
         elif out.shape != q.shape:
             raise ValueError("out must have the shape of q")
@@ -329,8 +332,7 @@ def append_rotated(c: PagedCache, layer: int, q, k_new, v_new, cu_new, rotation,
             ot, oh = _rows(c, out, H, "out")
     elif out is not None:
         raise ValueError("out needs q")
-    turn = Rotation(table=rotation.data_ptr(), row_stride=rotation.stride(0), positions=rotation.shape[0],
-                    dim=rotation.shape[1], neighbours=int(interleaved))
+    turn = Rotation(rotation.data_ptr(), stride[0], shape[0], shape[1], 1 if interleaved else 0)
     _call(c, "spec_cache_append_rotated", None, layer, k_new.data_ptr(), kt, kh, v_new.data_ptr(), vt, vh, _ptr(q),
           qt, qh, H, _ptr(out), ot, oh, cu_new.data_ptr(), B, N, _ptr(parent), ctypes.byref(turn))
     return out
@@ -341,13 +343,17 @@ def share(c: PagedCache, min_tokens: int = 256, B: int | None = None, out=None, 
     their neighbours (spec_cache_share): int32 [B, 4], per request the first of its group, the end, the tokens that the
     group shares, 0.  The plan of ``attention(shared=...)`` for all layers and steps in which the requests keep these
     pages; ordered like the calls that change the cache."""
+    if torch._C._cuda_getDevice() != c.index:
+        with torch.cuda.device(c.index):
+            return share(c, min_tokens, B, out, stream)
     if stream is not None:
         return _on_stream(c, stream, out is None, share, c, min_tokens, B, out)
-    B = int(c.lens.shape[0]) if B is None else int(B)
+    if B is None:
+        B = c.lens.shape[0]
     if out is None:
-        with torch.cuda.device(c.index):
-            out = torch.empty((max(B, 0), 4), dtype=torch.int32, device=c.device)
-    _int32(out, (B, 4), "out", c.device)
+        out = torch.empty((max(B, 0), 4), dtype=torch.int32, device=c.device)
+    else:
+        _int32(out, (B, 4), "out", c.device)
     _call(c, "spec_cache_share", None, B, _clamped(min_tokens), out.data_ptr())
     return out
 

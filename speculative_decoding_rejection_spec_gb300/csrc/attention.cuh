@@ -68,9 +68,11 @@ constexpr int kMaxGrid = 160;       // blocks a call may use (SMs of the device,
 constexpr int kBlockCost = 3;
 constexpr int kMinShare = 2;        // least places of a block's share (2 / 4 / 8: one token 17 / 20 / 23 us)
 // Windows and shared prefixes, whose calls mix row blocks of both kinds and many of few tiles, weigh them in thirds
-// of a narrow tile.  (Measured in the blocks: narrow tile 1.05-1.3 us, wide 1.7-1.8, between two row blocks 3.5 and
-// 5.2 us.)
-constexpr int kNarrowTile = 3, kWideTile = 5, kNarrowBlock = 10, kWideBlock = 14, kMinWeighed = 10;
+// of a narrow tile.  (Measured in the blocks: a narrow tile 1.05-1.3 us, a wide one 1.7-1.8; beginning and ending a
+// row block 2.5-3.2 us of twins, 4.5 of a narrow one and 5.5-7 of a wide one.  Twins as narrow ones: a shared batch in
+// plain decoding 59 us against 57; narrow ones as twins: windows over trees 38.9 us against 36.9.)
+constexpr int kNarrowTile = 3, kWideTile = 5, kTwinBlock = 8, kNarrowBlock = 10, kWideBlock = 14;
+constexpr int kMinWeighed = 7;      // as kMinShare; at least one tile's places in any case (7 / 10: one token 14.6 / 15.9)
 constexpr float kLazy = 8.0f;       // log2 of the growth that moves a row's maximum (4 is no faster)
 // log2 of the largest weight when a row's maximum moves.  fp16: far below the maximum, where a long context
 // may have a good part of its weight, the product with V keeps 2^-21 of it in full and 2^-32 at all (with
@@ -393,11 +395,14 @@ struct Cost {
     }
 };
 
-template <int MODE> __device__ __forceinline__ Cost cost_of(int rows)
+// ... of a block of `rows` of all the rows of a request or group
+template <int MODE> __device__ __forceinline__ Cost cost_of(const AttentionParams &p, int rows, int all)
 {
     if (MODE == kWhole)
         return Cost{kBlockCost, 1};
-    return rows > kTile ? Cost{kWideBlock, kWideTile} : Cost{kNarrowBlock, kNarrowTile};
+    if (rows > kTile)
+        return Cost{kWideBlock, kWideTile};
+    return Cost{all <= kTile && p.heads > p.group ? kTwinBlock : kNarrowBlock, kNarrowTile};
 }
 
 // Of row block b: up to the last row's own key.  What is left out begins and ends with a copy of `box` keys: before
@@ -456,23 +461,23 @@ __device__ __forceinline__ Request request_of(const CacheView &c, const Attentio
         q.tokens = group_tokens(c, p, r, len, g, &q.group_rows);
         if (q.group_rows > 0) {
             const int tiles = block_range<MODE>(p, q, true, 0).tiles(), last = q.group_rows % kBlockRows;
-            q.group_cost = q.group_rows / kBlockRows * cost_of<MODE>(kBlockRows).of(tiles) +
-                           (last > 0 ? cost_of<MODE>(last).of(tiles) : 0);
+            q.group_cost = q.group_rows / kBlockRows * cost_of<MODE>(p, kBlockRows, q.group_rows).of(tiles) +
+                           (last > 0 ? cost_of<MODE>(p, last, q.group_rows).of(tiles) : 0);
         }
     }
     if (n <= 0)
         return q;
     const int64_t blocks = (q.rows + kBlockRows - 1) / kBlockRows;
     if (!holds(c, held, len, n) || (p.parent && n > kMaxTree) ||
-        blocks * cost_of<MODE>(kBlockRows).of(1) + blocks * (((int64_t)len + n) / kTile) * cost_of<MODE>(kBlockRows).tile >
-            (MODE == kWhole ? INT32_MAX : INT32_MAX / 2)) {
+        blocks * (kBlockCost + 1 + ((int64_t)len + n) / kTile) > (MODE == kWhole ? INT32_MAX : INT32_MAX / 16)) {
         if (report)
             cache_error(c.error, p.parent && n > kMaxTree ? SPEC_DEVERR_TREE : SPEC_DEVERR_LENGTH, r);
         return q;
     }
 #pragma unroll 1
     for (int b = 0; b * kBlockRows < q.rows; ++b)
-        q.cost += cost_of<MODE>(min(kBlockRows, q.rows - b * kBlockRows)).of(block_range<MODE>(p, q, false, b).tiles());
+        q.cost += cost_of<MODE>(p, min(kBlockRows, q.rows - b * kBlockRows), q.rows)
+                      .of(block_range<MODE>(p, q, false, b).tiles());
     return q;
 }
 
@@ -511,7 +516,7 @@ template <int MODE> struct Walk {
         for (h = 0; at >= cost; ++h)
             at -= cost;
         for (b = 0;; ++b) {
-            const int all = cost_of<MODE>(rows()).of(block_range<MODE>(p, q, of_group, b).tiles());
+            const int all = cost_of<MODE>(p, rows(), all_rows()).of(block_range<MODE>(p, q, of_group, b).tiles());
             if (at < all)
                 break;
             at -= all;
@@ -523,7 +528,7 @@ template <int MODE> struct Walk {
     {
         range = block_range<MODE>(p, q, of_group, b);
         tiles = range.tiles();
-        const Cost cost = cost_of<MODE>(rows());
+        const Cost cost = cost_of<MODE>(p, rows(), all_rows());
         const int all = cost.of(tiles), to = (int)min((int64_t)all, from + (end - pos));
         t0 = cost.first(from);
         t1 = cost.first(to);

@@ -3,6 +3,10 @@
 //
 // Elements a, b of a head that form a pair become a c - b s and b c + a s, with c and s of the row's position
 // from the caller's table: fp32 throughout, rounded to 16 bits once.
+//
+// What bounds it (GB300): prompt chunks, memory (548 MB: 87.5 us in the kernel, 6.26 TB/s; 107 us before the first
+// rows were asked for ahead of the lookup, and with batches of loads four heads long).  A decoding step's rows, the
+// chain of loads (layout, request, length, page, table: 4.4 us for 160 tokens, of which the launch takes 2).
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -80,20 +84,66 @@ __device__ __forceinline__ int warp_depth(const int32_t *parent, int n, int i, i
     return depth;
 }
 
-// A warp per new token, or several: a lane keeps its unit of every head, and so its sines and cosines.
+// 16 bytes that are read once; they may be written by this kernel (queries turned in place, by the thread that read
+// them).
+__device__ __forceinline__ uint4 ld_once(const void *p)
+{
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p));
+    return r;
+}
+
+// A warp per new token, or several: a lane keeps its unit of every head, and so its sines and cosines.  The first keys,
+// values and queries are asked for before the token's place is looked up.
 template <int DT, bool NEIGHBOURS>
-__global__ void __launch_bounds__(kCopyThreads) rotate_kernel(CacheView c, Rotated in, int64_t layer_offset,
-                                                              const int32_t *cu, int B, int64_t N)
+__global__ void __launch_bounds__(kCopyThreads, 3) rotate_kernel(CacheView c, Rotated in, int64_t layer_offset,
+                                                                 const int32_t *cu, int B, int64_t N)
 {
     const int lane = threadIdx.x & 31;
+    const int64_t job = (int64_t)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5);
+    const int64_t t = job / in.parts;
+    const int part = (int)(job - t * in.parts);
+    // units of a head: first those that turn (8 pairs, of two vectors half apart; neighbours: 4 pairs of one), then
+    // the rest, vector by vector
+    const int per = 32 / in.units, u = lane % in.units, mine = lane / in.units;
+    const int turning = NEIGHBOURS ? in.half / 4 : in.half / 8;
+    const bool turns = u < turning;
+    const int e0 = (turns || NEIGHBOURS ? u : u + turning) * 8, e1 = e0 + in.half;  // e1: the other vector of a pair
+    constexpr int U = 2;  // heads at a time (four: prompts 104 us against 87, for want of registers)
+    const int step = per * in.parts, h0 = part * per + mine;
+    auto load = [&](const char *src, int64_t src_head, int heads, int from, uint4 *x, uint4 *y) {
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int h = from + j * step;
+            if (mine < per && h < heads) {
+                x[j] = ld_once(src + 2 * (h * src_head + e0));
+                if (!NEIGHBOURS && turns)
+                    y[j] = ld_once(src + 2 * (h * src_head + e1));
+            }
+        }
+    };
+    const int vecs = c.dim / 8, v0 = part * 32 + lane, v_step = 32 * in.parts;
+    auto load_v = [&](int from, uint4 *x) {
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int i = from + j * v_step, head = i / vecs;
+            if (i < c.heads * vecs)
+                x[j] = ld_stream(in.v + 2 * (t * in.v_token + head * in.v_head + (i - head * vecs) * 8));
+        }
+    };
+    const char *k_row = in.k + 2 * t * in.k_token, *q_row = in.q + 2 * t * in.q_token;
+    uint4 vx[U], kx[U], ky[U];
+    if (t < N) {  // (rows of padding are read too: they are there)
+        load(k_row, in.k_head, c.heads, h0, kx, ky);
+        load_v(v0, vx);
+    }
     if (!block_layout_ok(cu, B, N)) {
         if (blockIdx.x == 0 && threadIdx.x == 0)
             cache_error(c.error, SPEC_DEVERR_LAYOUT, -1);
         return;
     }
-    const int64_t job = (int64_t)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5);
-    const int64_t t = job / in.parts;
-    const int part = (int)(job - t * in.parts);
     if (t >= cu[B])
         return;
     const int r = warp_find_request(cu, B, t, lane);
@@ -105,6 +155,8 @@ __global__ void __launch_bounds__(kCopyThreads) rotate_kernel(CacheView c, Rotat
             cache_error(c.error, SPEC_DEVERR_LENGTH, r);
         return;
     }
+    const int col = (int)(pos / c.page_size);
+    const int held = c.held[r], page = c.table[r * c.table_stride + col];
     int depth = i;
     if (in.parent) {
         depth = n <= kMaxTree ? warp_depth(in.parent + first, n, i, lane) : -1;
@@ -114,28 +166,6 @@ __global__ void __launch_bounds__(kCopyThreads) rotate_kernel(CacheView c, Rotat
             return;
         }
     }
-    const int col = (int)(pos / c.page_size);
-    const int page = c.table[r * c.table_stride + col];
-    if (col >= c.held[r] || page < 0 || page >= c.num_pages || c.ref[page] != 1) {
-        if (lane == 0)
-            cache_error(c.error, SPEC_DEVERR_PAGE, r);
-        return;
-    }
-    const int64_t at = layer_offset + page * c.page_stride + pos % c.page_size * c.token_stride;
-    const int vecs = c.dim / 8;
-    for (int j = part * 32 + lane; j < c.heads * vecs; j += 32 * in.parts) {
-        const int head = j / vecs, e = (j - head * vecs) * 8;
-        *reinterpret_cast<uint4 *>(c.v + 2 * (at + head * c.head_stride + e)) =
-            ld_stream(in.v + 2 * (t * in.v_token + head * in.v_head + e));
-    }
-    // units of a head: first those that turn (8 pairs, of two vectors half apart; neighbours: 4 pairs of one), then
-    // the rest, vector by vector
-    const int per = 32 / in.units, u = lane % in.units, mine = lane / in.units;
-    if (mine >= per)
-        return;
-    const int turning = NEIGHBOURS ? in.half / 4 : in.half / 8;
-    const bool turns = u < turning;
-    const int e0 = (turns || NEIGHBOURS ? u : u + turning) * 8, e1 = e0 + in.half;  // e1: the other vector of a pair
     constexpr int P = NEIGHBOURS ? 4 : 8;
     float cs[P], sn[P];
     if (turns) {
@@ -148,54 +178,64 @@ __global__ void __launch_bounds__(kCopyThreads) rotate_kernel(CacheView c, Rotat
             sn[j] = y.x, sn[j + 1] = y.y, sn[j + 2] = y.z, sn[j + 3] = y.w;
         }
     }
-    auto turn = [&](const char *src, int64_t src_head, char *dst, int64_t dst_head, int heads) {
-        constexpr int U = 4;
-        const int step = per * in.parts;
-        for (int h0 = part * per + mine; h0 < heads; h0 += U * step) {
-            uint4 x[U], y[U];
+    if (col >= held || page < 0 || page >= c.num_pages || c.ref[page] != 1) {
+        if (lane == 0)
+            cache_error(c.error, SPEC_DEVERR_PAGE, r);
+        return;
+    }
+    const int64_t at = layer_offset + page * c.page_stride + pos % c.page_size * c.token_stride;
+    for (int from = v0; from < c.heads * vecs; from += U * v_step) {
+        if (from != v0)
+            load_v(from, vx);
 #pragma unroll
-            for (int j = 0; j < U; ++j) {
-                const int h = h0 + j * step;
-                if (h < heads) {
-                    x[j] = *reinterpret_cast<const uint4 *>(src + 2 * (h * src_head + e0));
-                    if (!NEIGHBOURS && turns)
-                        y[j] = *reinterpret_cast<const uint4 *>(src + 2 * (h * src_head + e1));
-                }
-            }
+        for (int j = 0; j < U; ++j) {
+            const int i = from + j * v_step, head = i / vecs;
+            if (i < c.heads * vecs)
+                *reinterpret_cast<uint4 *>(c.v + 2 * (at + head * c.head_stride + (i - head * vecs) * 8)) = vx[j];
+        }
+    }
+    if (mine >= per)
+        return;
+    auto turn = [&](char *dst, int64_t dst_head, int heads, int from, const uint4 *x, const uint4 *y) {
 #pragma unroll
-            for (int j = 0; j < U; ++j) {
-                const int h = h0 + j * step;
-                if (h >= heads)
-                    break;
-                if (turns) {
-                    float a[8], b[8];
-                    unpack16<DT>(x[j], a);
-                    if (NEIGHBOURS) {
+        for (int j = 0; j < U; ++j) {
+            const int h = from + j * step;
+            if (h >= heads)
+                break;
+            uint4 z = x[j];
+            if (turns) {
+                float a[8], b[8], d[8];
+                unpack16<DT>(x[j], a);
+                if (NEIGHBOURS) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            b[2 * i] = fmaf(a[2 * i], cs[i % P], -a[2 * i + 1] * sn[i % P]);
-                            b[2 * i + 1] = fmaf(a[2 * i + 1], cs[i % P], a[2 * i] * sn[i % P]);
-                        }
-                        x[j] = pack16<DT>(b);
-                    } else {
-                        unpack16<DT>(y[j], b);
-                        float d[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            d[i] = fmaf(a[i], cs[i % P], -b[i] * sn[i % P]);
-                            b[i] = fmaf(b[i], cs[i % P], a[i] * sn[i % P]);
-                        }
-                        x[j] = pack16<DT>(d);
-                        *reinterpret_cast<uint4 *>(dst + 2 * (h * dst_head + e1)) = pack16<DT>(b);
+                    for (int i = 0; i < 4; ++i) {
+                        d[2 * i] = fmaf(a[2 * i], cs[i % P], -a[2 * i + 1] * sn[i % P]);
+                        d[2 * i + 1] = fmaf(a[2 * i + 1], cs[i % P], a[2 * i] * sn[i % P]);
                     }
+                } else {
+                    unpack16<DT>(y[j], b);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        d[i] = fmaf(a[i], cs[i % P], -b[i] * sn[i % P]);
+                        b[i] = fmaf(b[i], cs[i % P], a[i] * sn[i % P]);
+                    }
+                    *reinterpret_cast<uint4 *>(dst + 2 * (h * dst_head + e1)) = pack16<DT>(b);
                 }
-                *reinterpret_cast<uint4 *>(dst + 2 * (h * dst_head + e0)) = x[j];
+                z = pack16<DT>(d);
             }
+            *reinterpret_cast<uint4 *>(dst + 2 * (h * dst_head + e0)) = z;
         }
     };
-    turn(in.k + 2 * t * in.k_token, in.k_head, c.k + 2 * at, c.head_stride, c.heads);
-    if (in.q_heads > 0)
-        turn(in.q + 2 * t * in.q_token, in.q_head, in.q_out + 2 * t * in.out_token, in.out_head, in.q_heads);
+    for (int from = h0; from < c.heads; from += U * step) {
+        if (from != h0)
+            load(k_row, in.k_head, c.heads, from, kx, ky);
+        turn(c.k + 2 * at, c.head_stride, c.heads, from, kx, ky);
+    }
+    char *out_row = in.q_out + 2 * t * in.out_token;
+    for (int from = h0; from < in.q_heads; from += U * step) {
+        load(q_row, in.q_head, in.q_heads, from, kx, ky);
+        turn(out_row, in.out_head, in.q_heads, from, kx, ky);
+    }
 }
 
 }  // namespace
@@ -258,7 +298,11 @@ spec_status spec_cache_append_rotated(const spec_cache *cache, int32_t layer, co
     in.positions = rotation->positions;
     in.half = rotation->dim / 2;
     in.units = c.dim / 8 - (rotation->neighbours ? 0 : in.half / 8);
+    // a warp per token when they fill the device, else up to 8 that share out its heads (160 tokens: 4.4 us against 7.3
+    // with one; 2752 tokens: 9.8 us with one, 12 with two)
     in.parts = 1;
+    while (in.parts < 8 && N * in.parts < sms * 16)
+        in.parts *= 2;
     const int64_t blocks = (N * in.parts + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
     auto kernel = cache->dtype == SPEC_BF16
                       ? (rotation->neighbours ? rotate_kernel<SPEC_BF16, true> : rotate_kernel<SPEC_BF16, false>)
