@@ -420,34 +420,31 @@ def _on_stream(c, stream, made, function, *args):
     return result
 
 
-def _workspace(c, H, B, N, shared=False):
-    """A workspace for one call on the current stream (of the cache's device, the current one): that of the
-    stream, kept with the cache (its calls run one after the other), for KEPT_WORKSPACES streams; under
+def _workspace(c, H, B, N, shared, handle):
+    """A workspace for one call on the current stream (of the cache's device, the current one; its raw handle): that
+    of the stream, kept with the cache (its calls run one after the other), for KEPT_WORKSPACES streams; under
     capture a new one from the graph's memory, as graphs may run at the same time.  The caller holds the
     cache's lock until it has launched the call."""
-    rows = min(256, N * (H // c.heads))  # its size grows with these
-    handle = torch._C._cuda_getCurrentRawStream(c.index)
-    capturing = torch._C._cuda_isCurrentStreamCapturing()
-    kept = None if capturing else c.workspaces.get(handle)
-    if shared:  # its size grows with N * H, too
-        size = _lib.spec_attention_shared_workspace_size(c.ref, H, B, N)
-        if kept is not None and kept[1].numel() >= size:
-            return kept[1]
-    else:
-        if kept is not None and kept[0] >= rows:
-            return kept[1]
-        size = _lib.spec_attention_workspace_size(c.ref, H, B, N)
+    rows = min(256, N * (H // c.heads))  # its size grows with these, for shared prefixes with all rows as well
+    all_rows = N * H if shared else 0
+    kept = None if torch._C._cuda_isCurrentStreamCapturing() else c.workspaces.get(handle, _none_kept)
+    if kept is not None and kept[0] >= rows and kept[1] >= all_rows:
+        return kept[2]
     if kept is not None:
-        rows, size = max(rows, kept[0]), max(size, kept[1].numel())
+        rows, all_rows = max(rows, kept[0]), max(all_rows, kept[1])
+    size = (_lib.spec_attention_shared_workspace_size if shared else _lib.spec_attention_workspace_size)(c.ref, H, B, N)
+    if size and kept is not None:
+        size = max(size, 0 if kept[2] is None else kept[2].numel())
     workspace = torch.empty(size, dtype=torch.uint8, device=c.device)
-    if size and not capturing:
+    if size and kept is not None:
         c.workspaces.pop(handle, None)
         while len(c.workspaces) >= KEPT_WORKSPACES:  # (memory of its own stream: what runs there goes on)
             del c.workspaces[next(iter(c.workspaces))]
-        c.workspaces[handle] = (rows, workspace)
+        c.workspaces[handle] = (rows, all_rows, workspace)
     return workspace
 
 
+_none_kept = (0, 0, None)  # rows of a softmax group's partial sums, rows in all, the workspace
 _no_lock = contextlib.nullcontext()
 
 
@@ -481,7 +478,7 @@ def attention(c: PagedCache, layer: int, q, cu_new, parent=None, scale=None, out
     if parent is not None:
         _int32(parent, (N,), "parent", c.device)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
         ot, oh = H * c.dim, c.dim
     elif out.shape != q.shape:
         raise ValueError("out must have the shape of q")
@@ -493,20 +490,26 @@ def attention(c: PagedCache, layer: int, q, cu_new, parent=None, scale=None, out
     if workspace is not None and (workspace.dtype is not torch.uint8 or workspace.device != c.device or
                                   not workspace.is_contiguous()):
         raise TypeError(f"workspace must be a contiguous uint8 tensor on {c.device}")
-    name, more = "spec_attention", ()
+    given = (c.dim ** -0.5 if scale is None else scale,)
     if window is not None:
         if shared is not None:
             raise ValueError("attention takes a window or a plan of shared prefixes, not both")
-        name, more = "spec_attention_window", (_clamped(window), _clamped(sinks))
+        function = _lib.spec_attention_window
+        given += (_clamped(window), _clamped(sinks))
     elif sinks:
         raise ValueError("sinks need a window")
     elif shared is not None:
         _int32(shared, (B, 4), "shared", c.device)
-        name, more = "spec_attention_shared", (shared.data_ptr(),)
+        function = _lib.spec_attention_shared
+        given += (shared.data_ptr(),)
+    else:
+        function = _lib.spec_attention
+    handle = torch._C._cuda_getCurrentRawStream(c.index)
     with c.lock if workspace is None else _no_lock:
         if workspace is None:
-            workspace = _workspace(c, H, B, N, shared is not None)
-        _call(c, name, None, layer, q.data_ptr(), qt, qh, H, cu_new.data_ptr(), B, N, _ptr(parent),
-              c.dim ** -0.5 if scale is None else scale, *more, out.data_ptr(), ot, oh, _ptr(lse),
-              workspace.data_ptr(), workspace.numel())
+            workspace = _workspace(c, H, B, N, shared is not None, handle)
+        status = function(c.ref, layer, q.data_ptr(), qt, qh, H, cu_new.data_ptr(), B, N, _ptr(parent), *given,
+                          out.data_ptr(), ot, oh, _ptr(lse), workspace.data_ptr(), workspace.numel(), handle)
+    if status != 0:
+        raise SpecRejectError(status, function.__name__)
     return out
