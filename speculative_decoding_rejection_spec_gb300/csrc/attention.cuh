@@ -143,6 +143,8 @@ struct AttentionParams {
     int2 *row_parts;     // [2][N * heads] of a row block, at its first row: the block it begins in, and the parts
                          // that it was cut into (0: none, the rows' sums are in row_o, or their results in out)
     int32_t *begun;      // [1] whether there is work at all (a malformed cu: none)
+    int4 *requests;      // [B] query rows of a head (0: none, or an error), first row of q, tokens shared, first row of
+                         // q of the group
 };
 
 template <int DT> __device__ __forceinline__ uint32_t from_float2(float a, float b)
@@ -722,11 +724,13 @@ __device__ __forceinline__ bool find_share(const CacheView &c, const AttentionPa
     auto add_up = [&](int r0, const Loads &x) {
         const int r = r0 + lane;
         bad |= x.here > x.next || x.next > p.N || x.here < 0 || (r == 0 && x.here != 0);
-        q.cost = q.group_cost = 0;
+        q.cost = q.group_cost = q.tokens = 0;
         if (r < p.B && !bad) {
             q = request_of<MODE>(c, p, r, x.next - x.here, x.len, x.held, x.g, false);
             wrong |= q.cost == 0 && q.n > 0;
         }
+        if (MODE == kShared && blockIdx.x == 0 && r < p.B)
+            p.requests[r] = make_int4(q.cost > 0 ? q.rows : 0, x.here, q.tokens, q.tokens ? p.cu[x.g.x] : 0);
         work = (int64_t)q.cost * c.heads;
         if (MODE == kShared)
             work += (int64_t)q.group_cost * c.heads;
@@ -1785,46 +1789,48 @@ __global__ void __launch_bounds__(256) join_kernel(CacheView c, AttentionParams 
 }
 
 // Joins what the rows of a call with shared prefixes have from their group's tokens and from their own, each in one
-// piece or in the parts that it was cut into.  Blocks (request, y), a warp per row; bound by latency as join() is.
+// piece or in the parts that it was cut into.  Blocks (request, y), a warp per row, up to kJoinShared of them in turn.
+// Bound by latency, a chain of three loads (the request, its row blocks, their sums).
+constexpr int kJoinShared = 4;
+
 template <int DT, int DP> __global__ void __launch_bounds__(256) join_shared_kernel(CacheView c, AttentionParams p)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int r = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (!*p.begun)
+    const int4 q = p.requests[blockIdx.x];
+    const int begun = *p.begun, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (!begun || q.x == 0)
         return;
-    const Request q = request_of<kShared>(c, p, r, false);
-    if (q.cost == 0)
-        return;
-    const int first = p.cu[r], group_first = q.tokens ? p.cu[p.shared[r].x] : 0;
-    const int rows = q.n * p.heads;
-    constexpr int E = DP / 32;  // elements per lane
+    constexpr int E = DP / 32, U = 4;  // elements per lane, parts on their way before the weights are known
+    const int rows = q.x * c.heads;    // head by head, so that a warp's next row has mostly the same row blocks
+#pragma unroll 1
     for (int i = blockIdx.y * 8 + warp; i < rows; i += gridDim.y * 8) {
-        const int token = i / p.heads, head = i - token * p.heads, kv = by_group(p, head), in_kv = head - kv * p.group;
-        const int64_t at = (int64_t)(first + token) * p.heads + head;
-        // a row's place in the row blocks of the group and of the request, and those blocks' first rows
-        auto parts_of = [&](int from, int64_t side, int *row) {
-            const int m = (first + token - from) * p.group + in_kv, m0 = m & -kBlockRows, t0 = by_group(p, m0);
-            *row = m - m0;
-            return p.row_parts[(side + from + t0) * p.heads + kv * p.group + m0 - t0 * p.group];
+        const int kv = (uint32_t)i / (uint32_t)q.x, m = i - kv * q.x, token = by_group(p, m);
+        const int head = kv * p.group + m - token * p.group;
+        const int64_t t = (int64_t)q.y + token, at = t * p.heads + head;
+        // a row's place in the row blocks of the group and of the request, and what became of them
+        auto parts_of = [&](int m, int from, int64_t side, int *row) {
+            const int first = m & -kBlockRows, token = by_group(p, first);
+            *row = m - first;
+            return p.row_parts[(side + from + token) * p.heads + kv * p.group + first - token * p.group];
         };
         int row_a = 0, row_b;
-        const int2 b = parts_of(first, p.N, &row_b);
+        const int2 b = parts_of(m, q.y, p.N, &row_b);
         int2 a = make_int2(0, 0);
-        if (q.tokens)
-            a = parts_of(group_first, 0, &row_a);
+        if (q.z)
+            a = parts_of(m + (q.y - q.w) * p.group, q.w, 0, &row_a);
         else if (b.y == 0)
             continue;  // nothing to join: it is in out
-        const int in_a = q.tokens ? max(a.y, 1) : 0, parts = in_a + max(b.y, 1);
-        // where part j's sums are: its place among those of cut row blocks, or below zero the row's
-        auto place = [&](int j) {
-            const bool own = j >= in_a;
+        const int in_a = q.z ? max(a.y, 1) : 0, parts = in_a + max(b.y, 1);
+        // where part k's sums are: its place among those of cut row blocks, or below zero the row's
+        auto place = [&](int k) {
+            const bool own = k >= in_a;
             const int2 x = own ? b : a;
-            const int k = own ? j - in_a : j;
-            return x.y > 0 ? ((int64_t)(x.x + k) * 2 + (k == 0)) * p.max_rows + (own ? row_b : row_a)
+            const int j = own ? k - in_a : k;
+            return x.y > 0 ? ((int64_t)(x.x + j) * 2 + (j == 0)) * p.max_rows + (own ? row_b : row_a)
                            : -1 - (at + (own ? p.N * p.heads : 0));
         };
-        auto load = [&](int j, float *v) {
-            const int64_t x = place(j);
+        auto load = [&](int k, float *v) {
+            const int64_t x = place(k);
             const float *o = (x >= 0 ? p.part_o + x * DP : p.row_o + (-1 - x) * DP) + lane * E;
             if (E == 4) {
                 const float4 y = *reinterpret_cast<const float4 *>(o);
@@ -1837,48 +1843,48 @@ template <int DT, int DP> __global__ void __launch_bounds__(256) join_shared_ker
         float top = -INFINITY, l = 0, acc[4] = {};
         bool refused = false;
 #pragma unroll 1
-        for (int j0 = 0; j0 < parts; j0 += 32) {
-            const int some = min(32, parts - j0);
+        for (int k0 = 0; k0 < parts; k0 += 32) {
+            const int some = min(32, parts - k0);
             float2 ml = make_float2(-INFINITY, 0);
             if (lane < some) {
-                const int64_t x = place(j0 + lane);
+                const int64_t x = place(k0 + lane);
                 ml = x >= 0 ? p.part_ml[x] : p.row_ml[-1 - x];
             }
-            constexpr int U = 4;  // parts on their way before the weights are known
             float v[U][4];
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                load(j0 + min(u, some - 1), v[u]);
+                load(k0 + min(u, some - 1), v[u]);
             refused |= __any_sync(kFull, ml.y < 0);
             const float now = fmaxf(top, warp_max(ml.x)), f = top == -INFINITY ? 0.0f : ex2(top - now);
             top = now;
-            ml.x = ml.x == -INFINITY ? 0.0f : ex2(ml.x - now);
-            l = l * f + warp_sum(ml.x * ml.y);
+            const float w = ml.x == -INFINITY ? 0.0f : ex2(ml.x - now);
+            l = l * f + warp_sum(w * ml.y);
+            if (k0 > 0)
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                acc[e] *= j0 > 0 ? f : 1.0f;
+                for (int e = 0; e < E; ++e)
+                    acc[e] *= f;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const float w = __shfl_sync(kFull, ml.x, u);
+                const float x = __shfl_sync(kFull, w, u);
 #pragma unroll
                 for (int e = 0; e < E; ++e)
                     if (u < some)
-                        acc[e] = fmaf(w, v[u][e], acc[e]);
+                        acc[e] = fmaf(x, v[u][e], acc[e]);
             }
 #pragma unroll 4
-            for (int j = U; j < some; ++j) {
-                load(j0 + j, v[0]);
-                const float w = __shfl_sync(kFull, ml.x, j);
+            for (int k = U; k < some; ++k) {
+                load(k0 + k, v[0]);
+                const float x = __shfl_sync(kFull, w, k);
 #pragma unroll
                 for (int e = 0; e < E; ++e)
-                    acc[e] = fmaf(w, v[0][e], acc[e]);
+                    acc[e] = fmaf(x, v[0][e], acc[e]);
             }
         }
         if (refused)
             continue;  // its parts have sums of -1
         const float by = 1.0f / l;
         if (lane * E < c.dim) {
-            char *out = p.out + 2 * ((first + token) * p.out_token + head * p.out_head + lane * E);
+            char *out = p.out + 2 * (t * p.out_token + head * p.out_head + lane * E);
             const uint32_t low = from_float2<DT>(acc[0] * by, acc[1] * by);
             if (E == 4)
                 *reinterpret_cast<uint2 *>(out) = make_uint2(low, from_float2<DT>(acc[2] * by, acc[3] * by));
@@ -1896,7 +1902,7 @@ template <int DT, int DP> __global__ void __launch_bounds__(256) join_shared_ker
 
 struct AttentionPlan {
     int dp, max_rows;
-    size_t partial, ml, o, begun, row_parts, row_ml, row_o, total;
+    size_t partial, ml, o, begun, requests, row_parts, row_ml, row_o, total;
 };
 
 AttentionPlan attention_plan(const CacheView &c, int32_t num_q_heads, int64_t N, bool shared)
@@ -1914,6 +1920,8 @@ AttentionPlan attention_plan(const CacheView &c, int32_t num_q_heads, int64_t N,
     const int64_t rows = shared ? 2 * N * num_q_heads : 0;
     a.begun = o;
     o = align256(o + (shared ? sizeof(int32_t) : 0));
+    a.requests = o;
+    o = align256(o + (shared ? sizeof(int4) * (size_t)c.num_requests : 0));
     a.row_parts = o;
     o = align256(o + sizeof(int2) * rows);
     a.row_ml = o;
@@ -2036,8 +2044,9 @@ cudaError_t launch_attention(const CUtensorMap &kmap, const CUtensorMap &vmap, c
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     if constexpr (MODE == kShared) {
-        const int64_t rows = (p.N * p.heads + p.B - 1) / p.B;  // of a request, on average
-        cfg.gridDim = dim3(p.B, (unsigned)std::min<int64_t>((rows + 7) / 8, 65535));
+        const int64_t all = p.N * p.heads, rows = (all + p.B - 1) / p.B;  // of a request, on average
+        const int64_t turns = std::max<int64_t>(1, std::min<int64_t>(kJoinShared, all / (grid * 40)));  // of a warp
+        cfg.gridDim = dim3(p.B, (unsigned)std::min<int64_t>((rows + 8 * turns - 1) / (8 * turns), 65535));
         return cudaLaunchKernelEx(&cfg, join_shared_kernel<DT, DP>, c, p);
     }
     const int warps = p.max_rows <= 64 ? 4 : 1;  // per row
@@ -2138,6 +2147,7 @@ template <int MODE> spec_status attend(const spec_cache *cache, const AttentionC
     p.sinks = std::min(a.sinks, INT32_MAX / 2);
     p.shared = reinterpret_cast<const int4 *>(a.shared);
     p.begun = reinterpret_cast<int32_t *>(ws + plan.begun);
+    p.requests = reinterpret_cast<int4 *>(ws + plan.requests);
     p.row_parts = reinterpret_cast<int2 *>(ws + plan.row_parts);
     p.row_ml = reinterpret_cast<float2 *>(ws + plan.row_ml);
     p.row_o = reinterpret_cast<float *>(ws + plan.row_o);
