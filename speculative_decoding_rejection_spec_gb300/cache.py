@@ -444,7 +444,7 @@ def _workspace(c, H, B, N, shared, handle):
     return workspace
 
 
-_none_kept = (0, 0, None)  # rows of a softmax group's partial sums, rows in all, the workspace
+_none_kept = (-1, 0, None)  # rows of a softmax group's partial sums, rows in all, the workspace
 _no_lock = contextlib.nullcontext()
 
 
