@@ -104,7 +104,7 @@ struct Shares {
     template <int LEAST> __device__ __forceinline__ void cut(int64_t cost, int most)
     {
         if (cost < INT32_MAX) {  // nearly always: a 64-bit division takes some hundred cycles
-            blocks = max(1, min(most, (int)((uint32_t)cost + LEAST - 1) / LEAST));
+            blocks = max(1, min(most, (int)(((uint32_t)cost + LEAST - 1) / LEAST)));
             each = (uint32_t)cost / (uint32_t)blocks;
         } else {
             blocks = most;
