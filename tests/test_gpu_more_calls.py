@@ -150,3 +150,25 @@ def test_small_weights_of_a_long_prefix_count():
         tol = want * (2 * u + 2 * es + 2 * L * 2.0 ** -23 + 2.0 ** -20) + (L * 2.0 ** -32 if dtype == "f16" else 0)
         assert np.abs(out.double().cpu().numpy() - want).max() <= tol
         assert np.abs(lse.double().cpu().numpy() - np.log1p(p)).max() <= es + L * 2.0 ** -23 + 2.0 ** -20
+
+
+@pytest.mark.parametrize("dim", [64, 80, 128])
+@pytest.mark.parametrize("n,ctx", [([5, 1, 2], [200, 4, 60]), ([150, 40, 3], [100, 0, 500])])
+def test_outputs_between_two_sectors(dim, n, ctx):
+    """Outputs whose rows are 16-byte aligned and no more, whose tokens or heads are an odd number of 16 bytes apart, and
+    what lies between them: written as others are, and not beside."""
+    import torch
+    plain = Case(n, ctx, heads=2, group=3, dim=dim, seed=2)
+    window = Windowed(n, ctx, 90, 5, heads=2, group=3, dim=dim, seed=2)
+    shared = Grouped([(0, 2, 6)], n, ctx, heads=2, group=3, dim=dim, seed=2)
+    N, H, D = plain.q.shape
+    for c in (plain, window, shared):
+        want, want_lse = c.run()
+        c.check(want, want_lse)
+        for token, head, start in ((H * D, D, 8), (H * D + 8, D, 0), (H * (D + 8), D + 8, 0), (H * (D + 8) + 16, D + 8, 8)):
+            memory = torch.full((start + N * token + 64,), 7.0, dtype=c.q.dtype, device="cuda")
+            out = memory[start:].as_strided((N, H, D), (token, head, 1))
+            out, lse = c.run(out=out)
+            assert torch.equal(out, want) and torch.equal(lse, want_lse)
+            out.fill_(7.0)
+            assert (memory == 7).all()
