@@ -338,11 +338,16 @@ def append_rotated(c: PagedCache, layer: int, q, k_new, v_new, cu_new, rotation,
     return out
 
 
-def share(c: PagedCache, min_tokens: int = 256, B: int | None = None, out=None, stream=None):
+def share(c: PagedCache, min_tokens: int = 512, B: int | None = None, out=None, stream=None):
     """Which of the requests 0 .. B-1 (None: all) share the pages of a prefix of ``min_tokens`` tokens or more with
     their neighbours (spec_cache_share): int32 [B, 4], per request the first of its group, the end, the tokens that the
     group shares, 0.  The plan of ``attention(shared=...)`` for all layers and steps in which the requests keep these
-    pages; ordered like the calls that change the cache."""
+    pages; ordered like the calls that change the cache.
+
+    A prefix read once saves its bytes and costs a join of every row.  Single tokens of eight or more requests gain from
+    64 shared tokens on, pairs of requests and steps of nine tokens from about 1000 (64 requests, 8 kv heads of 128, own
+    context 200: 512 tokens under groups of eight 47.6 -> 39.2 us, under pairs 50 -> 53, nine tokens each 52 -> 59; 4096
+    tokens 148 -> 54, 177 -> 110, 157 -> 93)."""
     if torch._C._cuda_getDevice() != c.index:
         with torch.cuda.device(c.index):
             return share(c, min_tokens, B, out, stream)

@@ -412,7 +412,7 @@ def test_plan_calls():
     import torch
     c = Grouped([(0, 3, 11), (3, 5, 40)], [1] * 6, [30, 20, 5, 0, 70, 16], seed=6)
     want = oracle_cache.share_plan(c.table.tolist(), c.ctx, c.c.held.tolist(), 16, 256)[0]
-    assert want[:, 2].tolist() == [0, 0, 0, 640, 640, 0]  # 176 tokens are too few
+    assert want[:, 2].tolist() == [0, 0, 0, 640, 640, 0]  # 176 tokens are too few (as for the default)
     s = torch.cuda.Stream()
     torch.cuda.synchronize()
     first = cache.share(c.c, stream=s)
