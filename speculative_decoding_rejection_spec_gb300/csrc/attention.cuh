@@ -63,6 +63,7 @@
 
 #include "cache.cuh"
 #include "drain.cuh"
+#include "parts.cuh"
 
 namespace specrej {
 namespace {
@@ -135,6 +136,7 @@ struct AttentionParams {
     float *lse;
     int64_t q_token, q_head, out_token, out_head;  // elements
     int32_t heads, group, B;
+    int32_t blocks;    // of the attention kernel
     uint32_t group_mul, group_shift;  // m / group = m * group_mul >> group_shift for 0 <= m < 2^31
     int32_t box;       // tokens per copy of K or V
     int32_t q_tokens;  // tokens of 128 query rows, when the group divides them: Q of wide row blocks then
@@ -1681,7 +1683,7 @@ __device__ __forceinline__ void join(const CacheView &c, const AttentionParams &
     // the last are the first over again
     auto place = [&](int i, int j) {
         const int row = row0 + j * next;
-        return ((int64_t)(blockIdx.x + i) * 2 + (i == 0)) * p.max_rows + (row < x.rows ? row : row0);
+        return part_place(blockIdx.x, i, p.max_rows, row < x.rows ? row : row0);
     };
     constexpr int E = DP / 32;  // elements per lane
     auto load = [&](int i, int j, float *v) {
@@ -1834,13 +1836,15 @@ template <int DT, int DP> __global__ void __launch_bounds__(256) join_shared_ker
             a = parts_of(m + (q.y - q.w) * p.group, q.w, 0, &row_a);
         else if (b.y == 0)
             continue;  // nothing to join: it is in out
+        if (!parts_within(a.x, a.y, p.blocks) || !parts_within(b.x, b.y, p.blocks))
+            continue;  // never written: a wait gave up
         const int in_a = q.z ? max(a.y, 1) : 0, parts = in_a + max(b.y, 1);
         // where part k's sums are: its place among those of cut row blocks, or below zero the row's
         auto place = [&](int k) {
             const bool own = k >= in_a;
             const int2 x = own ? b : a;
             const int j = own ? k - in_a : k;
-            return x.y > 0 ? ((int64_t)(x.x + j) * 2 + (j == 0)) * p.max_rows + (own ? row_b : row_a)
+            return x.y > 0 ? part_place(x.x, j, p.max_rows, own ? row_b : row_a)
                            : -1 - (at + (own ? p.N * p.heads : 0));
         };
         auto load = [&](int k, float *v) {
@@ -2039,8 +2043,9 @@ template <int MODE> cudaError_t prepare_kernels(int *sms)
 
 template <int DT, int DP, int MODE>
 cudaError_t launch_attention(const CUtensorMap &kmap, const CUtensorMap &vmap, const CUtensorMap &qmap,
-                             const CacheView &c, const AttentionParams &p, int grid, cudaStream_t st)
+                             const CacheView &c, const AttentionParams &p, cudaStream_t st)
 {
+    const int grid = p.blocks;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -2147,6 +2152,7 @@ template <int MODE> spec_status attend(const spec_cache *cache, const AttentionC
         ++p.group_shift;
     p.group_mul = (uint32_t)((((uint64_t)1 << p.group_shift) + p.group - 1) / p.group);
     p.B = a.B;
+    p.blocks = std::min(sms, kMaxGrid);
     p.N = a.N;
     p.cu = a.cu_new;
     p.parent = a.parent;
@@ -2175,15 +2181,14 @@ template <int MODE> spec_status attend(const spec_cache *cache, const AttentionC
         !encode_pages(&vmap, c, cache->dtype, c.v + 2 * a.layer * c.layer_stride, p.box) ||
         (p.q_tokens && !encode_queries(&qmap, c, cache->dtype, p)))
         return SPEC_ERR_UNSUPPORTED;
-    const int grid = std::min(sms, kMaxGrid);
     cudaStream_t st = static_cast<cudaStream_t>(a.stream);
     cudaError_t e;
     if (cache->dtype == SPEC_BF16)
-        e = plan.dp == 64 ? launch_attention<SPEC_BF16, 64, MODE>(kmap, vmap, qmap, c, p, grid, st)
-                          : launch_attention<SPEC_BF16, 128, MODE>(kmap, vmap, qmap, c, p, grid, st);
+        e = plan.dp == 64 ? launch_attention<SPEC_BF16, 64, MODE>(kmap, vmap, qmap, c, p, st)
+                          : launch_attention<SPEC_BF16, 128, MODE>(kmap, vmap, qmap, c, p, st);
     else
-        e = plan.dp == 64 ? launch_attention<SPEC_F16, 64, MODE>(kmap, vmap, qmap, c, p, grid, st)
-                          : launch_attention<SPEC_F16, 128, MODE>(kmap, vmap, qmap, c, p, grid, st);
+        e = plan.dp == 64 ? launch_attention<SPEC_F16, 64, MODE>(kmap, vmap, qmap, c, p, st)
+                          : launch_attention<SPEC_F16, 128, MODE>(kmap, vmap, qmap, c, p, st);
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
