@@ -64,7 +64,8 @@ extern "C" {
 #define SPEC_DEVERR_CAPACITY 64 /* reserve: the free pages do not suffice */
 #define SPEC_DEVERR_LENGTH 128  /* a negative length; more tokens than max_pages pages (reserve, append)
                                    or the pages held (attention, commit, fork) contain, so also a step
-                                   whose reserve found no room; an accepted count outside [-1, n_r) */
+                                   whose reserve found no room; an accepted count outside [-1, n_r);
+                                   attention: more work than it can number (see there) */
 #define SPEC_DEVERR_FORK 256    /* a fork's source or destination out of range, a destination that
                                    holds pages, is named twice or is also a source */
 
@@ -236,7 +237,9 @@ spec_status spec_cache_release(const spec_cache *cache, const int32_t *keep_lens
  * read, from the pages held (SPEC_DEVERR_LENGTH where those contain fewer); rows behind them are not
  * used whatever they hold.  A key or value that is not finite reaches the rows that see it and no
  * others.  A page id out of range reads as zeros (SPEC_DEVERR_PAGE); the rows of other requests with
- * errors are not written.
+ * errors are not written.  A request whose work for one kv head is past counting is an error too
+ * (SPEC_DEVERR_LENGTH): with R blocks of 256 query rows and K = lens[r] + n_r keys, where
+ * R (4 + K / 128) reaches 2^31.
  */
 size_t spec_attention_workspace_size(const spec_cache *cache, int32_t num_q_heads, int32_t B, int64_t N);
 spec_status spec_attention(const spec_cache *cache, int32_t layer, const void *q, int64_t q_token_stride,
@@ -251,6 +254,8 @@ spec_status spec_attention(const spec_cache *cache, int32_t layer, const void *q
  * a tree at lens[r] + its depth.  Keys that no row of a request sees are not read, nor are their table entries.
  *   window  >= 1;  sinks  >= 0
  * Everything else, the workspace too, is as for spec_attention(): all lens[r] + n_r tokens lie in the pages held.
+ * Work is past counting where R (19 + 5 (K / 128)) reaches 2^31, of the K keys that a block of query rows can see: at
+ * most window + sinks, its own tokens and 256 more.
  */
 spec_status spec_attention_window(const spec_cache *cache, int32_t layer, const void *q, int64_t q_token_stride,
                                   int64_t q_head_stride, int32_t num_q_heads, const int32_t *cu_new, int32_t B,
@@ -279,6 +284,8 @@ spec_status spec_cache_share(const spec_cache *cache, int32_t B, int32_t min_tok
  * its first request: same results, but for the order of sums.  Entries of the plan that the requests do not fit (a
  * group out of range or of one request, fewer committed tokens than it shares, another entry for its first request)
  * count as no group; whether the pages are in fact the same is not looked at.
+ * Work is past counting where R (19 + 5 (K / 128)) reaches 2^31, of the K keys that a request does not share; a group
+ * whose own reaches 2^30 shares nothing.
  *   shared     device int32 [B, 4], 16-byte aligned, as spec_cache_share() writes it
  *   workspace  spec_attention_shared_workspace_size() bytes; contents need no initialisation
  */

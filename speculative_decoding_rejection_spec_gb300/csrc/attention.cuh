@@ -64,6 +64,7 @@
 #include "cache.cuh"
 #include "drain.cuh"
 #include "parts.cuh"
+#include "places.cuh"
 
 namespace specrej {
 namespace {
@@ -485,9 +486,12 @@ __device__ __forceinline__ Request request_of(const CacheView &c, const Attentio
     }
     if (n <= 0)
         return q;
-    const int64_t blocks = (q.rows + kBlockRows - 1) / kBlockRows;
+    int64_t keys = (int64_t)len + n - (MODE == kShared ? q.tokens : 0);  // of a row block, at most
+    if (MODE == kWindow)
+        keys = most_window_keys(keys, p.parent ? n : min(n, by_group(p, kBlockRows) + 2), p.window, p.sinks, p.box);
     if (!holds(c, held, len, n) || (p.parent && n > kMaxTree) ||
-        blocks * (kBlockCost + 1 + ((int64_t)len + n) / kTile) > (MODE == kWhole ? INT32_MAX : INT32_MAX / 16)) {
+        most_places((q.rows + kBlockRows - 1) / kBlockRows, keys, MODE == kWhole ? kBlockCost : kWideBlock,
+                    MODE == kWhole ? 1 : kWideTile, kTile) > INT32_MAX) {
         if (report)
             cache_error(c.error, p.parent && n > kMaxTree ? SPEC_DEVERR_TREE : SPEC_DEVERR_LENGTH, r);
         return q;
