@@ -93,7 +93,8 @@ typedef struct spec_cache {
     int64_t layer_stride, page_stride, token_stride, head_stride;
     int32_t *page_table;   /* [num_requests, max_pages], rows table_stride elements apart: the page
                               of tokens i * page_size .. (i + 1) * page_size - 1 in column i;
-                              columns from held[r] on are not read */
+                              columns from held[r] on are not used (append and fork may read them,
+                              the other calls do not) */
     int64_t table_stride;
     int32_t num_requests, max_pages;
     int32_t *lens;         /* [num_requests] committed tokens */

@@ -125,6 +125,10 @@ __device__ __forceinline__ void cache_error(int32_t *error, int32_t bits, int32_
         atomicMin(&error[1], request);
 }
 
+// A word that is asked for here, not behind the branches between here and its use, where it would be a load more in a
+// chain.
+__device__ __forceinline__ int32_t load_now(const int32_t *p) { return *const_cast<const volatile int32_t *>(p); }
+
 __device__ __forceinline__ int pages_of(int64_t tokens, int page_size)
 {
     return (int)((tokens + page_size - 1) / page_size);

@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(kCopyThreads, 3) rotate_kernel(CacheView c, Ro
         return;
     const int r = warp_find_request(cu, B, t, lane);
     const int first = cu[r], n = cu[r + 1] - first, i = (int)(t - first);
+    const int held = load_now(&c.held[r]);
     const int64_t len = c.lens[r], pos = len + i;
     // the step's positions lie in the table, a tree's among them
     if (len < 0 || len + n > in.positions || pos >= (int64_t)c.max_pages * c.page_size) {
@@ -159,7 +160,7 @@ __global__ void __launch_bounds__(kCopyThreads, 3) rotate_kernel(CacheView c, Ro
         return;
     }
     const int col = (int)(pos / c.page_size);
-    const int held = c.held[r], page = c.table[r * c.table_stride + col];
+    const int page = col < held ? c.table[r * c.table_stride + col] : -1;
     int depth = i;
     if (in.parent) {
         depth = n <= kMaxTree ? warp_depth(in.parent + first, n, i, lane) : -1;
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(kCopyThreads, 3) rotate_kernel(CacheView c, Ro
             sn[j] = y.x, sn[j + 1] = y.y, sn[j + 2] = y.z, sn[j + 3] = y.w;
         }
     }
-    if (col >= held || page < 0 || page >= c.num_pages || c.ref[page] != 1) {
+    if (page < 0 || page >= c.num_pages || c.ref[page] != 1) {
         if (lane == 0)
             cache_error(c.error, SPEC_DEVERR_PAGE, r);
         return;

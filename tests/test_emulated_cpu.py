@@ -1,6 +1,6 @@
 """The cache's kernels compiled for the host (tests/emulated: a block's threads are host threads) on memory that ends
-where they may read no further: rows of padding and table columns behind the pages held are not read, rows land where
-they belong."""
+where they may read no further: rows of padding are not read, by rotated append no table columns behind the pages held,
+and rows land where they belong."""
 import json
 import os
 import re
@@ -44,3 +44,9 @@ def test_rows_of_padding_are_not_read(library, entry):
     run(library, entry, n=[3, 5, 1], ctx=[10, 30, 0], held=[1, 3, 1], pad=60)
     if entry == "rotated":
         run(library, entry, n=[3, 5, 1], ctx=[10, 30, 0], held=[1, 3, 1], pad=60, interleaved=True, turn=32, tree=True)
+
+
+def test_table_columns_behind_the_pages_held_are_not_read(library):
+    """The last request's new tokens lie behind its pages, the first ones or all: those rows are skipped."""
+    run(library, "rotated", n=[3, 5, 4], ctx=[10, 30, 30], held=[1, 3, 2], error=[32, 2])
+    run(library, "rotated", n=[3, 5, 4], ctx=[10, 30, 32], held=[1, 3, 2], error=[32, 2])
