@@ -430,8 +430,8 @@ def _workspace(c, H, B, N, shared, handle):
     of the stream, kept with the cache (its calls run one after the other), for KEPT_WORKSPACES streams; under
     capture a new one from the graph's memory, as graphs may run at the same time.  The caller holds the
     cache's lock until it has launched the call."""
-    rows = min(256, N * (H // c.heads))  # its size grows with these, for shared prefixes with all rows as well
-    all_rows = N * H if shared else 0
+    rows = min(256, N * (H // c.heads))  # its size grows with these, for shared prefixes with all rows as well: their
+    all_rows = N * H if shared else -1   # layout has more parts even where there are none
     kept = None if torch._C._cuda_isCurrentStreamCapturing() else c.workspaces.get(handle, _none_kept)
     if kept is not None and kept[0] >= rows and kept[1] >= all_rows:
         return kept[2]
@@ -449,7 +449,7 @@ def _workspace(c, H, B, N, shared, handle):
     return workspace
 
 
-_none_kept = (-1, 0, None)  # rows of a softmax group's partial sums, rows in all, the workspace
+_none_kept = (-1, -1, None)  # rows of a softmax group's partial sums, rows in all, the workspace
 _no_lock = contextlib.nullcontext()
 
 
