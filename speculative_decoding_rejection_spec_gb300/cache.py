@@ -178,7 +178,8 @@ def _int32(t, shape, name, device, contiguous=True):
 
 
 def _clamped(x):
-    """An integer as the library takes it: what lies outside of int32 is as good as its ends, or refused as -1 is."""
+    """An integer as the library takes it (ctypes would keep its low 32 bits): what lies outside of int32 is as good as
+    its ends, or refused as they are."""
     return max(-1, min(x, 2 ** 31 - 1))
 
 
@@ -274,7 +275,7 @@ def append(c: PagedCache, layer: int, k_new, v_new, cu_new, stream=None):
     N = k_new.shape[0]
     if v_new.shape[0] != N:
         raise ValueError("k_new and v_new must have the same rows")
-    _call(c, "spec_cache_append", stream, layer, k_new.data_ptr(), kt, kh, v_new.data_ptr(), vt, vh,
+    _call(c, "spec_cache_append", stream, _clamped(layer), k_new.data_ptr(), kt, kh, v_new.data_ptr(), vt, vh,
           cu_new.data_ptr(), B, N)
 
 
@@ -332,9 +333,9 @@ def append_rotated(c: PagedCache, layer: int, q, k_new, v_new, cu_new, rotation,
             ot, oh = _rows(c, out, H, "out")
     elif out is not None:
         raise ValueError("out needs q")
-    turn = Rotation(rotation.data_ptr(), stride[0], shape[0], shape[1], 1 if interleaved else 0)
-    _call(c, "spec_cache_append_rotated", None, layer, k_new.data_ptr(), kt, kh, v_new.data_ptr(), vt, vh, _ptr(q),
-          qt, qh, H, _ptr(out), ot, oh, cu_new.data_ptr(), B, N, _ptr(parent), ctypes.byref(turn))
+    turn = Rotation(rotation.data_ptr(), stride[0], _clamped(shape[0]), _clamped(shape[1]), 1 if interleaved else 0)
+    _call(c, "spec_cache_append_rotated", None, _clamped(layer), k_new.data_ptr(), kt, kh, v_new.data_ptr(), vt, vh,
+          _ptr(q), qt, qh, H, _ptr(out), ot, oh, cu_new.data_ptr(), B, N, _ptr(parent), ctypes.byref(turn))
     return out
 
 
@@ -355,11 +356,11 @@ def share(c: PagedCache, min_tokens: int = 512, B: int | None = None, out=None, 
         return _on_stream(c, stream, out is None, share, c, min_tokens, B, out)
     if B is None:
         B = c.lens.shape[0]
-    if out is None:
-        out = torch.empty((max(B, 0), 4), dtype=torch.int32, device=c.device)
+    if out is None:  # (of more requests than there are, the library refuses it)
+        out = torch.empty((max(min(B, c.lens.shape[0]), 0), 4), dtype=torch.int32, device=c.device)
     else:
         _int32(out, (B, 4), "out", c.device)
-    _call(c, "spec_cache_share", None, B, _clamped(min_tokens), out.data_ptr())
+    _call(c, "spec_cache_share", None, _clamped(B), _clamped(min_tokens), out.data_ptr())
     return out
 
 
@@ -400,7 +401,7 @@ def release(c: PagedCache, keep_lens=None, stream=None):
 
 
 def attention_workspace_size(c: PagedCache, num_q_heads: int, B: int, N: int) -> int:
-    n = load().spec_attention_workspace_size(c.ref, int(num_q_heads), int(B), int(N))
+    n = load().spec_attention_workspace_size(c.ref, _clamped(int(num_q_heads)), _clamped(int(B)), int(N))
     if n == 0:
         raise ValueError("invalid or unsupported sizes for spec_attention_workspace_size")
     return int(n)
@@ -513,7 +514,7 @@ def attention(c: PagedCache, layer: int, q, cu_new, parent=None, scale=None, out
     with c.lock if workspace is None else _no_lock:
         if workspace is None:
             workspace = _workspace(c, H, B, N, shared is not None, handle)
-        status = function(c.ref, layer, q.data_ptr(), qt, qh, H, cu_new.data_ptr(), B, N, _ptr(parent), *given,
+        status = function(c.ref, _clamped(layer), q.data_ptr(), qt, qh, H, cu_new.data_ptr(), B, N, _ptr(parent), *given,
                           out.data_ptr(), ot, oh, _ptr(lse), workspace.data_ptr(), workspace.numel(), handle)
     if status != 0:
         raise SpecRejectError(status, function.__name__)
