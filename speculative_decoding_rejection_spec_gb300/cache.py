@@ -400,10 +400,14 @@ def release(c: PagedCache, keep_lens=None, stream=None):
     _call(c, "spec_cache_release", stream, _ptr(keep_lens), B)
 
 
-def attention_workspace_size(c: PagedCache, num_q_heads: int, B: int, N: int) -> int:
-    n = load().spec_attention_workspace_size(c.ref, _clamped(int(num_q_heads)), _clamped(int(B)), int(N))
+def attention_workspace_size(c: PagedCache, num_q_heads: int, B: int, N: int, shared: bool = False) -> int:
+    """Bytes of a ``workspace`` for calls of ``attention`` on N rows, of those with ``shared`` or of the others.  (Shared
+    ones keep two sums per row and query head: 2 (4 dim + 16) bytes with dim 64 or 128, 553 MB of 16384 tokens with 32
+    heads of 128; the others 42 MB at most.)"""
+    name = "spec_attention_shared_workspace_size" if shared else "spec_attention_workspace_size"
+    n = getattr(load(), name)(c.ref, _clamped(int(num_q_heads)), _clamped(int(B)), int(N))
     if n == 0:
-        raise ValueError("invalid or unsupported sizes for spec_attention_workspace_size")
+        raise ValueError(f"invalid or unsupported sizes for {name}")
     return int(n)
 
 
@@ -462,8 +466,8 @@ def attention(c: PagedCache, layer: int, q, cu_new, parent=None, scale=None, out
     ``parent`` (int32 [N]) makes the new tokens draft trees, otherwise they are chains; ``scale``
     defaults to head_dim ** -0.5; ``out`` may be given (one made for a call on another ``stream`` is
     memory of that stream, kept for the current one); ``lse`` (float32 [N, q_heads], given) receives
-    the log of each row's softmax sum; ``workspace`` (uint8) may be given, calls that can run at the
-    same time and calls of several host threads need one each (without one, the cache keeps one per
+    the log of each row's softmax sum; ``workspace`` (uint8, ``attention_workspace_size``) may be given, calls that
+    can run at the same time and calls of several host threads need one each (without one, the cache keeps one per
     stream, for KEPT_WORKSPACES streams, and a captured graph has its own).  Rows behind
     ``cu_new[B]`` are left as they were in ``out``.
 
