@@ -50,3 +50,11 @@ def test_table_columns_behind_the_pages_held_are_not_read(library):
     """The last request's new tokens lie behind its pages, the first ones or all: those rows are skipped."""
     run(library, "rotated", n=[3, 5, 4], ctx=[10, 30, 30], held=[1, 3, 2], error=[32, 2])
     run(library, "rotated", n=[3, 5, 4], ctx=[10, 30, 32], held=[1, 3, 2], error=[32, 2])
+
+
+def test_every_pass_of_a_warp_over_its_heads(library):
+    """One, two and eight warps a token (two multiprocessors are made believe) and more heads than a pass takes."""
+    for n, heads in (([20, 3, 30], 20), ([9, 0, 10], 40), ([1, 1, 1], 130)):
+        run(library, "rotated", n=n, ctx=[10, 30, 0], held=[2, 3, 2], heads=heads, group=1, pad=2)
+    run(library, "rotated", n=[20, 3, 30], ctx=[10, 30, 0], held=[2, 3, 2], heads=20, group=1, dim=40, turn=24, tree=True,
+        interleaved=True)
