@@ -2071,12 +2071,13 @@ cudaError_t launch_attention(const CUtensorMap &kmap, const CUtensorMap &vmap, c
         const int64_t turns = std::max<int64_t>(1, std::min<int64_t>(kJoinShared, all / (grid * 40)));  // of a warp
         cfg.gridDim = dim3(p.B, (unsigned)std::min<int64_t>((rows + 8 * turns - 1) / (8 * turns), 65535));
         return cudaLaunchKernelEx(&cfg, join_shared_kernel<DT, DP>, c, p);
+    } else {
+        const int warps = p.max_rows <= 64 ? 4 : 1;  // per row
+        const int rows = warps == 4 ? 2 : 8 * kJoinRows;  // per block
+        cfg.gridDim = dim3(grid, (p.max_rows + rows - 1) / rows);
+        return warps == 4 ? cudaLaunchKernelEx(&cfg, join_kernel<DT, DP, 4>, c, p)
+                          : cudaLaunchKernelEx(&cfg, join_kernel<DT, DP, 1>, c, p);
     }
-    const int warps = p.max_rows <= 64 ? 4 : 1;  // per row
-    const int rows = warps == 4 ? 2 : 8 * kJoinRows;  // per block
-    cfg.gridDim = dim3(grid, (p.max_rows + rows - 1) / rows);
-    return warps == 4 ? cudaLaunchKernelEx(&cfg, join_kernel<DT, DP, 4>, c, p)
-                      : cudaLaunchKernelEx(&cfg, join_kernel<DT, DP, 1>, c, p);
 }
 
 spec_status check_attention(const spec_cache *cache, CacheView *c, int32_t num_q_heads, int32_t B, int64_t N)
