@@ -27,7 +27,8 @@
  * lens[r] .. lens[r] + n_r - 1.  Row cu_new[r] + i of a step's arrays belongs to new token i of
  * request r: k_r drafts are k_r + 1 new tokens, the target rows of spec_reject_sample, the nodes
  * of spec_tree_verify_greedy.  cu_new[0] = 0, and cu_new[B] may be below the arrays' N rows: rows
- * from cu_new[B] on are padding and are neither read nor written.
+ * from cu_new[B] on are padding and are neither used nor written (attention may read queries there, the
+ * appends read nothing).
  *
  * Conventions beyond those of spec_reject.h (ownership, asynchrony, host-visible errors, pending
  * CUDA errors):
@@ -288,7 +289,9 @@ spec_status spec_cache_share(const spec_cache *cache, int32_t B, int32_t min_tok
  * Work is past counting where R (19 + 5 (K / 128)) reaches 2^31, of the K keys that a request does not share; a group
  * whose own reaches 2^30 shares nothing.
  *   shared     device int32 [B, 4], 16-byte aligned, as spec_cache_share() writes it
- *   workspace  spec_attention_shared_workspace_size() bytes; contents need no initialisation
+ *   workspace  spec_attention_shared_workspace_size() bytes; contents need no initialisation (two sums of every row
+ *              and query head beside spec_attention()'s: 553 MB for 16384 rows of 32 heads of 128)
+ * After a wait that gave up (SPEC_DEVERR_TIMEOUT) the results count for nothing, as those of the other calls do.
  */
 size_t spec_attention_shared_workspace_size(const spec_cache *cache, int32_t num_q_heads, int32_t B, int64_t N);
 spec_status spec_attention_shared(const spec_cache *cache, int32_t layer, const void *q, int64_t q_token_stride,

@@ -41,7 +41,7 @@
 // In both, two heads of a request of at most 128 rows are taken together where both lie whole in a share ("twins"):
 // a group each, over every tile of its head, nothing to merge.
 //
-// What bounds it (GB300; measured rates 6779 GB/s, 1948.5 TFLOP/s): decoding and verifying long
+// What bounds it (GB300; measured rates 6792 GB/s, 1923.6 TFLOP/s): decoding and verifying long
 // contexts, HBM (64 requests of 1 to 8191 keys, 1.03 GB: 168 us, 6.1 TB/s, nothing read twice); short
 // ones, the start of a block (the search for its share, the tables, the code itself, which comes from memory: the
 // first scores are there after 6 us of one request, 11 of 64) and the join; prompt chunks, the chain of a group:
@@ -512,7 +512,8 @@ __device__ __forceinline__ Request request_of(const CacheView &c, const Attentio
 
 // Walks a block's share, one (request or group, head, row block) at a time; a whole warp.  A row block takes
 // some places of the list before those of its tiles; a share that ends within them leaves the row block to the next.
-// (Every share but a call's last is longer than a tile's places: a row block that is cut has a part in each block from
+// (A share has at least a tile's places, with kMinWeighed at least the 5 of a wide one from lists of 11 places on, the
+// shortest there are; so it has the first place of some tile, and a row block that is cut has a part in each block from
 // its first to its last.)
 template <int MODE> struct Walk {
     Request q;
@@ -1809,8 +1810,11 @@ __global__ void __launch_bounds__(256) join_kernel(CacheView c, AttentionParams 
 }
 
 // Joins what the rows of a call with shared prefixes have from their group's tokens and from their own, each in one
-// piece or in the parts that it was cut into.  Blocks (request, y), a warp per row, up to kJoinShared of them in turn.
-// Bound by latency, a chain of three loads (the request, its row blocks, their sums).
+// piece or in the parts that it was cut into.  Blocks (request, y), a warp per row, of requests of about as many rows up
+// to kJoinShared of them in turn.  Bound by latency, a chain of three loads (the request, its row blocks, their sums).
+// The blocks per request are those of an average one's rows, so a step in which one request has most of the rows keeps
+// few warps busy: 127 requests of one token and one of 2048, 32/8 heads of 128, behind 2048 shared tokens 882 us, without
+// sharing 340; where no request is in a group, 490 and 345.
 constexpr int kJoinShared = 4;  // (2 / 4 / 8: a verify step of 1152 tokens 235 / 234.5 / 238 us in all)
 
 template <int DT, int DP> __global__ void __launch_bounds__(256) join_shared_kernel(CacheView c, AttentionParams p)

@@ -4,7 +4,7 @@
 // Elements a, b of a head that form a pair become a c - b s and b c + a s, with c and s of the row's position
 // from the caller's table: fp32 throughout, rounded to 16 bits once.
 //
-// What bounds it (GB300): prompt chunks, memory (548 MB: 87.5 us in the kernel, 6.26 TB/s; 107 us before the first
+// What bounds it (GB300): prompt chunks, memory (548 MB: 89.7 us in the kernel, 6.1 TB/s; 107 us before the first
 // rows were asked for ahead of the lookup, and with batches of loads four heads long).  A decoding step's rows, the
 // chain of loads (rows in all, layout, request, length, page, table: 4.3 us for 160 tokens, of which the launch takes
 // 2).  Without the first of these, the number of rows that are not padding, 4.1 us, and prompt chunks from Python 90.7
@@ -302,8 +302,10 @@ spec_status spec_cache_append_rotated(const spec_cache *cache, int32_t layer, co
     in.positions = rotation->positions;
     in.half = rotation->dim / 2;
     in.units = c.dim / 8 - (rotation->neighbours ? 0 : in.half / 8);
-    // a warp per token when they fill the device, else up to 8 that share out its heads (160 tokens: 4.4 us against 7.3
-    // with one; 2752 tokens: 9.8 us with one, 12 with two)
+    // a warp per token when they fill the device, else up to 8 that share out its heads (32/8 heads of 128, us with 1 / 2
+    // / 4 / 8: 160 tokens 6.9 / 5.2 / 4.6 / 4.4; 900 tokens 7.5 / 6.3 / 5.9 / 8.5; 1800 tokens 9.1 / 7.7 / 10.0 / 15.1;
+    // 2752 tokens 11.9 / 13.0 / 15.7 / 23.4.  Towards the upper end of each range the rule is late: 600 tokens 7.8 with
+    // its 8 and 5.3 with 4, 1200 tokens 8.7 with its 4 and 6.5 with 2.)
     in.parts = 1;
     while (in.parts < 8 && N * in.parts < sms * 16)
         in.parts *= 2;
