@@ -1480,6 +1480,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             a = ex2(a);
                             b = ex2(b);
                             sum[e / 2 & 3] = add2(sum[e / 2 & 3], pack2(a, b));
+                            // 16 bits, as the product with V takes them (the sum above does not lose them): errors
+                            // against 64 bits of 0.0023 in bf16, where outputs alone rounded have 0.0017, and of
+                            // 0.00027 beside 0.00021 in fp16
                             x[e / 2] = __uint_as_float(from_float2<DT>(a, b));
                         }
                         tmem_st32(s_addr + j * 32, x);
